@@ -354,6 +354,210 @@ STT_API int stt_verify(const float* p_target, const float* p_draft, const int32_
                        int32_t* n_accepted, int32_t* out_tokens, void* stream);
 
 /* --------------------------------------------------------------------------
+ * Query/key norm and position rotation.  The fused QKV projection gives each
+ * token one row of H query heads, H_kv key heads and H_kv value heads of D
+ * elements each.  For every query and key head x of a token at position t:
+ *     x^  = x * (mean(x^2) + eps)^(-1/2),   n = x^ * w     (n = x if w is NULL)
+ *     y_a = amplitude * (n_a cos(t f_i) - n_b sin(t f_i)),
+ *     y_b = amplitude * (n_b cos(t f_i) + n_a sin(t f_i))
+ * for the pairs i = 0..R/2-1 of the head's first R elements: (a, b) =
+ * (i, i + R/2), or (2i, 2i + 1) with STT_ROPE_INTERLEAVED; elements R..D-1 are
+ * y = n.  Values pass through.  Sums are fp32, y is rounded once.
+ *
+ * The frequencies are the caller's, so any scaling for long contexts is a
+ * matter of the array.  Angles are exact for far positions: t f_i is reduced
+ * modulo a full turn in 64-bit fixed point before its sine is taken.
+ *
+ *  freq     fp64 [R/2] (device): radians per position, finite; NULL iff R = 0.
+ *  R        rotated elements of a head: a multiple of 16, 0 <= R <= D
+ *           (0: norms only; STT_ERR_UNSUPPORTED for other values).
+ *  flags    STT_ROPE_INTERLEAVED or 0.
+ *  amplitude  finite; multiplies the rotated elements (1 in the usual case).
+ *  w_q, w_k bf16 [D] (device) or NULL, each 16-byte aligned.
+ *  eps      finite and > 0 where a weight is given.
+ * ------------------------------------------------------------------------ */
+#define STT_ROPE_INTERLEAVED 0x1u
+typedef struct {
+  const double* freq;
+  const void* w_q;
+  const void* w_k;
+  int R;
+  uint32_t flags;
+  float amplitude;
+  float eps;
+} stt_rope;
+
+/* --------------------------------------------------------------------------
+ * Training form: projection rows to the attention's layout.
+ *
+ *  qkv      bf16, row b S + s at qkv + (b S + s) ld: heads in the order q, k, v.
+ *  ld       elements between rows, >= (H + 2 H_kv) D, a multiple of 8.
+ *  positions int32 [B, S] (device), any values, or NULL for 0..S-1.
+ *  B, S >= 0; H, H_kv >= 1 (H need not be a multiple of H_kv here); D 64 or 128.
+ *  q        bf16 [B, H, S, D];  k, v  bf16 [B, H_kv, S, D].
+ * Device pointers 16-byte aligned (positions 4, freq 8).
+ * ------------------------------------------------------------------------ */
+STT_API int stt_qkv_rope_fwd(const void* qkv, int64_t ld, const int32_t* positions, int B, int S,
+                             int H, int H_kv, int D, const stt_rope* rope, void* q, void* k,
+                             void* v, void* stream);
+
+/* Bytes of device workspace stt_qkv_rope_bwd needs (>= 16). */
+STT_API size_t stt_qkv_rope_bwd_workspace_size(int D);
+
+/* --------------------------------------------------------------------------
+ * Its gradient.  With u the transposed rotation of dL/dy:
+ *     dL/dw = sum over tokens and heads of u x^,
+ *     dL/dx = r (u w - x^ mean(u w x^)),  r = (mean(x^2) + eps)^(-1/2)
+ * (dL/dx = u without a weight).
+ *
+ *  dq, dk, dv  gradients of q, k, v in their layout, fp32 as stt_attn_bwd writes
+ *           them, or bf16 with STT_ROPE_BF16_GRADS.
+ *  qkv, ld  as forward; qkv may be NULL when neither weight is given.
+ *  dqkv     bf16, rows ld_d elements apart (as ld), OVERWRITTEN: the operand
+ *           of the projection's own gradient products, rounded once.
+ *  dw_q, dw_k  fp32 [D], OVERWRITTEN; NULL exactly where the weight is NULL.
+ *           Summed in an order fixed by the sizes and the device.
+ *  workspace at least stt_qkv_rope_bwd_workspace_size(D) bytes, 16-byte aligned
+ *           (NULL allowed when neither weight is given); contents on entry are
+ *           ignored, calls that may overlap need one each.
+ * ------------------------------------------------------------------------ */
+#define STT_ROPE_BF16_GRADS 0x2u
+STT_API int stt_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, const void* qkv,
+                             int64_t ld, const int32_t* positions, int B, int S, int H, int H_kv,
+                             int D, const stt_rope* rope, uint32_t flags, void* dqkv, int64_t ld_d,
+                             float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* --------------------------------------------------------------------------
+ * A paged KV cache and a ragged batch of new tokens on it, shared by
+ * stt_kv_append and stt_paged_attn.  Everything but the sizes is read on the
+ * device, so a captured call follows the batch as it changes.
+ *
+ *  k, v     bf16 caches: key x of page p, head h is the D elements at
+ *           p stride_page + h stride_head + x stride_tok (elements; both caches
+ *           alike).  16-byte aligned, strides multiples of 8.  Any order of the
+ *           page's heads and tokens, and a k/v pair in one allocation, are a
+ *           matter of the strides.
+ *  table    int32 [B, max_pages]: page of keys x page_size.. of each sequence.
+ *           Entries past a sequence's last page are not read.
+ *  cu_q     int32 [B + 1], cu_q[0] = 0, nondecreasing: sequence b's new tokens
+ *           are rows cu_q[b]..cu_q[b+1]-1 of the call's N rows.  A sequence may
+ *           have none.  Rows from cu_q[B] on are left as they are.
+ *  seq_lens int32 [B]: keys of each sequence, its new tokens among them; new
+ *           token i of n is key seq_len - n + i.
+ *  B        0 <= B <= STT_MAX_BATCH.   H_kv >= 1.   D 64 or 128.
+ *  page_size a power of two, 8..1024 (STT_ERR_UNSUPPORTED otherwise).
+ *  num_pages >= 1, max_pages >= 1; max_pages * page_size < 2^31.
+ *
+ * A page outside [0, num_pages), or a key at or past max_pages * page_size or
+ * before 0, is never read or written: it is skipped and reported as
+ * STT_DEVERR_PAGE in the device error word, and the attention of that sequence
+ * is undefined.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* table;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int64_t stride_page, stride_head, stride_tok;
+  int B, H_kv, D, page_size, num_pages, max_pages;
+} stt_pages;
+
+/* --------------------------------------------------------------------------
+ * Serving form of the norm and rotation: new tokens into the cache.
+ *
+ *  qkv      bf16 [N, .], rows ld elements apart, as stt_qkv_rope_fwd.
+ *  positions int32 [N] or NULL: the rotation's position of each row where it is
+ *           not its key index (the depth of a token in a draft tree).
+ *  N        rows, >= 0.
+ *  q        bf16 [N, H, D]: the normed and rotated queries.
+ * Two rows of one call may not have the same key slot.
+ * ------------------------------------------------------------------------ */
+STT_API int stt_kv_append(const void* qkv, int64_t ld, const int32_t* positions, int64_t N, int H,
+                          const stt_pages* pages, const stt_rope* rope, void* q, void* stream);
+
+/* Bytes of device workspace stt_paged_attn needs (>= 16). */
+STT_API size_t stt_paged_attn_workspace_size(int64_t N, int B, int H, int H_kv, int D);
+
+/* --------------------------------------------------------------------------
+ * Attention of the new tokens over their sequences' pages, whose new keys are
+ * already there (stt_kv_append).  New token i of a sequence with n new tokens
+ * and L keys sees keys 0..L-n+i, or, with `tree`, keys 0..L-n-1 and those of the
+ * n new ones whose bit is set in its row.
+ *
+ *  q        bf16, row r at q + r ld_q: H heads of D; ld_q >= H D, a multiple
+ *           of 8.  Query head h reads KV head h / (H / H_kv); H % H_kv == 0,
+ *           H / H_kv <= 16.
+ *  N        rows, >= 0, N H < 2^31.
+ *  scale    finite and > 0.
+ *  tree     uint32 [N, tree_words] or NULL: bit j % 32 of word j / 32 of a row
+ *           is set iff it sees new token j of its sequence (itself only if its
+ *           own bit is set).  New tokens from 32 tree_words on are not seen.
+ *  out      bf16 [N, H, D], rounded to nearest even; zeros for a row that sees
+ *           nothing.  May not overlap q.
+ *  lse      fp32 [N, H] or NULL: natural logarithm of the sum of exponentials
+ *           of the visible scaled scores, -inf for a row that sees nothing.
+ *  workspace at least stt_paged_attn_workspace_size() bytes, 256-byte aligned;
+ *           contents on entry are ignored.  Calls that may overlap (two
+ *           streams, two graphs) need one each.
+ * ------------------------------------------------------------------------ */
+STT_API int stt_paged_attn(const void* q, int64_t ld_q, int64_t N, int H, const stt_pages* pages,
+                           float scale, const uint32_t* tree, int tree_words, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Logits to the distributions stt_verify tests against.  Rows come `rows` to a
+ * sequence: row r is position i = r % rows of sequence b = r / rows.  With c the
+ * number of times token v occurs in the sequence's output so far:
+ *     z <- z > 0 ? z / repetition : z * repetition   if v occurs in its history
+ *     z <- z - frequency * c - presence * [c > 0]
+ *     z <- z + bias,   z <- -inf where the mask forbids v
+ *     out = softmax(z / temperature)
+ * The history of row (b, i) is tokens[cu_tokens[b]..cu_tokens[b+1]), the first
+ * n_prompt[b] of them the prompt and the rest output, and then the draft's
+ * tokens 0..i-1, output too.  Tokens outside [0, V) count for nothing.
+ *
+ *  z        fp32 [N, V], or bf16 with STT_LOGITS_BF16.  A forbidden element may
+ *           hold anything; NaN or +inf elsewhere makes its row's probabilities
+ *           NaN (greedy: NaN is passed over).
+ *  N        rows, >= 0, a multiple of `rows` >= 1.   V  >= 1.
+ *  temperature, repetition, frequency, presence  fp32 [N / rows] or NULL (1, 1,
+ *           0, 0).  temperature = 0 is greedy: the distribution is 1 at the
+ *           largest z (the lowest such v) and 0 elsewhere.  temperature >= 0 and
+ *           repetition > 0 are the caller's to see to.
+ *  tokens, cu_tokens, n_prompt  int32; all NULL without a history (n_prompt
+ *           NULL alone: no prompt).
+ *  draft    int32 [N / rows, draft_ld] or NULL; draft_ld >= rows - 1.
+ *  bias     fp32 [bias_rows, V]; bias_rows 0 (none), 1, or N / rows.
+ *  mask     uint32 [N, ceil(V / 32)] or NULL: bit v % 32 of word v / 32 set iff
+ *           row r allows v.
+ *  out      fp32 [N, V]; may be z itself when that is fp32.  With
+ *           STT_LOGITS_RAW it receives z / temperature instead (z itself where
+ *           temperature is 0).  A row with nothing allowed gets zeros (-inf raw).
+ * V above 16 x 24576 returns STT_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------ */
+#define STT_LOGITS_BF16 0x1u
+#define STT_LOGITS_RAW 0x2u
+typedef struct {
+  const float* temperature;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* tokens;
+  const int32_t* cu_tokens;
+  const int32_t* n_prompt;
+  const int32_t* draft;
+  const float* bias;
+  const uint32_t* mask;
+  int draft_ld;
+  int bias_rows;
+} stt_logits;
+STT_API int stt_logits_process(const void* z, int64_t N, int64_t V, int rows,
+                               const stt_logits* params, uint32_t flags, float* out,
+                               void* stream);
+
+/* --------------------------------------------------------------------------
  * Per-launch timing (measurement support; no counterpart on the pages).
  * stt_profile_start(capacity) makes every subsequent kernel launch of the
  * library (from any thread) record a CUDA event pair around itself on its
@@ -380,6 +584,11 @@ STT_API const char* stt_kernel_name(int kernel_id);
 #define STT_KERNEL_SOFT_CE_VARIANT 7
 #define STT_KERNEL_VERIFY 8
 #define STT_KERNEL_LM_HEAD_CE 9
+#define STT_KERNEL_QKV_ROPE 10
+#define STT_KERNEL_QKV_ROPE_BWD 11
+#define STT_KERNEL_KV_APPEND 12
+#define STT_KERNEL_PAGED_ATTN 13
+#define STT_KERNEL_LOGITS 14
 
 /* Device error-word bits: sites of bounded waits that gave up, and blocks
  * whose dynamic shared memory did not have the 1024-byte alignment the
@@ -389,8 +598,11 @@ STT_API const char* stt_kernel_name(int kernel_id);
 #define STT_DEVERR_CE_WAIT 0x4u
 #define STT_DEVERR_SMEM_ALIGN 0x8u
 #define STT_DEVERR_LM_WAIT 0x10u
-#define STT_DEVERR_WAIT_MASK \
-  (STT_DEVERR_FWD_WAIT | STT_DEVERR_BWD_WAIT | STT_DEVERR_CE_WAIT | STT_DEVERR_LM_WAIT)
+#define STT_DEVERR_PAGE 0x20u /* a page or key slot out of range, skipped */
+#define STT_DEVERR_PAGED_WAIT 0x40u
+#define STT_DEVERR_WAIT_MASK                                                           \
+  (STT_DEVERR_FWD_WAIT | STT_DEVERR_BWD_WAIT | STT_DEVERR_CE_WAIT | STT_DEVERR_LM_WAIT | \
+   STT_DEVERR_PAGED_WAIT)
 
 #ifdef __cplusplus
 }

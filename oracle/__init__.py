@@ -25,6 +25,11 @@ lm_head    the draft's LM head z = h W^T followed by the soft-CE: loss and
            the gradients of h and W.
 verify     speculative-decoding verification by rejection sampling (the
            "FlashSpec" practice page, §3.4 "验证器的具体实现").
+rope       per-head RMS norm and position rotation of queries and keys, and
+           its gradient.
+paged      attention of new tokens over a paged KV cache.
+logits     penalties, bias, grammar mask, temperature and softmax of the
+           target's logits.
 
 Readings of the page where it is silent:
   * kv indexes the concatenation of k+1 blocks, each Q_LEN long; block 0 is
@@ -41,5 +46,6 @@ Readings of the page where it is silent:
 """
 
 from . import mask, attention, soft_ce, lm_head, verify  # noqa: F401
+from . import rope, paged, logits  # noqa: F401
 
-__all__ = ["mask", "attention", "soft_ce", "lm_head", "verify"]
+__all__ = ["mask", "attention", "soft_ce", "lm_head", "verify", "rope", "paged", "logits"]

@@ -43,10 +43,40 @@ EXPORTS = (
     "stt_verify",
     "stt_lm_head_ce_workspace_size",
     "stt_lm_head_ce",
+    "stt_qkv_rope_fwd",
+    "stt_qkv_rope_bwd_workspace_size",
+    "stt_qkv_rope_bwd",
+    "stt_kv_append",
+    "stt_paged_attn_workspace_size",
+    "stt_paged_attn",
+    "stt_logits_process",
     "stt_profile_start",
     "stt_profile_stop",
     "stt_kernel_name",
 )
+
+
+
+class Rope(ctypes.Structure):
+    """stt_rope."""
+    _fields_ = [("freq", ctypes.c_void_p), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+                ("R", ctypes.c_int), ("flags", ctypes.c_uint32), ("amplitude", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class Pages(ctypes.Structure):
+    """stt_pages."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "cu_q", "seq_lens")] + [
+        (n, ctypes.c_int64) for n in ("stride_page", "stride_head", "stride_tok")] + [
+        (n, ctypes.c_int) for n in ("B", "H_kv", "D", "page_size", "num_pages", "max_pages")]
+
+
+class Logits(ctypes.Structure):
+    """stt_logits."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "temperature", "repetition", "frequency", "presence", "tokens", "cu_tokens", "n_prompt",
+        "draft", "bias", "mask")] + [("draft_ld", ctypes.c_int), ("bias_rows", ctypes.c_int)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +132,22 @@ def _declare(L):
     L.stt_verify.restype = i32
     L.soft_ce_fwd_bwd_inplace_noalloc.argtypes = [vp, vp, vp, i64, i64, vp, vp, vp]
     L.soft_ce_fwd_bwd_inplace_noalloc.restype = i32
+    rope, pages = c.POINTER(Rope), c.POINTER(Pages)
+    L.stt_qkv_rope_fwd.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, rope, vp, vp, vp, vp]
+    L.stt_qkv_rope_fwd.restype = i32
+    L.stt_qkv_rope_bwd_workspace_size.argtypes = [i32]
+    L.stt_qkv_rope_bwd_workspace_size.restype = sz
+    L.stt_qkv_rope_bwd.argtypes = [vp, vp, vp, vp, i64, vp, i32, i32, i32, i32, i32, rope,
+                                   c.c_uint32, vp, i64, vp, vp, vp, sz, vp]
+    L.stt_qkv_rope_bwd.restype = i32
+    L.stt_kv_append.argtypes = [vp, i64, vp, i64, i32, pages, rope, vp, vp]
+    L.stt_kv_append.restype = i32
+    L.stt_paged_attn_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    L.stt_paged_attn_workspace_size.restype = sz
+    L.stt_paged_attn.argtypes = [vp, i64, i64, i32, pages, f32, vp, i32, vp, vp, vp, sz, vp]
+    L.stt_paged_attn.restype = i32
+    L.stt_logits_process.argtypes = [vp, i64, i64, i32, c.POINTER(Logits), c.c_uint32, vp, vp]
+    L.stt_logits_process.restype = i32
     L.stt_profile_start.argtypes = [i32]
     L.stt_profile_start.restype = i32
     L.stt_profile_stop.argtypes = [c.POINTER(i32), c.POINTER(i32), c.POINTER(f32), i32]

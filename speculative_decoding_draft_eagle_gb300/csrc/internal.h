@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace stt {
@@ -98,7 +99,68 @@ struct AttnBwdArgs {
 size_t attn_bwd_workspace(int B, int H, int H_kv, int D, int Q_LEN, uint32_t flags);
 cudaError_t attn_bwd_launch(const AttnArgs& a, const AttnBwdArgs& g, cudaStream_t s);
 
+// ------------------------------------------- rotation, paged cache, logits --
+struct RopeArgs {
+  const double* freq;
+  const __nv_bfloat16* w_q;
+  const __nv_bfloat16* w_k;
+  int R;
+  bool inter;
+  float amplitude, eps;
+};
+struct PagesArgs {
+  void* k;
+  void* v;
+  const int32_t* table;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int64_t stride_page, stride_head, stride_tok;
+  int B, H_kv, D, page_shift, num_pages, max_pages;
+};
+constexpr int kRopeBwdMaxGrid = 1024;  // blocks of the rotation's gradient
+cudaError_t qkv_rope_launch(const RopeArgs& r, const void* qkv, int64_t ld,
+                            const int32_t* positions, int B, int S, int H, int H_kv, int D, void* q,
+                            void* k, void* v, cudaStream_t s);
+size_t qkv_rope_bwd_workspace(int D);
+cudaError_t qkv_rope_bwd_launch(const RopeArgs& r, const void* dq, const void* dk, const void* dv,
+                                const void* qkv, int64_t ld, const int32_t* positions, int B,
+                                int S, int H, int H_kv, int D, bool bf16, void* dqkv, int64_t ld_d,
+                                float* dw_q, float* dw_k, void* workspace, cudaStream_t s);
+cudaError_t kv_append_launch(const RopeArgs& r, const PagesArgs& pg, const void* qkv, int64_t ld,
+                             const int32_t* positions, int64_t N, int H, void* q, cudaStream_t s);
+
+struct PagedAttnArgs {
+  const void* q;
+  int64_t ld_q;
+  int N, H;
+  float scale;
+  const uint32_t* tree;
+  int tree_words;
+  void* out;
+  float* lse;
+  void* workspace;
+};
+size_t paged_attn_workspace(int64_t N, int B, int H, int H_kv, int D);
+cudaError_t paged_attn_launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s);
+
+struct LogitsArgs {
+  const void* z;
+  int N, rows;
+  int V;
+  bool bf16, raw;
+  const float *temperature, *repetition, *frequency, *presence;
+  const int32_t *tokens, *cu_tokens, *n_prompt, *draft;
+  const float* bias;
+  const uint32_t* mask;
+  int draft_ld, bias_rows;
+  float* out;
+};
+constexpr int64_t kLogitsMaxV = 16 * 24576;
+cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s);
+
 // Per-file device error words (read and cleared).
+cudaError_t qkv_rope_error_word(uint32_t* w);
+cudaError_t paged_attn_error_word(uint32_t* w);
 cudaError_t soft_ce_error_word(uint32_t* w);
 cudaError_t attn_fwd_error_word(uint32_t* w);
 cudaError_t attn_bwd_error_word(uint32_t* w);
@@ -106,6 +168,7 @@ cudaError_t attn_bwd_error_word(uint32_t* w);
 cudaError_t soft_ce_set_wait_budget(uint64_t ns);
 cudaError_t attn_fwd_set_wait_budget(uint64_t ns);
 cudaError_t attn_bwd_set_wait_budget(uint64_t ns);
+cudaError_t paged_attn_set_wait_budget(uint64_t ns);
 
 // Streaming multiprocessors of the current device (cached per device; 1 if
 // the query fails, which only shrinks persistent grids).

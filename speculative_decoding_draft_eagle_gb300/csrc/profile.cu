@@ -102,6 +102,11 @@ const char* stt_kernel_name(int kernel_id) {
     case STT_KERNEL_SOFT_CE_VARIANT: return "soft_ce_variant";
     case STT_KERNEL_VERIFY: return "verify";
     case STT_KERNEL_LM_HEAD_CE: return "lm_head_ce";
+    case STT_KERNEL_QKV_ROPE: return "qkv_rope";
+    case STT_KERNEL_QKV_ROPE_BWD: return "qkv_rope_bwd";
+    case STT_KERNEL_KV_APPEND: return "kv_append";
+    case STT_KERNEL_PAGED_ATTN: return "paged_attn";
+    case STT_KERNEL_LOGITS: return "logits";
     default: return "unknown";
   }
 }

@@ -117,6 +117,82 @@ int check_attn(const void* q, const void* const* k_blocks, const void* const* v_
   return STT_OK;
 }
 
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Validation of the rotation's arguments; fills `r` on success.
+int check_rope(const stt_rope* rope, int D, stt::RopeArgs* r) {
+  if (!rope) return STT_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return STT_ERR_UNSUPPORTED;
+  if (rope->R < 0 || rope->R > D) return STT_ERR_INVALID_ARG;
+  if (rope->R % 16 != 0) return STT_ERR_UNSUPPORTED;
+  if ((rope->R > 0) != (rope->freq != nullptr)) return STT_ERR_INVALID_ARG;
+  if (rope->flags & ~(uint32_t)STT_ROPE_INTERLEAVED) return STT_ERR_INVALID_ARG;
+  if (!std::isfinite(rope->amplitude)) return STT_ERR_INVALID_ARG;
+  if ((rope->w_q || rope->w_k) && (!std::isfinite(rope->eps) || !(rope->eps > 0.f)))
+    return STT_ERR_INVALID_ARG;
+  if (!aligned(rope->freq, 8) || !aligned16(rope->w_q) || !aligned16(rope->w_k))
+    return STT_ERR_MISALIGNED;
+  r->freq = rope->freq;
+  r->w_q = static_cast<const __nv_bfloat16*>(rope->w_q);
+  r->w_k = static_cast<const __nv_bfloat16*>(rope->w_k);
+  r->R = rope->R;
+  r->inter = (rope->flags & STT_ROPE_INTERLEAVED) != 0;
+  r->amplitude = rope->amplitude;
+  r->eps = rope->eps;
+  return STT_OK;
+}
+
+// Rows of the projection: N of them, ld elements apart.
+int check_rows(const void* rows, int64_t ld, int64_t heads, int D) {
+  if (!rows) return STT_ERR_INVALID_ARG;
+  if (ld < heads * D) return STT_ERR_INVALID_ARG;
+  if (ld % 8 != 0 || !aligned16(rows)) return STT_ERR_MISALIGNED;
+  return STT_OK;
+}
+
+int check_pages(const stt_pages* p, int64_t N, stt::PagesArgs* g) {
+  if (!p) return STT_ERR_INVALID_ARG;
+  if (p->B < 0 || p->B > STT_MAX_BATCH || p->H_kv < 1 || N < 0) return STT_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return STT_ERR_UNSUPPORTED;
+  if (p->page_size < 1 || p->num_pages < 1 || p->max_pages < 1) return STT_ERR_INVALID_ARG;
+  int shift = 3;
+  while (shift < 10 && (1 << shift) != p->page_size) ++shift;
+  if ((1 << shift) != p->page_size) return STT_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages * p->page_size > 0x7fffffffll) return STT_ERR_UNSUPPORTED;
+  if (p->B > 0 && N > 0) {
+    if (!p->k || !p->v || !p->table || !p->cu_q || !p->seq_lens) return STT_ERR_INVALID_ARG;
+    if (!aligned16(p->k) || !aligned16(p->v) || !aligned(p->table, 4) || !aligned(p->cu_q, 4) ||
+        !aligned(p->seq_lens, 4))
+      return STT_ERR_MISALIGNED;
+    // Every key of a cache at its own place, in any order of page, head and key.
+    if (p->stride_page < 1 || p->stride_head < 1 || p->stride_tok < p->D)
+      return STT_ERR_INVALID_ARG;
+    if (p->stride_page % 8 || p->stride_head % 8 || p->stride_tok % 8) return STT_ERR_MISALIGNED;
+    if (p->stride_page > (1ll << 38) || p->stride_head > (1ll << 38) ||
+        p->stride_tok > (1ll << 38))
+      return STT_ERR_UNSUPPORTED;  // a tensor map's strides are 40-bit byte counts
+  }
+  g->k = p->k;
+  g->v = p->v;
+  g->table = p->table;
+  g->cu_q = p->cu_q;
+  g->seq_lens = p->seq_lens;
+  g->stride_page = p->stride_page;
+  g->stride_head = p->stride_head;
+  g->stride_tok = p->stride_tok;
+  g->B = p->B;
+  g->H_kv = p->H_kv;
+  g->D = p->D;
+  g->page_shift = shift;
+  g->num_pages = p->num_pages;
+  g->max_pages = p->max_pages;
+  return STT_OK;
+}
+
+static_assert(STT_ROPE_INTERLEAVED == 1u && STT_ROPE_BF16_GRADS == 2u, "rotation flags");
+
 }  // namespace
 
 extern "C" {
@@ -149,6 +225,10 @@ int stt_device_error(void* stream, uint32_t* word) {
   w |= part;
   if (stt::lm_head_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
   w |= part;
+  if (stt::qkv_rope_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
+  w |= part;
+  if (stt::paged_attn_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
+  w |= part;
   *word = w;
   return (w & STT_DEVERR_WAIT_MASK) ? STT_ERR_TIMEOUT : STT_OK;
 }
@@ -165,6 +245,7 @@ int stt_debug_set_wait_budget(uint64_t ns) {
   if (e == cudaSuccess) e = stt::attn_fwd_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::attn_bwd_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::lm_head_set_wait_budget(ns);
+  if (e == cudaSuccess) e = stt::paged_attn_set_wait_budget(ns);
   return from_cuda(e);
 }
 
@@ -355,6 +436,193 @@ int stt_verify(const float* p_target, const float* p_draft, const int32_t* draft
     return from_cuda(stt::verify_launch(p_target, p_draft, draft_tokens, u_accept, u_sample, B,
                                         gamma, V, n_accepted, out_tokens,
                                         static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int stt_qkv_rope_fwd(const void* qkv, int64_t ld, const int32_t* positions, int B, int S, int H,
+                     int H_kv, int D, const stt_rope* rope, void* q, void* k, void* v,
+                     void* stream) {
+  try {
+    begin_call();
+    stt::RopeArgs r{};
+    if (B < 0 || S < 0 || H < 1 || H_kv < 1) return STT_ERR_INVALID_ARG;
+    int st = check_rope(rope, D, &r);
+    if (st != STT_OK) return st;
+    if ((int64_t)B * S == 0) return STT_OK;
+    if ((int64_t)B * S > 0x7fffffffll || (int64_t)H + 2ll * H_kv > (1 << 20))
+      return STT_ERR_UNSUPPORTED;
+    st = check_rows(qkv, ld, (int64_t)H + 2ll * H_kv, D);
+    if (st != STT_OK) return st;
+    if (!q || !k || !v) return STT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned(positions, 4))
+      return STT_ERR_MISALIGNED;
+    return from_cuda(stt::qkv_rope_launch(r, qkv, ld, positions, B, S, H, H_kv, D, q, k, v,
+                                          static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+size_t stt_qkv_rope_bwd_workspace_size(int D) {
+  return D > 0 && D <= 128 ? stt::qkv_rope_bwd_workspace(D) : 16;
+}
+
+int stt_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, const void* qkv, int64_t ld,
+                     const int32_t* positions, int B, int S, int H, int H_kv, int D,
+                     const stt_rope* rope, uint32_t flags, void* dqkv, int64_t ld_d, float* dw_q,
+                     float* dw_k, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    begin_call();
+    stt::RopeArgs r{};
+    if (B < 0 || S < 0 || H < 1 || H_kv < 1) return STT_ERR_INVALID_ARG;
+    if (flags & ~(uint32_t)STT_ROPE_BF16_GRADS) return STT_ERR_INVALID_ARG;
+    int st = check_rope(rope, D, &r);
+    if (st != STT_OK) return st;
+    const bool norm = r.w_q || r.w_k;
+    if ((r.w_q != nullptr) != (dw_q != nullptr) || (r.w_k != nullptr) != (dw_k != nullptr))
+      return STT_ERR_INVALID_ARG;
+    if (!aligned(dw_q, 4) || !aligned(dw_k, 4)) return STT_ERR_MISALIGNED;
+    if (norm) {
+      if (!workspace || workspace_bytes < stt::qkv_rope_bwd_workspace(D))
+        return STT_ERR_WORKSPACE;
+      if (!aligned16(workspace)) return STT_ERR_MISALIGNED;
+    }
+    if ((int64_t)B * S > 0x7fffffffll || (int64_t)H + 2ll * H_kv > (1 << 20))
+      return STT_ERR_UNSUPPORTED;
+    if ((int64_t)B * S > 0) {
+      st = check_rows(dqkv, ld_d, (int64_t)H + 2ll * H_kv, D);
+      if (st == STT_OK && norm) st = check_rows(qkv, ld, (int64_t)H + 2ll * H_kv, D);
+      if (st != STT_OK) return st;
+      if (!dq || !dk || !dv) return STT_ERR_INVALID_ARG;
+      if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned(positions, 4))
+        return STT_ERR_MISALIGNED;
+    } else if (!norm) {
+      return STT_OK;
+    }
+    return from_cuda(stt::qkv_rope_bwd_launch(
+        r, dq, dk, dv, qkv, ld, positions, B, S, H, H_kv, D, (flags & STT_ROPE_BF16_GRADS) != 0,
+        dqkv, ld_d, dw_q, dw_k, workspace, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int stt_kv_append(const void* qkv, int64_t ld, const int32_t* positions, int64_t N, int H,
+                  const stt_pages* pages, const stt_rope* rope, void* q, void* stream) {
+  try {
+    begin_call();
+    stt::RopeArgs r{};
+    stt::PagesArgs g{};
+    if (H < 1) return STT_ERR_INVALID_ARG;
+    int st = check_pages(pages, N, &g);
+    if (st != STT_OK) return st;
+    st = check_rope(rope, g.D, &r);
+    if (st != STT_OK) return st;
+    if (N == 0 || g.B == 0) return STT_OK;
+    if (N > 0x7fffffffll || (int64_t)H + 2ll * g.H_kv > (1 << 20)) return STT_ERR_UNSUPPORTED;
+    st = check_rows(qkv, ld, (int64_t)H + 2ll * g.H_kv, g.D);
+    if (st != STT_OK) return st;
+    if (!q) return STT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned(positions, 4)) return STT_ERR_MISALIGNED;
+    return from_cuda(stt::kv_append_launch(r, g, qkv, ld, positions, N, H, q,
+                                           static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+size_t stt_paged_attn_workspace_size(int64_t N, int B, int H, int H_kv, int D) {
+  if (N < 1 || B < 1 || H < 1 || H_kv < 1 || D < 1 || H % H_kv != 0) return 16;
+  return stt::paged_attn_workspace(N, B, H, H_kv, D);
+}
+
+int stt_paged_attn(const void* q, int64_t ld_q, int64_t N, int H, const stt_pages* pages,
+                   float scale, const uint32_t* tree, int tree_words, void* out, float* lse,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    begin_call();
+    stt::PagesArgs g{};
+    int st = check_pages(pages, N, &g);
+    if (st != STT_OK) return st;
+    if (H < 1 || H % g.H_kv != 0) return STT_ERR_INVALID_ARG;
+    if (H / g.H_kv > 16) return STT_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return STT_ERR_INVALID_ARG;
+    if (tree && (tree_words < 1 || tree_words > (1 << 20))) return STT_ERR_INVALID_ARG;
+    if (N == 0 || g.B == 0) return STT_OK;
+    if (N > 0x7fffffffll || N * H > 0x7fffffffll) return STT_ERR_UNSUPPORTED;
+    st = check_rows(q, ld_q, H, g.D);
+    if (st != STT_OK) return st;
+    if (ld_q > (1ll << 38)) return STT_ERR_UNSUPPORTED;
+    if (!out) return STT_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned(lse, 4) || !aligned(tree, 4)) return STT_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < stt::paged_attn_workspace(N, g.B, H, g.H_kv, g.D))
+      return STT_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return STT_ERR_MISALIGNED;
+    stt::PagedAttnArgs a{};
+    a.q = q;
+    a.ld_q = ld_q;
+    a.N = (int)N;
+    a.H = H;
+    a.scale = scale;
+    a.tree = tree;
+    a.tree_words = tree_words;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    return from_cuda(stt::paged_attn_launch(g, a, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int stt_logits_process(const void* z, int64_t N, int64_t V, int rows, const stt_logits* params,
+                       uint32_t flags, float* out, void* stream) {
+  try {
+    begin_call();
+    if (!params || N < 0 || V < 1 || rows < 1) return STT_ERR_INVALID_ARG;
+    if (flags & ~(uint32_t)(STT_LOGITS_BF16 | STT_LOGITS_RAW)) return STT_ERR_INVALID_ARG;
+    if (N % rows != 0) return STT_ERR_INVALID_ARG;
+    if (V > stt::kLogitsMaxV || N > 0x7fffffffll / 16) return STT_ERR_UNSUPPORTED;
+    const stt_logits& p = *params;
+    if (!p.tokens != !p.cu_tokens || (p.n_prompt && !p.tokens)) return STT_ERR_INVALID_ARG;
+    if (p.draft && p.draft_ld < rows - 1) return STT_ERR_INVALID_ARG;
+    if (p.bias_rows < 0 || (p.bias_rows > 0) != (p.bias != nullptr)) return STT_ERR_INVALID_ARG;
+    if (p.bias_rows > 1 && p.bias_rows != N / rows) return STT_ERR_INVALID_ARG;
+    if (N == 0) return STT_OK;
+    if (!z || !out) return STT_ERR_INVALID_ARG;
+    const bool bf16 = (flags & STT_LOGITS_BF16) != 0;
+    if (bf16 && z == out) return STT_ERR_INVALID_ARG;
+    const uintptr_t all =
+        reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(p.temperature) |
+        reinterpret_cast<uintptr_t>(p.repetition) | reinterpret_cast<uintptr_t>(p.frequency) |
+        reinterpret_cast<uintptr_t>(p.presence) | reinterpret_cast<uintptr_t>(p.tokens) |
+        reinterpret_cast<uintptr_t>(p.cu_tokens) | reinterpret_cast<uintptr_t>(p.n_prompt) |
+        reinterpret_cast<uintptr_t>(p.draft) | reinterpret_cast<uintptr_t>(p.bias) |
+        reinterpret_cast<uintptr_t>(p.mask);
+    if ((all & 3u) || !aligned(z, bf16 ? 2 : 4)) return STT_ERR_MISALIGNED;
+    stt::LogitsArgs a{};
+    a.z = z;
+    a.N = (int)N;
+    a.rows = rows;
+    a.V = (int)V;
+    a.bf16 = bf16;
+    a.raw = (flags & STT_LOGITS_RAW) != 0;
+    a.temperature = p.temperature;
+    a.repetition = p.repetition;
+    a.frequency = p.frequency;
+    a.presence = p.presence;
+    a.tokens = p.tokens;
+    a.cu_tokens = p.cu_tokens;
+    a.n_prompt = p.n_prompt;
+    a.draft = p.draft;
+    a.bias = p.bias;
+    a.mask = p.mask;
+    a.draft_ld = p.draft_ld;
+    a.bias_rows = p.bias_rows;
+    a.out = out;
+    return from_cuda(stt::logits_launch(a, static_cast<cudaStream_t>(stream)));
   } catch (...) {
     return STT_ERR_CUDA;
   }
