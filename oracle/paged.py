@@ -12,11 +12,13 @@ def gather(cache, table_row, length):
 
 
 def attention(q, k_cache, v_cache, cu_q, seq_lens, table, scale, tree=None):
-    """out, lse, and sum p |v| (what bounds out's rounding) of every row; NaN in the
-    rows behind the last sequence.  tree: bool [N, new tokens] or None."""
+    """out, lse, and sum p |v| and sqrt(sum (p v)^2) (what bounds out's rounding, and
+    what it comes to where the roundings of p are independent) of every row; NaN in
+    the rows behind the last sequence.  tree: bool [N, new tokens] or None."""
     N, H, D = q.shape
     G = H // k_cache.shape[1]
-    out, lse, mag = np.full((N, H, D), np.nan), np.full((N, H), np.nan), np.full((N, H, D), np.nan)
+    out, lse = np.full((N, H, D), np.nan), np.full((N, H), np.nan)
+    mag, rms = np.full((N, H, D), np.nan), np.full((N, H, D), np.nan)
     for b in range(len(seq_lens)):
         first, n, L = int(cu_q[b]), int(cu_q[b + 1] - cu_q[b]), int(seq_lens[b])
         k, v = gather(k_cache, table[b], L), gather(v_cache, table[b], L)
@@ -29,7 +31,8 @@ def attention(q, k_cache, v_cache, cu_q, seq_lens, table, scale, tree=None):
                 sees[j[(j >= 0) & (j < L)]] = True
             for h in range(H):
                 if not sees.any():
-                    out[first + i, h], lse[first + i, h], mag[first + i, h] = 0.0, -np.inf, 0.0
+                    out[first + i, h], lse[first + i, h] = 0.0, -np.inf
+                    mag[first + i, h] = rms[first + i, h] = 0.0
                     continue
                 s = k[sees][:, h // G] @ q[first + i, h].astype(np.float64) * scale
                 m = s.max()
@@ -38,7 +41,8 @@ def attention(q, k_cache, v_cache, cu_q, seq_lens, table, scale, tree=None):
                 p /= p.sum()
                 out[first + i, h] = p @ v[sees][:, h // G]
                 mag[first + i, h] = p @ np.abs(v[sees][:, h // G])
-    return out, lse, mag
+                rms[first + i, h] = np.sqrt(p ** 2 @ v[sees][:, h // G] ** 2)
+    return out, lse, mag, rms
 
 
 def words(tree):

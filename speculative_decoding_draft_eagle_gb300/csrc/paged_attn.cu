@@ -1,8 +1,31 @@
 // paged_attn.cu -- attention of each sequence's new tokens over its pages.
 //
-// One warp per (row, query head): its lanes split D, keys come one after
-// another, with a running maximum and sum (the softmax's result does not depend
-// on the order).
+// A unit of work is a query tile of one KV head: up to 128 rows, row t G + g
+// being head g of the group of G query heads at new token t of the tile, so that
+// every key a CTA loads serves the whole group and, when there are few new
+// tokens, all of them.  A unit runs over the 128-key tiles that its last token
+// sees, flash-style: S = Q K^T and O += P V on the tensor cores (tcgen05, S and O
+// in tensor memory), keys and values brought page by page by TMA into swizzled
+// shared memory, softmax with a running maximum and sum in between.
+//
+// Persistent, one CTA per SM.  Every key tile of every unit counts one, and CTA c
+// takes the tiles [c W / G, (c + 1) W / G) of all W in the order (sequence, KV
+// head, query tile, key tile): whatever the lengths, the CTAs' shares differ by
+// one tile at most.  A unit cut by a share's border leaves partial results
+// (normalised rows and their logarithms of the sum) in the workspace, at most two
+// per CTA, and a second small kernel, launched as a programmatic dependent, joins
+// them in a fixed order.  The lengths are read on the device: nothing here depends
+// on what the host knows of the batch.
+//
+// Warp roles (384 threads), as in the training forward (attn_fwd.cu):
+//   warps 0-7  softmax: warps w and w + 4 own the 32 rows of TMEM lane quarter
+//              w % 4 and half of the 128 keys each; a quarter without live rows
+//              only keeps the barriers going.
+//   warp 8     queries and key pages (TMA); lanes look the pages up, a tile ahead.
+//   warp 9     issues S(g) into TMEM buffer g % 3.
+//   warp 10    issues O += P(g) V(g), P read from TMEM.
+//   warp 11    value pages (TMA).
+// Barrier phases count S products, stage uses and units over the CTA's whole share.
 #include <algorithm>
 
 #include "../../include/stt.h"
@@ -11,96 +34,768 @@
 namespace stt {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kStages = 2;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarpK = 8, kWarpMma = 9, kWarpPv = 10, kWarpV = 11;
+constexpr int kThreads = 384;
+constexpr int kMaxCtas = 160;  // CTAs the workspace has room for
+constexpr int kJoinThreads = 512;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 2^8 between rescales
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSBufs = 3;
+constexpr uint32_t kColO = kSBufs * kTile;
+
+// A unit cut by share borders, as seen from the CTA whose share begins inside it.
+struct JoinDesc {
+  int c0, c1;  // first and last CTA with a part; c0 < 0: none
+  int tok0, ntok, kvh, pad[3];
+};
 
 struct Params {
   PagesArgs g;
-  PagedAttnArgs a;
+  const uint32_t* tree;
+  __nv_bfloat16* out;
+  float* lse;
+  JoinDesc* join;
+  float* part;       // [2 ctas][slot]: O [slot_rows][D], then lse [slot_rows]
+  int tree_words, N, H, G, TT, slot_rows;
+  int64_t slot;      // floats from slot to slot
+  int key_cap;       // max_pages * page_size
+  int d_tok, d_head, d_page;  // place of each among the cache map's outer dimensions
+  float scale_log2;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_attn_simple(const __grid_constant__ Params P) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = w / P.a.H;
-  const int h = (int)(w - row * P.a.H);
-  if (row >= P.a.N) return;
-  const PagesArgs& G = P.g;
-  int b = 0;
-  for (int j = 0; j < G.B; j += 32) {
-    const bool ends = j + lane < G.B && __ldg(G.cu_q + 1 + j + lane) <= (int)row;
-    b += __popc(__ballot_sync(0xffffffffu, ends));
-  }
-  if (b >= G.B) return;
-  const int first = __ldg(G.cu_q + b), n = __ldg(G.cu_q + b + 1) - first;
-  const int len = __ldg(G.seq_lens + b), ctx = len - n, i = (int)row - first;
-  const int kvh = h / (P.a.H / G.H_kv);
+struct Smem {
+  static constexpr int kQ = kTile * D * 2;
+  static constexpr int kKV = kTile * D * 2;
+  static constexpr int q = 0;  // two Q buffers (unit parity)
+  static constexpr int k0 = 2 * kQ;
+  static constexpr int v0 = 2 * kQ + kStages * kKV;
+  static constexpr int total = 2 * kQ + 2 * kStages * kKV;
+  static constexpr int alloc = total + 1024;
+};
 
-  float q[E], o[E];
-  const __nv_bfloat16* qr =
-      static_cast<const __nv_bfloat16*>(P.a.q) + row * P.a.ld_q + (int64_t)h * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qr[e]) * P.a.scale;
-    o[e] = 0.f;
+// The batch in shared memory.
+struct Batch {
+  long long pref[kMaxBatch + 1];  // tiles before each sequence
+  int first[kMaxBatch], n[kMaxBatch], len[kMaxBatch];
+};
+
+// Keys the query tile j of a sequence needs.
+__device__ __forceinline__ int unit_keys(const Params& P, int n, int len, int j) {
+  const int cap = min(len, P.key_cap);
+  if (P.tree) return max(cap, 0);
+  const int last = min((j + 1) * P.TT, n);  // tokens up to the tile's end
+  return max(min(len - n + last, cap), 0);
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+
+// Part of one unit in a CTA's share: key tiles [t0, t1) of `tiles`.
+struct Seg {
+  int b, h, j, t0, t1, tiles, keys;
+  int tok0, ntok, n, ctx;
+  long long u0;  // the unit's first tile in the order of all
+};
+
+struct Walk {
+  long long pos, end;
+  int b, h, j, off;
+
+  __device__ __forceinline__ void init(const Params& P, const Batch& S, long long c, long long n) {
+    const int B = P.g.B;
+    const long long W = S.pref[B];
+    pos = W * c / n;
+    end = W * (c + 1) / n;
+    if (pos >= end) return;
+    int lo = 0, hi = B - 1;  // last sequence with pref <= pos and tiles of its own
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (S.pref[mid] <= pos) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    long long rem = pos - S.pref[b];
+    const long long per_head = (S.pref[b + 1] - S.pref[b]) / P.g.H_kv;
+    h = (int)(rem / per_head);
+    rem -= h * per_head;
+    for (j = 0;; ++j) {
+      const int cost = max(tiles_of(unit_keys(P, S.n[b], S.len[b], j)), 1);
+      if (rem < cost) break;
+      rem -= cost;
+    }
+    off = (int)rem;
   }
-  float m = -INFINITY, l = 0.f;
-  const int end = P.a.tree ? len : ctx + i + 1;
-  bool bad = false;
-  for (int key = 0; key < end; ++key) {
-    if (P.a.tree && key >= ctx) {
-      const int j = key - ctx;
-      if (j >= 32 * P.a.tree_words) break;
-      if (!((__ldg(P.a.tree + row * P.a.tree_words + (j >> 5)) >> (j & 31)) & 1u)) continue;
+
+  __device__ __forceinline__ bool next(const Params& P, const Batch& S, Seg& s) {
+    if (pos >= end) return false;
+    s.b = b;
+    s.h = h;
+    s.j = j;
+    s.n = S.n[b];
+    s.ctx = S.len[b] - s.n;
+    s.keys = unit_keys(P, s.n, S.len[b], j);
+    s.tiles = tiles_of(s.keys);
+    s.tok0 = S.first[b] + j * P.TT;
+    s.ntok = min(P.TT, s.n - j * P.TT);
+    s.u0 = pos - off;
+    const int cost = max(s.tiles, 1);
+    const long long left = end - pos;
+    s.t0 = off;
+    s.t1 = (long long)(cost - off) <= left ? cost : off + (int)left;
+    pos += s.t1 - s.t0;
+    off = 0;
+    if ((j + 1) * P.TT < s.n) {
+      ++j;
+    } else {
+      j = 0;
+      if (++h == P.g.H_kv) {
+        h = 0;
+        do ++b; while (b < P.g.B && S.n[b] <= 0);
+      }
     }
-    const int slot = key >> G.page_shift;
-    if (slot >= G.max_pages) {
-      bad = true;
-      break;
-    }
-    const int page = __ldg(G.table + (int64_t)b * G.max_pages + slot);
-    if (page < 0 || page >= G.num_pages) {
-      bad = true;
-      continue;
-    }
-    const int64_t at = (int64_t)page * G.stride_page + (int64_t)kvh * G.stride_head +
-                       (int64_t)(key & ((1 << G.page_shift) - 1)) * G.stride_tok + lane * E;
-    const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(G.k) + at;
-    const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(G.v) + at;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(kr[e]), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s);
-    const float alpha = expf(m - mn), p = expf(s - mn);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(p, __bfloat162float(vr[e]), o[e] * alpha);
-    m = mn;
+    if (s.tiles == 0) s.t0 = s.t1 = 0;  // its place in the order is not a tile
+    return true;
   }
-  if (bad && lane == 0) record_error(STT_DEVERR_PAGE);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.a.out) + (row * P.a.H + h) * D + lane * E;
+};
+
+// The 32 bits of a row's tree mask over keys whose first is `o` after the context:
+// ones before the context's end.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int o) {
+  const int w = o >> 5;
+  const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? __ldg(row + w) : 0u);
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? __ldg(row + w + 1) : 0u);
+  return __funnelshift_r(lo, hi, o & 31);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV) {
+  using L = Smem<D>;
+  constexpr uint32_t kSite = STT_DEVERR_PAGED_WAIT;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Phases as in the training forward: see there why p_full and s_free are per S
+  // buffer and o_done alternates.
+  __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kStages], bar_v_full[kStages],
+      bar_k_empty[kStages], bar_v_empty[kStages], bar_s_full[kSBufs], bar_s_free[kSBufs],
+      bar_p_full[kSBufs], bar_o_done[2], bar_o_final, bar_drain, bar_quad[4];
+  __shared__ uint32_t tmem_base;
+  __shared__ float s_max[2][2][kTile], s_sum[2][2][kTile];
+  __shared__ Batch S;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = P.g.B;
+
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar_q_full[x], 1);
+      mbar_init(&bar_q_empty[x], 1);
+      mbar_init(&bar_o_done[x], 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar_k_full[s], 1);
+      mbar_init(&bar_v_full[s], 1);
+      mbar_init(&bar_k_empty[s], 1);
+      mbar_init(&bar_v_empty[s], 1);
+    }
+    for (int s = 0; s < kSBufs; ++s) {
+      mbar_init(&bar_s_full[s], 1);
+      mbar_init(&bar_s_free[s], 1);
+      mbar_init(&bar_p_full[s], kSoftmaxWarps);
+    }
+    mbar_init(&bar_o_final, 1);
+    mbar_init(&bar_drain, 2);
+    for (int q = 0; q < 4; ++q) mbar_init(&bar_quad[q], 2);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  // The batch: rows and lengths, each sequence's tiles (a warp each), their sums.
+  for (int b = tid; b < B; b += kThreads) {
+    const int lo = max(0, min(__ldg(P.g.cu_q + b), P.N));
+    const int hi = max(lo, min(__ldg(P.g.cu_q + b + 1), P.N));
+    S.first[b] = lo;
+    S.n[b] = hi - lo;
+    S.len[b] = __ldg(P.g.seq_lens + b);
+    if (hi > lo && S.len[b] > P.key_cap) record_error(STT_DEVERR_PAGE);
+  }
+  __syncthreads();
+  for (int b = warp; b < B; b += kThreads / 32) {
+    const int n = S.n[b], len = S.len[b];
+    long long t = 0;
+    for (long long j = lane; j * P.TT < n; j += 32)
+      t += max(tiles_of(unit_keys(P, n, len, (int)j)), 1);
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
-  if (P.a.lse && lane == 0) P.a.lse[row * P.a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
+  }
+  __syncthreads();
+  if (warp == 1) {
+    long long carry = 0;
+    if (lane == 0) S.pref[0] = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      long long v = b0 + lane < B ? S.pref[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      v += carry;
+      if (b0 + lane < B) S.pref[b0 + lane + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const long long W = S.pref[B];
+  const int ctas = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
+  Walk walk;
+  walk.pos = walk.end = 0;
+  if ((int)blockIdx.x < ctas) walk.init(P, S, blockIdx.x, ctas);
+  Seg s;
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // --------------------------------------------------- page producers ----
+    const bool is_k = warp == kWarpK;
+    const CUtensorMap* const tm = is_k ? &tmK : &tmV;
+    unsigned char* const base = smem + (is_k ? L::k0 : L::v0);
+    uint64_t* const full = is_k ? bar_k_full : bar_v_full;
+    uint64_t* const empty = is_k ? bar_k_empty : bar_v_empty;
+    const int page = 1 << P.g.page_shift;
+    const int box = min(page, kTile);      // keys a copy brings
+    const int copies = kTile / box;        // copies a tile takes, one lane each
+    if (lane == 0) {
+      tma_prefetch_desc(tm);
+      if (is_k) tma_prefetch_desc(&tmQ);
+    }
+    uint32_t g = 0, i = 0, q_issued = 0;
+    bool ok = true;
+    while (ok && walk.next(P, S, s)) {
+      if (s.tiles == 0) continue;
+      if (is_k) {
+        const int qs = i & 1;
+        if (i >= 2) ok = warp_wait(&bar_q_empty[qs], ((i >> 1) - 1u) & 1u, kSite);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar_q_full[qs], (uint32_t)(P.G * P.TT * D * 2));
+          for (int cb = 0; cb < D / kColBlock; ++cb)
+            tma_load_3d(smem + L::q + qs * L::kQ + cb * kTile * 128, &tmQ, &bar_q_full[qs],
+                        cb * kColBlock, s.h * P.G, s.tok0);
+        }
+        q_issued = i + 1;
+      }
+      const int32_t* table = P.g.table + (int64_t)s.b * P.g.max_pages;
+      // This lane's page of a tile (-1: past the unit's keys).
+      auto look = [&](int t) {
+        const int key = t * kTile + lane * box;
+        return lane < copies && t < s.t1 && key < s.keys ? __ldg(table + (key >> P.g.page_shift))
+                                                          : -1;
+      };
+      int pg = look(s.t0);
+      for (int t = s.t0; t < s.t1; ++t, ++g) {
+        const int st = g & 1;
+        const int key = t * kTile + lane * box;
+        const bool mine = lane < copies && key < s.keys;
+        int p = pg;
+        pg = look(t + 1);
+        if (mine && (p < 0 || p >= P.g.num_pages)) {
+          record_error(STT_DEVERR_PAGE);
+          p = 0;
+        }
+        if (g >= (uint32_t)kStages) ok = warp_wait(&empty[st], ((g >> 1) - 1u) & 1u, kSite);
+        if (!ok) break;
+        const int n_copies = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(n_copies * box * D * 2));
+        __syncwarp();
+        if (mine) {
+          const int in_page = key & (page - 1);
+          const int c1 = P.d_tok == 1 ? in_page : (P.d_head == 1 ? s.h : p);
+          const int c2 = P.d_tok == 2 ? in_page : (P.d_head == 2 ? s.h : p);
+          const int c3 = P.d_tok == 3 ? in_page : (P.d_head == 3 ? s.h : p);
+          for (int cb = 0; cb < D / kColBlock; ++cb)
+            tma_load_4d(base + st * L::kKV + cb * kTile * 128 + lane * box * 128, tm, &full[st],
+                        cb * kColBlock, c1, c2, c3);
+        }
+      }
+      ++i;
+    }
+    // Every copy issued lands before the CTA exits (on the way out after a wait that
+    // gave up, too).
+    for (uint32_t x = g > (uint32_t)kStages ? g - kStages : 0; x < g; ++x)
+      mbar_wait(&full[x & 1], (x >> 1) & 1u, kSite);
+    if (q_issued > 0) mbar_wait(&bar_q_full[(q_issued - 1) & 1], ((q_issued - 1) >> 1) & 1u, kSite);
+  } else if (warp == kWarpMma || warp == kWarpPv) {
+    // ------------------------------------------------------- MMA issuers --
+    if (lane == 0) {
+      const uint32_t idS = idesc_bf16(128, kTile, false, false);
+      const uint32_t idO = idesc_bf16(128, D, false, true);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(smem + L::k0), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(smem + L::v0), kTile * 128, 1024);
+      uint32_t g = 0, i = 0;
+      bool ok = true;
+      while (ok && walk.next(P, S, s)) {
+        if (s.tiles == 0) continue;
+        if (warp == kWarpMma) {
+          ok = mbar_wait(&bar_q_full[i & 1], (i >> 1) & 1u, kSite);
+          const uint64_t dQ = sdesc_sw128(smem_u32(smem + L::q + (i & 1) * L::kQ), 16, 1024);
+          for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
+            const int st = g & 1, sb = (int)(g % kSBufs);
+            ok = mbar_wait(&bar_k_full[st], (g >> 1) & 1u, kSite);
+            if (ok && g >= (uint32_t)kSBufs)
+              ok = mbar_wait(&bar_s_free[sb], (g / kSBufs - 1u) & 1u, kSite);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dK = sdesc_add(dK0, st * L::kKV);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * kTile * 128 + (kk & 3) * 32;
+              umma_bf16_ss(tmem + sb * kTile, sdesc_add(dQ, off), sdesc_add(dK, off), idS,
+                           kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bar_s_full[sb]);
+            umma_commit(&bar_k_empty[st]);
+          }
+          if (ok) umma_commit(&bar_q_empty[i & 1]);
+        } else {
+          for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
+            const int st = g & 1, sb = (int)(g % kSBufs);
+            ok = mbar_wait(&bar_p_full[sb], (g / kSBufs) & 1u, kSite) &&
+                 mbar_wait(&bar_v_full[st], (g >> 1) & 1u, kSite);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dV = sdesc_add(dV0, st * L::kKV);
+            const uint32_t aP = tmem + sb * kTile;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_ts(tmem + kColO, aP + (kk >> 2) * 64 + (kk & 3) * 8,
+                           sdesc_add(dV, kk * 2048), idO, (t > s.t0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bar_o_done[g & 1]);
+            umma_commit(&bar_s_free[sb]);
+            umma_commit(&bar_v_empty[st]);
+          }
+          if (ok) umma_commit(&bar_o_final);
+        }
+        ++i;
+      }
+      umma_commit(&bar_drain);
+      mbar_wait(&bar_drain, 0, kSite);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax --
+    constexpr int DH = D / 2;  // O columns per thread
+    const int quarter = warp & 3, part = warp >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const float sl2 = P.scale_log2;
+    const int t_row = r / P.G, g_row = r - t_row * P.G;
+    uint32_t quad_uses = 0, g = 0, n_final = 0;
+    bool ok = true, joined = false;
+    for (uint32_t i = 0; ok && walk.next(P, S, s);) {
+      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      // A share's first segment that begins inside its unit leaves what the join
+      // needs to know.
+      if (!whole && s.t0 > 0 && tid == 0) {
+        joined = true;
+        const long long last = s.u0 + s.tiles - 1;
+        JoinDesc d;
+        d.c0 = (int)(((s.u0 + 1) * ctas - 1) / W);
+        d.c1 = (int)(((last + 1) * ctas - 1) / W);
+        d.tok0 = s.tok0;
+        d.ntok = s.ntok;
+        d.kvh = s.h;
+        P.join[blockIdx.x] = d;
+      }
+      const int live = s.ntok * P.G;             // live rows of the tile
+      const bool dead = quarter * 32 >= live;    // none in this quarter
+      const bool row_live = r < live;
+      const int q_tok = s.j * P.TT + t_row;      // new token of this row
+      int lim = P.tree ? s.keys - 1 : min(s.ctx + q_tok, s.keys - 1);
+      if (!row_live) lim = -1;
+      const uint32_t* tree_row =
+          P.tree && row_live ? P.tree + (int64_t)(s.tok0 + t_row) * P.tree_words : nullptr;
+
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
+        const int sb = (int)(g % kSBufs);
+        ok = warp_wait(&bar_s_full[sb], (g / kSBufs) & 1u, kSite);
+        if (!ok) break;
+        // Values behind the unit's last key may be anything: zeros, so that the
+        // products with their zero probabilities vanish.  These warps do not follow
+        // v_full's phases in turn, so they make sure first that the phase before
+        // V(g)'s is over: O += P(g-2) V, which consumed that stage's last values.
+        // (S(g) is there, so O += P(g-3) V and all before it are complete, and the
+        // phase of o_done waited for is its barrier's current or latest one.)
+        const int behind = s.keys - t * kTile;
+        if (behind < kTile) {
+          const int st = g & 1;
+          if (g >= (uint32_t)kStages) ok = warp_wait(&bar_o_done[g & 1], ((g >> 1) - 1u) & 1u, kSite);
+          ok = ok && warp_wait(&bar_v_full[st], (g >> 1) & 1u, kSite);
+          if (!ok) break;
+          unsigned char* const v = smem + L::v0 + st * L::kKV;
+          for (int x = behind * (D / 8) + tid; x < kTile * (D / 8); x += kSoftmaxWarps * 32)
+            *reinterpret_cast<uint4*>(v + swz_chunk_offset(x / (D / 8), x % (D / 8), kTile)) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        if (dead) {
+          warp_arrive(&bar_p_full[sb]);
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t scol = tmem + lane_off + sb * kTile + part * 64;
+        uint32_t sc[2][32];
+        tmem_ld32x2(scol, scol + 32, sc[0], sc[1]);
+
+        const int cbase = t * kTile + part * 64;
+        float mp[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
+        if (cbase + 63 <= (P.tree ? min(lim, s.ctx - 1) : lim)) {
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+            for (int x = 0; x < 32; x += 2)
+              mp[(x >> 1) & 7] = fmax3(mp[(x >> 1) & 7], __uint_as_float(sc[c2][x]),
+                                       __uint_as_float(sc[c2][x + 1]));
+        } else {
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            // Bit x: key cbase + 32 c2 + x is visible.
+            const int k0 = cbase + c2 * 32, left = lim + 1 - k0;
+            uint32_t bits = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+            if (tree_row) bits &= tree_bits(tree_row, P.tree_words, k0 - s.ctx);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float v = (bits >> x) & 1u ? __uint_as_float(sc[c2][x]) : -INFINITY;
+              sc[c2][x] = __float_as_uint(v);
+              mp[x & 7] = fmaxf(mp[x & 7], v);
+            }
+          }
+        }
+        float mt = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                         fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+        s_max[g & 1][part][r] = mt;
+        ok = group_sync(&bar_quad[quarter], quad_uses, kSite);
+        if (!ok) break;
+        mt = fmaxf(mt, s_max[g & 1][part ^ 1][r]);
+
+        float alpha = 1.f;
+        bool rescale_o = false;
+        const float m_new = fmaxf(m_run, mt);
+        if (m_new > m_run + kRescaleThreshold) {
+          alpha = ex2(m_run - m_new);
+          l_run *= alpha;
+          m_run = m_new;
+          rescale_o = t > s.t0;
+        }
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+        uint32_t pk[32];
+        const uint64_t sl2x2 = f32x2(sl2, sl2), negm2 = f32x2(-m_use, -m_use);
+        uint64_t rp[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rp[k] = f32x2(0.f, 0.f);
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float x0, x1;
+            unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(sc[c2][x]), __uint_as_float(sc[c2][x + 1])),
+                                   sl2x2, negm2),
+                         x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            rp[(x >> 1) & 3] = add_f32x2(rp[(x >> 1) & 3], f32x2(p0, p1));
+            pk[(c2 * 32 + x) >> 1] = pack_bf16(p0, p1);
+          }
+        float ra, rb;
+        unpack_f32x2(add_f32x2(add_f32x2(rp[0], rp[1]), add_f32x2(rp[2], rp[3])), ra, rb);
+        l_run += ra + rb;
+
+        if (__any_sync(0xffffffffu, rescale_o)) {
+          ok = warp_wait(&bar_o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u, kSite);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ocol = tmem + lane_off + kColO + part * DH;
+#pragma unroll
+          for (int c2 = 0; c2 < DH / 32; ++c2) {
+            uint32_t o[32];
+            tmem_ld32(ocol + c2 * 32, o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+            tmem_st32(ocol + c2 * 32, o);
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          uint32_t pp[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pp[c] = pk[c2 * 16 + c];
+          tmem_st16(scol + c2 * 16, pp);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&bar_p_full[sb]);
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------- results ----
+      float o[DH];
+      if (s.tiles > 0) {
+        ok = warp_wait(&bar_o_final, n_final & 1u, kSite);
+        ++n_final;
+        ++i;
+        if (!ok) break;
+        if (dead) continue;
+        tc_fence_after();
+        const uint32_t ocol = tmem + lane_off + kColO + part * DH;
+#pragma unroll
+        for (int c2 = 0; c2 < DH / 32; ++c2) {
+          uint32_t u[32];
+          tmem_ld32(ocol + c2 * 32, u);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[c2 * 32 + x] = __uint_as_float(u[x]);
+        }
+        tc_fence_before();
+        s_sum[i & 1][part][r] = l_run;
+        ok = group_sync(&bar_quad[quarter], quad_uses, kSite);
+        if (!ok) break;
+        l_run += s_sum[i & 1][part ^ 1][r];
+      } else {
+        if (dead) continue;
+#pragma unroll
+        for (int x = 0; x < DH; ++x) o[x] = 0.f;
+      }
+      if (row_live) {
+        // A row that saw nothing has l = 0 and O = 0.
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
+        if (whole) {
+          const int64_t at = (int64_t)(s.tok0 + t_row) * P.H + s.h * P.G + g_row;
+          uint4* dst = reinterpret_cast<uint4*>(P.out + at * D + part * DH);
+#pragma unroll
+          for (int c = 0; c < DH / 8; ++c)
+            dst[c] = make_uint4(pack_bf16(o[c * 8 + 0] * inv, o[c * 8 + 1] * inv),
+                                pack_bf16(o[c * 8 + 2] * inv, o[c * 8 + 3] * inv),
+                                pack_bf16(o[c * 8 + 4] * inv, o[c * 8 + 5] * inv),
+                                pack_bf16(o[c * 8 + 6] * inv, o[c * 8 + 7] * inv));
+          if (part == 0 && P.lse) P.lse[at] = lse2 * kLn2;
+        } else {
+          float* slot = P.part + (int64_t)(2 * blockIdx.x + (s.t0 > 0 ? 0 : 1)) * P.slot;
+          float4* dst = reinterpret_cast<float4*>(slot + (int64_t)r * D + part * DH);
+#pragma unroll
+          for (int c = 0; c < DH / 4; ++c)
+            dst[c] = make_float4(o[c * 4] * inv, o[c * 4 + 1] * inv, o[c * 4 + 2] * inv,
+                                 o[c * 4 + 3] * inv);
+          if (part == 0) slot[(int64_t)P.slot_rows * D + r] = lse2;
+        }
+      }
+    }
+    if (tid == 0 && !joined) P.join[blockIdx.x].c0 = -1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the units cut by share borders.  The CTAs c0 + 1 .. c1 whose
+// shares begin inside a unit divide its rows among their blocks; the warps of a
+// block take a row each, or several share a row's parts when there are few rows.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_constant__ Params P) {
+  constexpr int E = D / 32, kW = kJoinThreads / 32;
+  __shared__ float s_o[kW][D], s_l[kW];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const JoinDesc d = P.join[blockIdx.x];
+  if (d.c0 < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = d.c1 - d.c0 + 1, rows = d.ntok * P.G;
+  const int share = parts - 1, first = (int)blockIdx.x - d.c0 - 1;
+  const int mine = first < rows ? (rows - first + share - 1) / share : 0;
+  if (mine == 0) return;
+  int wpr = 1;  // warps per row
+  while (wpr * 2 * mine <= kW && wpr * 2 <= parts) wpr *= 2;
+  const int sub = warp % wpr;
+  for (int x0 = 0; x0 < mine; x0 += kW / wpr) {
+    const int x = x0 + warp / wpr;
+    const int r = first + x * share;
+    float acc[E], l = 0.f, m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (x < mine) {
+#pragma unroll 4
+      for (int p = sub; p < parts; p += wpr) {
+        const float* src = P.part + (int64_t)(2 * (d.c0 + p) + (p == 0 ? 1 : 0)) * P.slot;
+        const float lse = src[(int64_t)P.slot_rows * D + r];
+        float v[E];
+        if constexpr (E == 4) {
+          const float4 f = reinterpret_cast<const float4*>(src + (int64_t)r * D)[lane];
+          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+          const float2 f = reinterpret_cast<const float2*>(src + (int64_t)r * D)[lane];
+          v[0] = f.x; v[1] = f.y;
+        }
+        if (lse != -INFINITY) {
+          const float mn = fmaxf(m, lse), a = ex2(m - mn), w = ex2(lse - mn);
+          l = l * a + w;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e] * a);
+          m = mn;
+        }
+      }
+    }
+    if (wpr > 1) {
+      // The row's warps, in order, relative to the largest.
+      const float part_inv = l == 0.f ? 0.f : 1.f / l;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e] * part_inv;
+      if (lane == 0) s_l[warp] = l == 0.f ? -INFINITY : m + log2f(l);
+      __syncthreads();
+      if (sub == 0) {
+        m = -INFINITY;
+        l = 0.f;
+        for (int y = 0; y < wpr; ++y) m = fmaxf(m, s_l[warp + y]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int y = 0; y < wpr; ++y) {
+          if (s_l[warp + y] == -INFINITY) continue;
+          const float w = ex2(s_l[warp + y] - m);
+          l += w;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, s_o[warp + y][lane * E + e], acc[e]);
+        }
+      }
+    }
+    if (x < mine && sub == 0) {
+      const int t = r / P.G, g = r - t * P.G;
+      const int64_t at = (int64_t)(d.tok0 + t) * P.H + d.kvh * P.G + g;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + at * D) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+      if (P.lse && lane == 0) P.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+}
+
+int slot_rows(int64_t N, int G) { return (int)std::min<int64_t>(N * G, kTile); }
+
+// Floats of a partial result, each starting on a 128-byte line.
+int64_t slot_floats(int rows, int D) { return ((int64_t)rows * (D + 1) + 31) / 32 * 32; }
+
+constexpr size_t kJoinBytes = (kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+
+// A cache as a tensor map: elements, then keys, heads and pages by increasing
+// stride; a box is `box` keys of one head.
+cudaError_t encode_cache(CUtensorMap* map, const void* base, const PagesArgs& g, int box, int* place) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  struct Dim { int64_t stride; cuuint64_t size; int what; } d[3] = {
+      {g.stride_tok, (cuuint64_t)1 << g.page_shift, 0},
+      {g.stride_head, (cuuint64_t)g.H_kv, 1},
+      {g.stride_page, (cuuint64_t)g.num_pages, 2}};
+  std::stable_sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  cuuint64_t dims[4] = {(cuuint64_t)g.D, d[0].size, d[1].size, d[2].size};
+  cuuint64_t strides[3];
+  cuuint32_t boxes[4] = {(cuuint32_t)kColBlock, 1, 1, 1}, es[4] = {1, 1, 1, 1};
+  for (int x = 0; x < 3; ++x) {
+    strides[x] = (cuuint64_t)d[x].stride * 2;
+    place[d[x].what] = x + 1;
+    if (d[x].what == 0) boxes[x + 1] = (cuuint32_t)box;
+  }
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                   boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The queries: elements, heads, rows; a box is a group's heads at TT rows.
+cudaError_t encode_q(CUtensorMap* map, const PagedAttnArgs& a, int D, int G, int TT) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.ld_q * 2};
+  cuuint32_t box[3] = {(cuuint32_t)kColBlock, (cuuint32_t)G, (cuuint32_t)TT}, es[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s) {
+  Params P{};
+  P.g = pg;
+  P.tree = a.tree;
+  P.tree_words = a.tree_words;
+  P.out = static_cast<__nv_bfloat16*>(a.out);
+  P.lse = a.lse;
+  P.N = a.N;
+  P.H = a.H;
+  P.G = a.H / pg.H_kv;
+  P.TT = std::min(kTile / P.G, a.N);
+  P.slot_rows = slot_rows(a.N, P.G);
+  P.slot = slot_floats(P.slot_rows, D);
+  P.key_cap = pg.max_pages << pg.page_shift;
+  P.scale_log2 = a.scale * kLog2e;
+  P.join = static_cast<JoinDesc*>(a.workspace);
+  P.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + kJoinBytes);
+  CUtensorMap tmQ, tmK, tmV;
+  cudaError_t e;
+  const int box = std::min(1 << pg.page_shift, kTile);
+  int place[3];
+  if ((e = bind_device_context()) != cudaSuccess) return e;
+  if ((e = encode_q(&tmQ, a, D, P.G, P.TT)) != cudaSuccess) return e;
+  if ((e = encode_cache(&tmK, pg.k, pg, box, place)) != cudaSuccess) return e;
+  if ((e = encode_cache(&tmV, pg.v, pg, box, place)) != cudaSuccess) return e;
+  P.d_tok = place[0];
+  P.d_head = place[1];
+  P.d_page = place[2];
+  e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<D>::alloc);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min(sm_count(), kMaxCtas);
+  prof_before(s, STT_KERNEL_PAGED_ATTN);
+  paged_attn_kernel<D><<<grid, kThreads, Smem<D>::alloc, s>>>(P, tmQ, tmK, tmV);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_attn_join<D>, P);
+  }
+  prof_after(s);
+  return e;
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int64_t, int, int, int, int) { return 16; }
+size_t paged_attn_workspace(int64_t N, int B, int H, int H_kv, int D) {
+  (void)B;
+  return kJoinBytes +
+         (size_t)(2 * kMaxCtas * slot_floats(slot_rows(N, H / H_kv), D)) * sizeof(float);
+}
 
 cudaError_t paged_attn_launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s) {
-  Params P{pg, a};
-  const int64_t warps = (int64_t)a.N * a.H;
-  const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-  prof_before(s, STT_KERNEL_PAGED_ATTN);
-  if (pg.D == 128) paged_attn_simple<128><<<grid, kThreads, 0, s>>>(P);
-  else paged_attn_simple<64><<<grid, kThreads, 0, s>>>(P);
-  prof_after(s);
-  return cudaGetLastError();
+  if (pg.D == 128) return launch<128>(pg, a, s);
+  return launch<64>(pg, a, s);
 }
 
 STT_DEFINE_ERROR_ACCESSOR(paged_attn_error_word)

@@ -51,14 +51,14 @@ def test_paged_attention_is_attention_over_the_gathered_keys():
     k, v = rng.standard_normal((2, 8, H_kv, page, D))
     table = np.array([[5, 0, 3], [7, 2, 6]])
     q = rng.standard_normal((2 * L, H, D))
-    out, lse, _ = op.attention(q, k, v, [0, L, 2 * L], [L, L], table, 0.3)
+    out, lse, _, _ = op.attention(q, k, v, [0, L, 2 * L], [L, L], table, 0.3)
     dense = lambda c: np.stack([op.gather(c, t, L) for t in table]).transpose(0, 2, 1, 3)  # noqa: E731
     o2, l2 = oa.forward(q.reshape(B, L, H, D).transpose(0, 2, 1, 3), [dense(k)], [dense(v)],
                         [L, L], 0.3)
     assert np.abs(out.reshape(B, L, H, D).transpose(0, 2, 1, 3) - o2).max() < 1e-12
     assert np.abs(lse.reshape(B, L, H).transpose(0, 2, 1) - l2).max() < 1e-12
     tree = np.tril(np.ones((L, L), bool))
-    o3, _, _ = op.attention(q, k, v, [0, L, 2 * L], [L, L], table, 0.3, np.vstack([tree, tree]))
+    o3, _, _, _ = op.attention(q, k, v, [0, L, 2 * L], [L, L], table, 0.3, np.vstack([tree, tree]))
     assert np.array_equal(o3, out)
 
 

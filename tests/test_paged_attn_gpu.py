@@ -3,7 +3,11 @@
 Bounds.  p enters the second product rounded to bf16 (at most 2^-8 of it), the
 scores are fp32 sums of D products (|error| <= 2^-13 for these N(0, 1) inputs, so
 2^-12 of p covers them), and the result is rounded once:
-    |out - o| <= 2^-8 |o| + (2^-8 + 2^-11) sum p |v|,   |lse error| <= 2^-12."""
+    |out - o| <= 2^-8 |o| + (2^-8 + 2^-11) sum p |v|,   |lse error| <= 2^-12.
+That is wide where many keys share the weight.  A rounding is at most uniform over
+its step, 2^-8 / sqrt(3) root mean square, and those of p are independent, so the
+whole error's norm is held to twice that of 2^-8 / sqrt(3) sqrt(sum (p v)^2 + o^2)
+for cases with enough elements (1000) to speak of one."""
 
 import math
 
@@ -28,11 +32,18 @@ def _built():
 
 def _check(bt, q, out, lse, tree=None, scale=None):
     D = q.shape[-1]
-    o, l, mag = opg.attention(f64(q), f64(bt.k), f64(bt.v), bt.cu, bt.lens, bt.table,
+    o, l, mag, rms = opg.attention(f64(q), f64(bt.k), f64(bt.v), bt.cu, bt.lens, bt.table,
                               1 / math.sqrt(D) if scale is None else scale, tree)
     n = int(bt.cu[-1])
     within(out[:n], o[:n], BF16 * np.abs(o[:n]) + (BF16 + 2.0 ** -11) * mag[:n], "out")
     within(lse[:n], l[:n], 2.0 ** -12, "lse")
+    _in_norm(f64(out[:n]), o[:n], rms[:n])
+
+
+def _in_norm(got, o, rms):
+    if o.size >= 1000:
+        lim = 2 * BF16 / math.sqrt(3) * np.linalg.norm(np.hypot(rms, o))
+        assert np.linalg.norm(got - o) <= lim, (np.linalg.norm(got - o), lim)
 
 
 def _run(bt, H, tree=None, seed=1, wide=0, scale=None, std=1.0):
@@ -131,6 +142,10 @@ def test_long_prompt_and_many_items():
             o = p @ v[:, h // 4]
             within(f64(out)[first: first + n, h], o,
                    BF16 * np.abs(o) + (BF16 + 2.0 ** -11) * (p @ np.abs(v[:, h // 4])), "out")
+            # a row of 128 elements on its own: three times its expectation
+            lim = np.linalg.norm(np.hypot(np.sqrt(p ** 2 @ v[:, h // 4] ** 2), o), axis=1)
+            err = np.linalg.norm(f64(out)[first: first + n, h] - o, axis=1)
+            assert (err <= 3 * BF16 / math.sqrt(3) * lim).all()
             within(f64(lse)[first: first + n, h], (m + np.log(l))[:, 0], 2.0 ** -12, "lse")
 
 

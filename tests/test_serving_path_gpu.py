@@ -43,7 +43,7 @@ def test_verification_steps():
         qkv = randn(g, N, (H + 2 * H_kv) * D).to(DEV)
         q = ops.stt_kv_append(qkv, H, kc, vc, cu, ln, table, None, freq, w, w)
         out, lse = ops.stt_paged_attn(q, kc, vc, cu, ln, table)
-        o, l, mag = opg.attention(f64(q), f64(kc), f64(vc), cu.tolist(), lens,
+        o, l, mag, _ = opg.attention(f64(q), f64(kc), f64(vc), cu.tolist(), lens,
                                   table.cpu().numpy(), 1 / math.sqrt(D))
         within(out, o, BF16 * np.abs(o) + (BF16 + 2.0 ** -11) * mag, "out")
         within(lse, l, 2.0 ** -12, "lse")
