@@ -132,7 +132,7 @@ def _declare(L):
     L.stt_verify.restype = i32
     L.soft_ce_fwd_bwd_inplace_noalloc.argtypes = [vp, vp, vp, i64, i64, vp, vp, vp]
     L.soft_ce_fwd_bwd_inplace_noalloc.restype = i32
-    rope, pages = c.POINTER(Rope), c.POINTER(Pages)
+    rope = pages = logits = vp  # structs: a byref() or their packed bytes
     L.stt_qkv_rope_fwd.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, rope, vp, vp, vp, vp]
     L.stt_qkv_rope_fwd.restype = i32
     L.stt_qkv_rope_bwd_workspace_size.argtypes = [i32]
@@ -146,7 +146,7 @@ def _declare(L):
     L.stt_paged_attn_workspace_size.restype = sz
     L.stt_paged_attn.argtypes = [vp, i64, i64, i32, pages, f32, vp, i32, vp, vp, vp, sz, vp]
     L.stt_paged_attn.restype = i32
-    L.stt_logits_process.argtypes = [vp, i64, i64, i32, c.POINTER(Logits), c.c_uint32, vp, vp]
+    L.stt_logits_process.argtypes = [vp, i64, i64, i32, logits, c.c_uint32, vp, vp]
     L.stt_logits_process.restype = i32
     L.stt_profile_start.argtypes = [i32]
     L.stt_profile_start.restype = i32
@@ -170,6 +170,8 @@ def load(path: str):
 def lib():
     """The in-tree library, loaded once.  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             _lib = load(LIB_PATH)

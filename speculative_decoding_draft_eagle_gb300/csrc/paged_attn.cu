@@ -27,6 +27,7 @@
 //   warp 11    value pages (TMA).
 // Barrier phases count S products, stage uses and units over the CTA's whole share.
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/stt.h"
 #include "attn_common.cuh"
@@ -762,9 +763,16 @@ cudaError_t launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s) 
   P.d_tok = place[0];
   P.d_head = place[1];
   P.d_page = place[2];
-  e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Smem<D>::alloc);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> raised{0};  // devices whose limit is raised, the first 64
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D>::alloc);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   const unsigned grid = (unsigned)std::min(sm_count(), kMaxCtas);
   prof_before(s, STT_KERNEL_PAGED_ATTN);
   paged_attn_kernel<D><<<grid, kThreads, Smem<D>::alloc, s>>>(P, tmQ, tmK, tmV);

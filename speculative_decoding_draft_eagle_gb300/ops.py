@@ -9,11 +9,12 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from ._lib import Logits, Pages, Rope, check, lib
+from ._lib import check, lib
 
 __all__ = [
     "stt_attn_fwd",
@@ -371,19 +372,71 @@ def stt_verify(p_target: torch.Tensor, p_draft: torch.Tensor, draft_tokens: torc
     return n_accepted, out_tokens
 
 
-def _check_devices(*ts: Optional[torch.Tensor]):
-    """The library launches on the current device: every tensor must live there."""
+# The operators around the paged cache are called once per layer and token, so
+# their checks take one short path for a good argument and explain only a bad one.
+# The structs of the C ABI are packed as bytes.
+_ROPE = struct.Struct("@PPPiIff")
+_PAGES = struct.Struct("@PPPPPqqqiiiiii")
+_LOGITS = struct.Struct("@PPPPPPPPPPii")
+
+
+def _current(stream):
+    """The current device, and the raw stream the call goes to."""
     dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _own(stream, *ts: Optional[torch.Tensor]):
+def _refuse(t, name, dtype, shape, dev):
+    """Raises what is wrong with a tensor argument."""
+    _need(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} is not a usable tensor")
+
+
+def _arg(t, name, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of that type and shape on the current device."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _rows(t, name, shape, dev):
+    """Address of bf16 rows (the last dimension) that are dense but for the distance
+    between them, and that distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    width = shape[-1]
+    if t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != shape:
+        if t.dtype is not torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    stride = t.stride()
+    three = len(shape) == 3 and shape[0] > 1
+    ld = stride[-2] if shape[-2] > 1 else (stride[0] if three else width)
+    if ((width > 1 and stride[-1] != 1) or ld < width or
+            (three and stride[0] != shape[1] * ld)):
+        raise ValueError(f"{name} must be dense apart from the distance between its rows")
+    return t.data_ptr(), ld
+
+
+def _new(shape, dtype, dev):
+    return torch.empty(shape, device=torch.device("cuda", dev), dtype=dtype)
+
+
+def _keep(stream, *ts):
     """Tensors allocated here (on the current stream) and used on `stream`: their
     memory is not handed out again before that stream is done with them."""
-    if stream is None:
-        return
     if not isinstance(stream, torch.cuda.Stream):
         if int(stream) == 0:
             stream = torch.cuda.default_stream()
@@ -392,28 +445,6 @@ def _own(stream, *ts: Optional[torch.Tensor]):
     for t in ts:
         if t is not None:
             t.record_stream(stream)
-
-
-def _need_rows(t: torch.Tensor, name: str, width: int, dims: int):
-    """bf16 rows `width` wide, dense but for the distance between rows; returns it."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != dims or t.shape[-1] != width:
-        raise ValueError(f"{name} must have {dims} dimensions, the last of size {width}, "
-                         f"got {tuple(t.shape)}")
-    ld = width
-    if t.shape[-2] > 1:
-        ld = t.stride(-2)
-    elif dims == 3 and t.shape[0] > 1:
-        ld = t.stride(0)
-    if t.numel() and ((width > 1 and t.stride(-1) != 1) or ld < width or
-                      (dims == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld)):
-        raise ValueError(f"{name} must be dense apart from the distance between its rows")
-    return ld
 
 
 def rope_frequencies(R: int, base: float = 10000.0, factor: float = 1.0,
@@ -440,23 +471,21 @@ def rope_frequencies(R: int, base: float = 10000.0, factor: float = 1.0,
     return (f * keep + f / factor * (1 - keep)).to(device)
 
 
-def _rope(freq, w_q, w_k, D, eps, interleaved, amplitude) -> Rope:
-    R = 0
-    if freq is not None:
-        if freq.dim() != 1:
-            raise ValueError("freq must be [R/2]")
-        _need(freq, "freq", torch.float64)
-        R = 2 * freq.numel()
-    for name, w in (("w_q", w_q), ("w_k", w_k)):
-        if w is not None:
-            _need(w, name, torch.bfloat16, (D,))
-    return Rope(freq=_ptr(freq) if R else None, w_q=_ptr(w_q), w_k=_ptr(w_k), R=R,
-                flags=STT_ROPE_INTERLEAVED if interleaved else 0, amplitude=float(amplitude),
-                eps=float(eps))
-
-
 STT_ROPE_INTERLEAVED = 0x1
 STT_ROPE_BF16_GRADS = 0x2
+
+
+def _rope(freq, w_q, w_k, D, eps, interleaved, amplitude, dev) -> bytes:
+    R, f = 0, 0
+    if freq is not None:
+        if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+            raise ValueError("freq must be [R/2]")
+        f = _arg(freq, "freq", torch.float64, freq.shape, dev)
+        R = 2 * freq.numel()
+    return _ROPE.pack(
+        f if R else 0, 0 if w_q is None else _arg(w_q, "w_q", torch.bfloat16, (D,), dev),
+        0 if w_k is None else _arg(w_k, "w_k", torch.bfloat16, (D,), dev), R,
+        STT_ROPE_INTERLEAVED if interleaved else 0, amplitude, eps)
 
 
 def stt_qkv_rope_fwd(qkv: torch.Tensor, H: int, H_kv: int, D: int,
@@ -471,26 +500,28 @@ def stt_qkv_rope_fwd(qkv: torch.Tensor, H: int, H_kv: int, D: int,
     every query and key head with the weights w_q, w_k bf16 [D] (None: no norm), and
     rotation of each head's first 2 len(freq) elements by positions int32 [B, S]
     (None: 0..S-1) times freq (fp64 radians per position, see rope_frequencies)."""
-    ld = _need_rows(qkv, "qkv", (H + 2 * H_kv) * D, 3)
-    B, S = qkv.shape[:2]
-    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude)
-    if positions is not None:
-        _need(positions, "positions", torch.int32, (B, S))
-    fresh = []
-    outs = []
-    for name, t, h in (("q", q, H), ("k", k, H_kv), ("v", v, H_kv)):
-        if t is None:
-            t = torch.empty((B, h, S, D), device=qkv.device, dtype=torch.bfloat16)
-            fresh.append(t)
-        _need(t, name, torch.bfloat16, (B, h, S, D))
-        outs.append(t)
-    _check_devices(qkv, positions, freq, w_q, w_k, *outs)
-    st = lib().stt_qkv_rope_fwd(_ptr(qkv), ld, _ptr(positions), B, S, H, H_kv, D,
-                                ctypes.byref(rope), _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]),
-                                _stream(stream))
-    check("stt_qkv_rope_fwd", st)
-    _own(stream, *fresh)
-    return tuple(outs)
+    dev, raw = _current(stream)
+    if qkv.dim() != 3:
+        raise ValueError("qkv must be [B, S, (H + 2 H_kv) D]")
+    B, S, _ = qkv.shape
+    x, ld = _rows(qkv, "qkv", (B, S, (H + 2 * H_kv) * D), dev)
+    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude, dev)
+    bf16 = torch.bfloat16
+    if q is None:
+        q = _new((B, H, S, D), bf16, dev)
+    if k is None:
+        k = _new((B, H_kv, S, D), bf16, dev)
+    if v is None:
+        v = _new((B, H_kv, S, D), bf16, dev)
+    st = lib().stt_qkv_rope_fwd(
+        x, ld, None if positions is None else _arg(positions, "positions", torch.int32, (B, S), dev),
+        B, S, H, H_kv, D, rope, _arg(q, "q", bf16, (B, H, S, D), dev),
+        _arg(k, "k", bf16, (B, H_kv, S, D), dev), _arg(v, "v", bf16, (B, H_kv, S, D), dev), raw)
+    if st:
+        check("stt_qkv_rope_fwd", st)
+    if stream is not None:
+        _keep(stream, q, k, v)
+    return q, k, v
 
 
 def stt_qkv_rope_bwd_workspace_size(D: int) -> int:
@@ -509,85 +540,81 @@ def stt_qkv_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
     """Gradient of stt_qkv_rope_fwd from dq, dk, dv (all fp32 or all bf16, in the
     layout of q, k, v).  qkv is needed where a weight is given.  Returns (dqkv bf16
     [B, S, (H + 2 H_kv) D], dw_q, dw_k fp32 [D] or None)."""
+    dev, raw = _current(stream)
     if dq.dim() != 4 or dk.dim() != 4:
         raise ValueError("dq must be [B, H, S, D] and dk, dv [B, H_kv, S, D]")
     B, H, S, D = dq.shape
     H_kv = dk.shape[1]
-    if dq.dtype not in (torch.float32, torch.bfloat16):
+    t = dq.dtype
+    if t is not torch.float32 and t is not torch.bfloat16:
         raise ValueError("dq must be float32 or bfloat16")
-    _need(dq, "dq", dq.dtype)
-    _need(dk, "dk", dq.dtype, (B, H_kv, S, D))
-    _need(dv, "dv", dq.dtype, (B, H_kv, S, D))
     C = (H + 2 * H_kv) * D
-    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude)
+    p_dq = _arg(dq, "dq", t, (B, H, S, D), dev)
+    p_dk = _arg(dk, "dk", t, (B, H_kv, S, D), dev)
+    p_dv = _arg(dv, "dv", t, (B, H_kv, S, D), dev)
+    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude, dev)
     norm = w_q is not None or w_k is not None
-    ld = C
-    if qkv is not None:
-        ld = _need_rows(qkv, "qkv", C, 3)
-        if tuple(qkv.shape[:2]) != (B, S):
-            raise ValueError(f"qkv must have shape {(B, S, C)}, got {tuple(qkv.shape)}")
-    elif norm:
-        raise ValueError("qkv is needed for the gradient of the norm")
-    if positions is not None:
-        _need(positions, "positions", torch.int32, (B, S))
-    fresh = []
-
-    def out(t, name, shape, dtype):
-        if t is None:
-            t = torch.empty(shape, device=dq.device, dtype=dtype)
-            fresh.append(t)
-        return t
-
-    dqkv = out(dqkv, "dqkv", (B, S, C), torch.bfloat16)
-    ld_d = _need_rows(dqkv, "dqkv", C, 3)
-    if tuple(dqkv.shape[:2]) != (B, S):
-        raise ValueError(f"dqkv must have shape {(B, S, C)}, got {tuple(dqkv.shape)}")
+    x, ld = None, C
+    if norm:
+        if qkv is None:
+            raise ValueError("qkv is needed for the gradient of the norm")
+        x, ld = _rows(qkv, "qkv", (B, S, C), dev)
+    if dqkv is None:
+        dqkv = _new((B, S, C), torch.bfloat16, dev)
+    p_d, ld_d = _rows(dqkv, "dqkv", (B, S, C), dev)
+    p_wq = p_wk = p_ws = None
+    n_ws = 0
     if (dw_q is not None and w_q is None) or (dw_k is not None and w_k is None):
         raise ValueError("a weight's gradient is asked for without the weight")
     if w_q is not None:
-        dw_q = out(dw_q, "dw_q", (D,), torch.float32)
-        _need(dw_q, "dw_q", torch.float32, (D,))
+        if dw_q is None:
+            dw_q = _new((D,), torch.float32, dev)
+        p_wq = _arg(dw_q, "dw_q", torch.float32, (D,), dev)
     if w_k is not None:
-        dw_k = out(dw_k, "dw_k", (D,), torch.float32)
-        _need(dw_k, "dw_k", torch.float32, (D,))
-    if norm and workspace is None:
-        workspace = out(None, "workspace", (stt_qkv_rope_bwd_workspace_size(D),), torch.uint8)
-    _check_devices(dq, dk, dv, qkv, positions, freq, w_q, w_k, dqkv, dw_q, dw_k, workspace)
+        if dw_k is None:
+            dw_k = _new((D,), torch.float32, dev)
+        p_wk = _arg(dw_k, "dw_k", torch.float32, (D,), dev)
+    if norm:
+        if workspace is None:
+            workspace = _new((stt_qkv_rope_bwd_workspace_size(D),), torch.uint8, dev)
+        p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        n_ws = workspace.numel() * workspace.element_size()
     st = lib().stt_qkv_rope_bwd(
-        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(qkv) if norm else None, ld, _ptr(positions), B, S, H,
-        H_kv, D, ctypes.byref(rope), STT_ROPE_BF16_GRADS if dq.dtype == torch.bfloat16 else 0,
-        _ptr(dqkv), ld_d, _ptr(dw_q), _ptr(dw_k), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(stream))
-    check("stt_qkv_rope_bwd", st)
-    _own(stream, *fresh)
+        p_dq, p_dk, p_dv, x, ld,
+        None if positions is None else _arg(positions, "positions", torch.int32, (B, S), dev),
+        B, S, H, H_kv, D, rope, STT_ROPE_BF16_GRADS if t is torch.bfloat16 else 0, p_d, ld_d, p_wq,
+        p_wk, p_ws, n_ws, raw)
+    if st:
+        check("stt_qkv_rope_bwd", st)
+    if stream is not None:
+        _keep(stream, dqkv, dw_q, dw_k, workspace)
     return dqkv, dw_q, dw_k
 
 
-def _pages(k_cache, v_cache, cu_q, seq_lens, page_table) -> Pages:
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != torch.bfloat16 or t.dim() != 4:
-            raise ValueError(f"{name} must be bfloat16 [num_pages, H_kv, page_size, D]")
-        if t.numel() and t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+def _pages(k_cache, v_cache, cu_q, seq_lens, page_table, dev):
+    """The packed stt_pages, and H_kv, D and B."""
+    bf16 = torch.bfloat16
+    if (k_cache.dtype is not bf16 or v_cache.dtype is not bf16 or k_cache.dim() != 4
+            or k_cache.get_device() != dev or v_cache.get_device() != dev):
+        raise ValueError("k_cache and v_cache must be bfloat16 [num_pages, H_kv, page_size, D] "
+                         f"on cuda:{dev}")
+    stride = k_cache.stride()
+    n, H_kv, page, D = shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if stride[3] != 1 and D > 1 and k_cache.numel():
+        raise ValueError("the elements of a cached head must be contiguous")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, max_pages = page_table.shape
-    _need(page_table, "page_table", torch.int32)
-    _need(cu_q, "cu_q", torch.int32, (B + 1,))
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
-    n, H_kv, page, D = k_cache.shape
-    # A dimension of one element has no stride of its own.
-    stride = [s if size > 1 else max(8, (D + 7) // 8 * 8)
-              for s, size in zip(k_cache.stride(), k_cache.shape)]
-    return Pages(k=_ptr(k_cache), v=_ptr(v_cache), table=_ptr(page_table), cu_q=_ptr(cu_q),
-                 seq_lens=_ptr(seq_lens), stride_page=stride[0], stride_head=stride[1],
-                 stride_tok=stride[2], B=B, H_kv=H_kv, D=D, page_size=page, num_pages=n,
-                 max_pages=max_pages)
+    if n == 1 or H_kv == 1 or page == 1:  # a dimension of one element has no stride of its own
+        stride = [s if size > 1 else max(8, (D + 7) // 8 * 8) for s, size in zip(stride, shape)]
+    return _PAGES.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(),
+        _arg(page_table, "page_table", torch.int32, (B, max_pages), dev),
+        _arg(cu_q, "cu_q", torch.int32, (B + 1,), dev),
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), stride[0], stride[1], stride[2], B,
+        H_kv, D, page, n, max_pages), H_kv, D, B
 
 
 def stt_kv_append(qkv: torch.Tensor, H: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -604,22 +631,22 @@ def stt_kv_append(qkv: torch.Tensor, H: int, k_cache: torch.Tensor, v_cache: tor
     its transpose).  Norm and rotation as stt_qkv_rope_fwd, at positions int32 [N]
     (None: the key's index).  Returns the queries bf16 [N, H, D]; rows behind the
     last sequence are left as they are."""
-    pages = _pages(k_cache, v_cache, cu_q, seq_lens, page_table)
-    D = pages.D
-    ld = _need_rows(qkv, "qkv", (H + 2 * pages.H_kv) * D, 2)
+    dev, raw = _current(stream)
+    pages, H_kv, D, _ = _pages(k_cache, v_cache, cu_q, seq_lens, page_table, dev)
+    if qkv.dim() != 2:
+        raise ValueError("qkv must be [N, (H + 2 H_kv) D]")
     N = qkv.shape[0]
-    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude)
-    if positions is not None:
-        _need(positions, "positions", torch.int32, (N,))
-    fresh = None
+    x, ld = _rows(qkv, "qkv", (N, (H + 2 * H_kv) * D), dev)
+    rope = _rope(freq, w_q, w_k, D, eps, interleaved, amplitude, dev)
     if q is None:
-        q = fresh = torch.empty((N, H, D), device=qkv.device, dtype=torch.bfloat16)
-    _need(q, "q", torch.bfloat16, (N, H, D))
-    _check_devices(qkv, k_cache, v_cache, cu_q, seq_lens, page_table, positions, freq, w_q, w_k, q)
-    st = lib().stt_kv_append(_ptr(qkv), ld, _ptr(positions), N, H, ctypes.byref(pages),
-                             ctypes.byref(rope), _ptr(q), _stream(stream))
-    check("stt_kv_append", st)
-    _own(stream, fresh)
+        q = _new((N, H, D), torch.bfloat16, dev)
+    st = lib().stt_kv_append(
+        x, ld, None if positions is None else _arg(positions, "positions", torch.int32, (N,), dev),
+        N, H, pages, rope, _arg(q, "q", torch.bfloat16, (N, H, D), dev), raw)
+    if st:
+        check("stt_kv_append", st)
+    if stream is not None:
+        _keep(stream, q)
     return q
 
 
@@ -640,42 +667,41 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     and new token j iff bit j % 32 of word j / 32 of its row is set.
     Returns (out bf16 [N, H, D], lse fp32 [N, H]); rows behind the last sequence are
     left as they are."""
-    pages = _pages(k_cache, v_cache, cu_q, seq_lens, page_table)
-    if q.dim() != 3 or q.shape[2] != pages.D:
-        raise ValueError(f"q must be [N, H, {pages.D}]")
-    N, H, D = q.shape
-    if q.numel() and H > 1 and q.stride(1) != D:
-        raise ValueError("q must be dense apart from the distance between its rows")
-    ld = _need_rows(q.flatten(1) if q.is_contiguous() else
-                    q.as_strided((N, H * D), (q.stride(0), q.stride(2))), "q", H * D, 2)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    words = 0
+    dev, raw = _current(stream)
+    pages, H_kv, D, B = _pages(k_cache, v_cache, cu_q, seq_lens, page_table, dev)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype is not torch.bfloat16 or q.get_device() != dev:
+        raise ValueError(f"q must be bfloat16 [N, H, {D}] on cuda:{dev}")
+    N, H, _ = q.shape
+    ld = H * D
+    if not q.is_contiguous():
+        s = q.stride()
+        if s[2] != 1 or (H > 1 and s[1] != D) or (N > 1 and s[0] < ld):
+            raise ValueError("q must be dense apart from the distance between its rows")
+        if N > 1:
+            ld = s[0]
+    words, tree = 0, None
     if tree_mask is not None:
         if tree_mask.dim() != 2:
             raise ValueError("tree_mask must be [N, words]")
         words = tree_mask.shape[1]
-        _need(tree_mask, "tree_mask", torch.int32, (N, words))
-    fresh = []
-
-    def new(shape, dtype):
-        fresh.append(torch.empty(shape, device=q.device, dtype=dtype))
-        return fresh[-1]
-
+        tree = _arg(tree_mask, "tree_mask", torch.int32, (N, words), dev)
     if out is None:
-        out = new((N, H, D), torch.bfloat16)
+        out = _new((N, H, D), torch.bfloat16, dev)
     if lse is None:
-        lse = new((N, H), torch.float32)
-    _need(out, "out", torch.bfloat16, (N, H, D))
-    _need(lse, "lse", torch.float32, (N, H))
+        lse = _new((N, H), torch.float32, dev)
+    L = lib()
     if workspace is None:
-        workspace = new((stt_paged_attn_workspace_size(N, pages.B, H, pages.H_kv, D),),
-                        torch.uint8)
-    _check_devices(q, k_cache, v_cache, cu_q, seq_lens, page_table, tree_mask, out, lse, workspace)
-    st = lib().stt_paged_attn(_ptr(q), ld, N, H, ctypes.byref(pages), scale, _ptr(tree_mask),
-                              words, _ptr(out), _ptr(lse), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
-    check("stt_paged_attn", st)
-    _own(stream, *fresh)
+        workspace = _new((L.stt_paged_attn_workspace_size(N, B, H, H_kv, D),), torch.uint8, dev)
+    st = L.stt_paged_attn(
+        q.data_ptr(), ld, N, H, pages, D ** -0.5 if scale is None else scale, tree, words,
+        _arg(out, "out", torch.bfloat16, (N, H, D), dev),
+        _arg(lse, "lse", torch.float32, (N, H), dev),
+        _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+        workspace.numel() * workspace.element_size(), raw)
+    if st:
+        check("stt_paged_attn", st)
+    if stream is not None:
+        _keep(stream, out, lse, workspace)
     return out, lse
 
 
@@ -706,63 +732,60 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
     draft_tokens int32 [B, >= rows - 1].  bias fp32 [V], [1, V] or [B, V]; mask int32
     [N, ceil(V / 32)], bit v % 32 of word v / 32 set where v is allowed.  out may be z
     itself where that is fp32."""
+    dev, on = _current(stream)
     if z.dim() != 2:
         raise ValueError("z must be [N, V]")
     N, V = z.shape
-    if z.dtype not in (torch.float32, torch.bfloat16):
+    t, i32, f32 = z.dtype, torch.int32, torch.float32
+    if t is not f32 and t is not torch.bfloat16:
         raise ValueError("z must be float32 or bfloat16")
-    _need(z, "z", z.dtype)
+    p_z = _arg(z, "z", t, (N, V), dev)
     if rows < 1 or N % rows:
         raise ValueError("rows must be positive and divide N")
     B = N // rows
-    for name, t in (("temperature", temperature), ("repetition", repetition),
-                    ("frequency", frequency), ("presence", presence)):
-        if t is not None:
-            _need(t, name, torch.float32, (B,))
+    of = (B,)
+    p_t = 0 if temperature is None else _arg(temperature, "temperature", f32, of, dev)
+    p_r = 0 if repetition is None else _arg(repetition, "repetition", f32, of, dev)
+    p_f = 0 if frequency is None else _arg(frequency, "frequency", f32, of, dev)
+    p_p = 0 if presence is None else _arg(presence, "presence", f32, of, dev)
     if (tokens is None) != (cu_tokens is None):
         raise ValueError("tokens and cu_tokens go together")
+    p_tok = p_cu = p_np = p_dr = p_b = p_m = draft_ld = bias_rows = 0
     if tokens is not None:
         if tokens.dim() != 1:
             raise ValueError("tokens must be [total]")
-        _need(tokens, "tokens", torch.int32)
-        _need(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+        p_tok = _arg(tokens, "tokens", i32, tokens.shape, dev)
+        p_cu = _arg(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
     if n_prompt is not None:
         if tokens is None:
             raise ValueError("n_prompt is given without tokens")
-        _need(n_prompt, "n_prompt", torch.int32, (B,))
-    draft_ld = 0
+        p_np = _arg(n_prompt, "n_prompt", i32, of, dev)
+    if tokens is not None and tokens.numel() == 0:  # an empty history has no address
+        p_tok = p_cu = p_np = 0
     if draft_tokens is not None:
         if draft_tokens.dim() != 2 or draft_tokens.shape[1] < rows - 1:
             raise ValueError(f"draft_tokens must be [B, at least {rows - 1}]")
         draft_ld = draft_tokens.shape[1]
-        _need(draft_tokens, "draft_tokens", torch.int32, (B, draft_ld))
-    bias_rows = 0
+        p_dr = _arg(draft_tokens, "draft_tokens", i32, (B, draft_ld), dev) if draft_ld else 0
     if bias is not None:
         bias_rows = 1 if bias.dim() == 1 else bias.shape[0]
-        if bias_rows not in (1, B):
+        if bias_rows != 1 and bias_rows != B:
             raise ValueError("bias must be [V], [1, V] or [B, V]")
-        _need(bias, "bias", torch.float32, (V,) if bias.dim() == 1 else (bias_rows, V))
+        p_b = _arg(bias, "bias", f32, (V,) if bias.dim() == 1 else (bias_rows, V), dev)
     if mask is not None:
-        _need(mask, "mask", torch.int32, (N, (V + 31) // 32))
-    fresh = None
+        p_m = _arg(mask, "mask", i32, (N, (V + 31) // 32), dev)
     if out is None:
-        out = fresh = torch.empty((N, V), device=z.device, dtype=torch.float32)
-    _need(out, "out", torch.float32, (N, V))
-    _check_devices(z, temperature, repetition, frequency, presence, tokens, cu_tokens, n_prompt,
-                   draft_tokens, bias, mask, out)
-    # An empty history has no address.
-    has = tokens is not None and tokens.numel() > 0
-    p = Logits(temperature=_ptr(temperature), repetition=_ptr(repetition),
-               frequency=_ptr(frequency), presence=_ptr(presence),
-               tokens=_ptr(tokens) if has else None, cu_tokens=_ptr(cu_tokens) if has else None,
-               n_prompt=_ptr(n_prompt) if has else None,
-               draft=_ptr(draft_tokens) if draft_ld else None, bias=_ptr(bias), mask=_ptr(mask),
-               draft_ld=draft_ld, bias_rows=bias_rows)
-    flags = (STT_LOGITS_BF16 if z.dtype == torch.bfloat16 else 0) | (STT_LOGITS_RAW if raw else 0)
-    st = lib().stt_logits_process(_ptr(z), N, V, rows, ctypes.byref(p), flags, _ptr(out),
-                                  _stream(stream))
-    check("stt_logits_process", st)
-    _own(stream, fresh)
+        out = _new((N, V), f32, dev)
+    params = _LOGITS.pack(p_t, p_r, p_f, p_p, p_tok, p_cu, p_np, p_dr, p_b, p_m, draft_ld,
+                          bias_rows)
+    st = lib().stt_logits_process(
+        p_z, N, V, rows, params,
+        (STT_LOGITS_BF16 if t is torch.bfloat16 else 0) | (STT_LOGITS_RAW if raw else 0),
+        _arg(out, "out", f32, (N, V), dev), on)
+    if st:
+        check("stt_logits_process", st)
+    if stream is not None:
+        _keep(stream, out)
     return out
 
 
