@@ -527,7 +527,8 @@ STT_API int stt_paged_attn(const void* q, int64_t ld_q, int64_t N, int H, const 
  *           largest z (the lowest such v) and 0 elsewhere.  temperature >= 0 and
  *           repetition > 0 are the caller's to see to.
  *  tokens, cu_tokens, n_prompt  int32; all NULL without a history (n_prompt
- *           NULL alone: no prompt).
+ *           NULL alone: no prompt).  n_tokens: length of tokens, past which
+ *           nothing is read.
  *  draft    int32 [N / rows, draft_ld] or NULL; draft_ld >= rows - 1.
  *  bias     fp32 [bias_rows, V]; bias_rows 0 (none), 1, or N / rows.
  *  mask     uint32 [N, ceil(V / 32)] or NULL: bit v % 32 of word v / 32 set iff
@@ -550,6 +551,7 @@ typedef struct {
   const int32_t* draft;
   const float* bias;
   const uint32_t* mask;
+  int n_tokens;
   int draft_ld;
   int bias_rows;
 } stt_logits;
@@ -600,9 +602,10 @@ STT_API const char* stt_kernel_name(int kernel_id);
 #define STT_DEVERR_LM_WAIT 0x10u
 #define STT_DEVERR_PAGE 0x20u /* a page or key slot out of range, skipped */
 #define STT_DEVERR_PAGED_WAIT 0x40u
+#define STT_DEVERR_LOGITS_WAIT 0x80u
 #define STT_DEVERR_WAIT_MASK                                                           \
   (STT_DEVERR_FWD_WAIT | STT_DEVERR_BWD_WAIT | STT_DEVERR_CE_WAIT | STT_DEVERR_LM_WAIT | \
-   STT_DEVERR_PAGED_WAIT)
+   STT_DEVERR_PAGED_WAIT | STT_DEVERR_LOGITS_WAIT)
 
 #ifdef __cplusplus
 }

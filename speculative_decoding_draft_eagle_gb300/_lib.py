@@ -75,7 +75,7 @@ class Logits(ctypes.Structure):
     """stt_logits."""
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "temperature", "repetition", "frequency", "presence", "tokens", "cu_tokens", "n_prompt",
-        "draft", "bias", "mask")] + [("draft_ld", ctypes.c_int), ("bias_rows", ctypes.c_int)]
+        "draft", "bias", "mask")] + [(n, ctypes.c_int) for n in ("n_tokens", "draft_ld", "bias_rows")]
 
 
 _lock = threading.Lock()

@@ -152,7 +152,7 @@ struct LogitsArgs {
   const int32_t *tokens, *cu_tokens, *n_prompt, *draft;
   const float* bias;
   const uint32_t* mask;
-  int draft_ld, bias_rows;
+  int draft_ld, bias_rows, n_tokens;
   float* out;
 };
 constexpr int64_t kLogitsMaxV = 16 * 24576;
@@ -161,6 +161,7 @@ cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s);
 // Per-file device error words (read and cleared).
 cudaError_t qkv_rope_error_word(uint32_t* w);
 cudaError_t paged_attn_error_word(uint32_t* w);
+cudaError_t logits_error_word(uint32_t* w);
 cudaError_t soft_ce_error_word(uint32_t* w);
 cudaError_t attn_fwd_error_word(uint32_t* w);
 cudaError_t attn_bwd_error_word(uint32_t* w);
@@ -169,6 +170,7 @@ cudaError_t soft_ce_set_wait_budget(uint64_t ns);
 cudaError_t attn_fwd_set_wait_budget(uint64_t ns);
 cudaError_t attn_bwd_set_wait_budget(uint64_t ns);
 cudaError_t paged_attn_set_wait_budget(uint64_t ns);
+cudaError_t logits_set_wait_budget(uint64_t ns);
 
 // Streaming multiprocessors of the current device (cached per device; 1 if
 // the query fails, which only shrinks persistent grids).

@@ -2,34 +2,55 @@
 // against: penalties for repeated tokens, bias, grammar mask, temperature,
 // softmax.
 //
-// A cluster of C CTAs takes a row, each a slice of the vocabulary, and reads it
-// once: the slice stays in registers from the load to the store.  While the loads
-// are under way the CTA counts the row's history over its slice in shared memory
-// (whole numbers, so the order of the atomics does not matter; every CTA scans the
-// whole history, which is short against the row).  Each thread then applies
-// penalties, bias and mask to its elements, the CTA takes its maximum m and its
-// sum l of e^(y - m), the C pairs are exchanged through distributed shared memory
-// (one cluster barrier), and the exponentials leave scaled by e^(m - M) / L.  A
-// greedy row exchanges the largest value and then the lowest index that has it.
-// Bounded by HBM: 2 or 4 bytes read and 4 written per logit.
+// A cluster of C CTAs takes up to eight consecutive rows of a sequence, each CTA
+// every C-th block of 2048 logits (tokens crowd at the low end of a vocabulary, and
+// contiguous slices would leave most of the history to one CTA).  It counts the
+// sequence's history over its blocks in shared memory (whole numbers: the atomics'
+// order does not matter), goes over its elements for each row's maximum m and sum l
+// of e^(y - m), exchanges the pairs of all its rows with the other CTAs at once, and
+// goes over its elements again to write e^(y - M) / L.  The second reading comes from
+// L2: HBM sees 2 or 4 bytes read and 4 written per logit.  320 bf16 rows of 151936
+// with histories, bias and mask take 141 us, 69 us without them; what bounds both is
+// the issue of instructions (87 and 34 million), not HBM (44 us).  Keeping a row in
+// registers between the two passes halves the loads but left fewer warps to cover
+// the exchange: 136 to 205 us, with one row in flight, two, or a ring of bulk copies.
+//
+// The tokens that occur in the history are few against the vocabulary.  A bit map
+// holds the ones seen; a seen token's rank in it, from the running sum of its words'
+// bit counts, is the place of its count, so the counts take 8 KB and not 4 bytes a
+// logit, which would keep CTAs off the SM.  The passes over the elements take seen
+// and forbidden ones out with one bit each, and the seen ones are done apart, with
+// their penalties, a window of 2048 ranks at a time.
+//
+// The pairs go to the other CTAs by st.async, which signals an mbarrier there.  A
+// greedy row's pair is its largest value and the lowest index that has it.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/stt.h"
-#include "internal.h"
-#include "ptx.cuh"
+#include "attn_common.cuh"
 
 namespace stt {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kMaxNv = 6;                  // 8-element chunks a thread holds at most
+constexpr int kMaxRows = 8;             // rows a cluster takes together
+constexpr int kBlock = 8 * kThreads;    // consecutive logits of a CTA
+constexpr int kBlocksMax = 10;          // blocks of a CTA at most, where C allows
+constexpr int kCtasPerSm = 4;           // by registers
+constexpr int kFill = 16;               // CTAs an SM before rows are taken together
+constexpr int kWindow = 2048;           // seen tokens counted at a time
 constexpr uint32_t kPrompt = 0x80000000u;  // the token is in the prompt
 constexpr float kLog2E = 1.4426950408889634f;
 
 struct Params {
   LogitsArgs a;
-  int C, slice;  // CTAs per row, elements per CTA (a multiple of 8)
+  int C, log_c;            // CTAs per row (a power of two)
+  int groups, group_rows;  // row groups of a sequence, rows of a group
+  int words;               // of the bit map
 };
 
 // A logit after the penalties, each step rounded as written.
@@ -45,10 +66,6 @@ struct Penalty {
   }
 };
 
-__device__ __forceinline__ void st_cluster_f2(uint32_t addr, float a, float b) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
-}
-
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -60,310 +77,484 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// VEC: rows 16-byte aligned, a thread's chunk is 8 consecutive elements (vector
-// loads and stores); else its elements are a block apart (any alignment).
-template <class T, bool VEC, int NV>
-__global__ void __launch_bounds__(kMaxThreads, NV <= 5 ? 2 : 1)
-    logits_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) uint32_t count[];
-  __shared__ float s_red[kMaxThreads / 32];
-  __shared__ int s_idx[kMaxThreads / 32];
-  __shared__ __align__(16) float2 s_pair[kMaxCluster];
-  const LogitsArgs& A = P.a;
-  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5;
-  const int rank = (int)(blockIdx.x % (unsigned)P.C), r = (int)(blockIdx.x / (unsigned)P.C);
-  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to a neighbour
-  const int b = r / A.rows, i = r - b * A.rows;
-  const int begin = rank * P.slice, len = min(P.slice, A.V - begin);
-  const T* z = static_cast<const T*>(A.z) + (int64_t)r * A.V + begin;
-
-  // Element e of chunk k, relative to the slice.
-  auto at = [&](int k, int e) { return VEC ? (k * nt + tid) * 8 + e : (k * 8 + e) * nt + tid; };
-
-  float x[NV][8];
-  uint4 raw[NV];  // bf16 chunks as loaded
-  if constexpr (VEC) {
+// Four elements as loaded.  Four, because a warp then stores whole lines: with eight
+// to a thread its 16-byte stores cover half of every sector they touch.  A thread
+// takes two such chunks, kApart elements apart, at a time.
+constexpr int kChunk = 4;
+constexpr int kApart = kThreads * kChunk;
+constexpr uint32_t kNibble = (1u << kChunk) - 1u;
+template <int bytes> struct RawChunk { using type = uint4; };
+template <> struct RawChunk<2> { using type = uint2; };
+__device__ __forceinline__ void unpack(const uint4& r, float* x) {
+  x[0] = __uint_as_float(r.x);
+  x[1] = __uint_as_float(r.y);
+  x[2] = __uint_as_float(r.z);
+  x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(const uint2& r, float* x) {
+  x[0] = __uint_as_float(r.x << 16);
+  x[1] = __uint_as_float(r.x & 0xffff0000u);
+  x[2] = __uint_as_float(r.y << 16);
+  x[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+// 2^((x - base) c) of n values.
+template <int n>
+__device__ __forceinline__ void exponentials(const float (&x)[n], float base, float c,
+                                             float (&y)[n]) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (at(k, 0) < len) {
-        if constexpr (sizeof(T) == 2) {
-          raw[k] = *reinterpret_cast<const uint4*>(z + at(k, 0));
-        } else {
-          const float4 p = *reinterpret_cast<const float4*>(z + at(k, 0));
-          const float4 q = *reinterpret_cast<const float4*>(z + at(k, 4));
-          x[k][0] = p.x; x[k][1] = p.y; x[k][2] = p.z; x[k][3] = p.w;
-          x[k][4] = q.x; x[k][5] = q.y; x[k][6] = q.z; x[k][7] = q.w;
-        }
-      }
-    }
+  for (int e = 0; e < n; ++e) y[e] = ex2((x[e] - base) * c);
+}
+
+// A row's running maximum and sum, or (greedy) maximum and its lowest index.
+struct Stat {
+  float m, l;
+};
+
+// Adds n values to a row's statistics; at(e) is the index of value e.
+template <bool GREEDY, int n, class At>
+__device__ __forceinline__ void add_values(Stat& s, const float (&x)[n], float c, At&& at) {
+  float top = x[0];
+#pragma unroll
+  for (int e = 1; e < n; ++e) top = fmaxf(top, x[e]);
+  if constexpr (GREEDY) {
+    if (top > s.m) s.l = __int_as_float(0x7fffffff);
+    s.m = fmaxf(s.m, top);
+    int best = __float_as_int(s.l);
+#pragma unroll
+    for (int e = 0; e < n; ++e)
+      if (x[e] == s.m) best = min(best, at(e));
+    s.l = __int_as_float(best);
   } else {
+    // y - m as (x - m) / temperature: exact zeros at the maximum, whatever its size.
+    const float m = fmaxf(s.m, top), base = m == -INFINITY ? 0.f : m;
+    float l = s.l == 0.f ? 0.f : s.l * ex2((s.m - base) * c), y[n];
+    exponentials(x, base, c, y);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] = at(k, e) < len ? (float)z[at(k, e)] : 0.f;
+    for (int e = 0; e < n; ++e) l += y[e];
+    s.m = m;
+    s.l = l;
   }
+}
 
-  const bool hist = A.tokens != nullptr || (A.draft != nullptr && i > 0);
-  if (hist) {
-    for (int v = tid * 4; v < P.slice; v += nt * 4)
-      *reinterpret_cast<uint4*>(count + v) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (A.tokens) {
-      const int t0 = A.cu_tokens[b], n = A.cu_tokens[b + 1] - t0;
-      const int np = A.n_prompt ? A.n_prompt[b] : 0;
-      const int32_t* tok = A.tokens + t0;
-#pragma unroll 4
-      for (int j = tid; j < n; j += nt) {
-        const int v = __ldg(tok + j) - begin;
-        if (v >= 0 && v < len) {
-          if (j < np) atomicOr(&count[v], kPrompt);
-          else atomicAdd(&count[v], 1u);
-        }
-      }
-    }
-    if (A.draft) {
-      for (int j = tid; j < i; j += nt) {
-        const int v = A.draft[(int64_t)b * A.draft_ld + j] - begin;
-        if (v >= 0 && v < len) atomicAdd(&count[v], 1u);
-      }
-    }
-    __syncthreads();
+// Combines the lanes' statistics; every lane gets the result.
+__device__ __forceinline__ Stat warp_stat(Stat s, bool greedy, float c) {
+  const float M = warp_max(s.m);
+  if (greedy) {
+    int best = s.m == M ? __float_as_int(s.l) : 0x7fffffff;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+    return Stat{M, __int_as_float(best)};
   }
+  const float base = M == -INFINITY ? 0.f : M;
+  return Stat{M, warp_sum(s.l == 0.f ? 0.f : s.l * ex2((s.m - base) * c))};
+}
+
+// VEC: rows aligned to whole chunks, which a thread takes; else its elements are a
+// block apart.  FILTER: there is a mask or a history.
+template <class T, bool VEC, bool FILTER>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint32_t seen_bits[];  // [words], then [words] ranks before each
+  __shared__ Stat s_warp[kMaxRows][kWarps];
+  __shared__ __align__(16) float4 s_pair[kMaxRows][kMaxCluster];
+  __shared__ uint64_t bar_pair;
+  __shared__ uint32_t count[kWindow];
+  __shared__ uint16_t list[kWindow];
+  __shared__ float s_y[kWindow];  // the listed elements' results, each thread's own
+  __shared__ uint32_t s_scan[kWarps];
+  const LogitsArgs& A = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % (unsigned)P.C), item = (int)(blockIdx.x / (unsigned)P.C);
+  const int b = item / P.groups, i0 = (item - b * P.groups) * P.group_rows;
+  const int n_rows = min(P.group_rows, A.rows - i0);
+  const int64_t r0 = (int64_t)b * A.rows + i0;
+  uint32_t* const rank0 = seen_bits + P.words;
+  const bool hist = A.tokens != nullptr || A.draft != nullptr;
+  const uint32_t V = (uint32_t)A.V, words = (V + 31) / 32;
+  // This CTA's blocks, and the logit where its k-th begins.
+  const int n_blocks = ((A.V + kBlock - 1) / kBlock - rank + P.C - 1) >> P.log_c;
+  auto block_at = [&](int k) { return ((k << P.log_c) + rank) * kBlock; };
 
   const float temp = A.temperature ? A.temperature[b] : 1.f;
   const Penalty pen{A.repetition ? A.repetition[b] : 1.f, A.frequency ? A.frequency[b] : 0.f,
                     A.presence ? A.presence[b] : 0.f};
-  const float* bias =
-      A.bias_rows ? A.bias + (A.bias_rows > 1 ? (int64_t)b * A.V : 0) + begin : nullptr;
-  const uint32_t* mask = A.mask ? A.mask + (int64_t)r * ((A.V + 31) / 32) : nullptr;
-  const bool bias_vec = VEC && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
-
-  float m = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const bool live = at(k, 0) < len;
-    if (VEC && !live) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] = -INFINITY;
-      continue;
-    }
-    if constexpr (VEC && sizeof(T) == 2) {
-      const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[k][2 * e] = __uint_as_float(u[e] << 16);
-        x[k][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-      }
-    }
-    if (hist) {
-      uint32_t c[8];
-      if constexpr (VEC) {
-        const uint4 p = *reinterpret_cast<const uint4*>(count + at(k, 0));
-        const uint4 q = *reinterpret_cast<const uint4*>(count + at(k, 4));
-        c[0] = p.x; c[1] = p.y; c[2] = p.z; c[3] = p.w;
-        c[4] = q.x; c[5] = q.y; c[6] = q.z; c[7] = q.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = at(k, e) < len ? count[at(k, e)] : 0u;
-      }
-      if ((c[0] | c[1] | c[2] | c[3]) | (c[4] | c[5] | c[6] | c[7])) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = pen(x[k][e], c[e]);
-      }
-    }
-    if (bias) {
-      if (bias_vec) {
-        const float4 p = __ldg(reinterpret_cast<const float4*>(bias + at(k, 0)));
-        const float4 q = __ldg(reinterpret_cast<const float4*>(bias + at(k, 4)));
-        x[k][0] += p.x; x[k][1] += p.y; x[k][2] += p.z; x[k][3] += p.w;
-        x[k][4] += q.x; x[k][5] += q.y; x[k][6] += q.z; x[k][7] += q.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (at(k, e) < len) x[k][e] += __ldg(bias + at(k, e));
-      }
-    }
-    if (mask) {
-      if constexpr (VEC) {
-        const int v = begin + at(k, 0);
-        const uint32_t bits = __ldg(mask + (v >> 5)) >> (v & 31);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!((bits >> e) & 1u)) x[k][e] = -INFINITY;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int v = begin + at(k, e);
-          if (at(k, e) < len && !((__ldg(mask + (v >> 5)) >> (v & 31)) & 1u)) x[k][e] = -INFINITY;
-        }
-      }
-    }
-    if constexpr (!VEC) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at(k, e) >= len) x[k][e] = -INFINITY;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, x[k][e]);
+  if (tid == 0) {
+    mbar_init(&bar_pair, 1);
+    fence_mbar_init();
+    if (P.C > 1) mbar_arrive_expect_tx(&bar_pair, (uint32_t)(P.C * n_rows * 16));
   }
+  const int32_t* const draft = A.draft ? A.draft + (int64_t)b * A.draft_ld : nullptr;
+  if (hist)
+    for (int w = tid; w < P.words; w += kThreads) seen_bits[w] = 0;
+  __syncthreads();
+  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to a neighbour
 
-  float* out = A.out + (int64_t)r * A.V + begin;
-  auto store = [&](int k, const float (&y)[8]) {
+  // Hands f(v, what) every token of the slice in the history: `what` is kPrompt, 1
+  // for one of the output (draft tokens before this group among it), or 0 for a draft
+  // token of the group, which its later rows count themselves.
+  // A token's place among this CTA's logits, or -1.
+  auto mine = [&](int token) {
+    const uint32_t t = (uint32_t)token, block = t / kBlock;
+    return t < V && (block & (uint32_t)(P.C - 1)) == (uint32_t)rank
+               ? (int)((block >> P.log_c) * kBlock + t % kBlock)
+               : -1;
+  };
+  auto scan_history = [&](auto&& f) {
+    if (A.tokens) {
+      const int t0 = max(0, min(A.cu_tokens[b], A.n_tokens));
+      const int n = min(A.cu_tokens[b + 1], A.n_tokens) - t0;
+      const int np = A.n_prompt ? A.n_prompt[b] : 0;
+      const int32_t* tok = A.tokens + t0;
+#pragma unroll 4
+      for (int j = tid; j < n; j += kThreads) {
+        const int v = mine(__ldg(tok + j));
+        if (v >= 0) f(v, j < np ? kPrompt : 1u);
+      }
+    }
+    if (draft) {
+      for (int j = tid; j < i0 + n_rows - 1; j += kThreads) {
+        const int v = mine(__ldg(draft + j));
+        if (v >= 0) f(v, j < i0 ? 1u : 0u);
+      }
+    }
+  };
+  int n_seen = 0;
+  if (hist) {
+    scan_history([&](int v, uint32_t) { atomicOr(&seen_bits[v >> 5], 1u << (v & 31)); });
+    __syncthreads();
+    // Ranks: bits before each word.
+    const int per = (P.words + kThreads - 1) / kThreads, w0 = min(tid * per, P.words);
+    const int w1 = min(w0 + per, P.words);
+    uint32_t mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(seen_bits[w]);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - mine;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      n_seen += (int)s_scan[w];
+    }
+    for (int w = w0; w < w1; ++w) {
+      rank0[w] = before;
+      before += __popc(seen_bits[w]);
+    }
+  }
+  // Lists and counts the seen tokens of ranks [from, from + kWindow).
+  auto window = [&](int from) {
+    for (int j = tid; j < kWindow; j += kThreads) count[j] = 0;
+    __syncthreads();  // and the ranks, the first time
+    scan_history([&](int v, uint32_t what) {
+      const int at = (int)(rank0[v >> 5] + __popc(seen_bits[v >> 5] & ((1u << (v & 31)) - 1u))) - from;
+      if (at >= 0 && at < kWindow) {
+        list[at] = (uint16_t)v;  // every occurrence writes the same
+        if (what == kPrompt) atomicOr(&count[at], kPrompt);
+        else if (what) atomicAdd(&count[at], 1u);
+      }
+    });
+    __syncthreads();
+  };
+
+  const float* const bias =
+      A.bias_rows ? A.bias + (A.bias_rows > 1 ? (int64_t)b * A.V : 0) : nullptr;
+  const uint32_t* const mask = A.mask ? A.mask + r0 * words : nullptr;
+  const bool bias_vec = VEC && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
+  const T* const z0 = static_cast<const T*>(A.z) + r0 * A.V;
+  float* const out0 = A.out + r0 * A.V;
+
+  // The logit of a place.
+  auto logit_of = [&](int at) { return block_at(at / kBlock) + at % kBlock; };
+  // Element j of the window in row q, with everything applied.
+  auto listed = [&](int j, int q) {
+    const int v = logit_of(list[j]);
+    uint32_t c = count[j];
+    if (draft)
+      for (int d = i0; d < i0 + q; ++d) c += __ldg(draft + d) == v ? 1u : 0u;
+    float x = (float)z0[(uint32_t)q * V + v];
+    const float add = bias ? __ldg(bias + v) : 0.f;
+    const uint32_t ok =
+        mask ? __ldg(mask + (uint32_t)q * words + (v >> 5)) >> (v & 31) : 1u;
+    x = pen(x, c) + add;
+    return ok & 1u ? x : -INFINITY;
+  };
+  // f(j, v, q) for every seen element and row.
+  int counted = -1;
+  auto each_listed = [&](auto&& f) {
+    for (int from = 0; from < n_seen; from += kWindow) {
+      if (counted != from) {
+        if (counted >= 0) __syncthreads();  // the last window is done with
+        window(from);
+        counted = from;
+      }
+      const int n = min(kWindow, n_seen - from);
+      for (int j = tid; j < n; j += kThreads) f(j, logit_of(list[j]));
+    }
+  };
+
+  // Hands the elements of row q to f(values, seen bits, first): seen elements (those
+  // are the list's) and forbidden ones come as -inf.  A value's index is index(first, e).
+  auto sweep = [&](int q, auto&& f) {
+    const T* const z = z0 + (uint32_t)q * V;
+    const uint32_t* const allowed = mask ? mask + (uint32_t)q * words : nullptr;
     if constexpr (VEC) {
-      if (at(k, 0) < len) {
-        st_global_cs_f4(out + at(k, 0), make_float4(y[0], y[1], y[2], y[3]));
-        st_global_cs_f4(out + at(k, 4), make_float4(y[4], y[5], y[6], y[7]));
+      using Raw = typename RawChunk<sizeof(T)>::type;
+      struct Pair {
+        Raw raw[2];
+        uint32_t allow[2];
+      };
+      // A pair of chunks; `tail`: the slice may end in it.
+      auto load = [&](Pair& p, int k, auto tail) {
+        const int v = block_at(k) + tid * kChunk;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const int at = v + d * kApart;
+          if (!decltype(tail)::value || at < A.V) {
+            p.raw[d] = *reinterpret_cast<const Raw*>(z + at);
+            if (FILTER && allowed) p.allow[d] = __ldg(allowed + ((uint32_t)at >> 5));
+          }
+        }
+      };
+      auto work = [&](const Pair& p, int k, auto tail) {
+        const int v = block_at(k) + tid * kChunk, at = k * kBlock + tid * kChunk;
+        if (decltype(tail)::value && v >= A.V) return;
+        const bool second = !decltype(tail)::value || v + kApart < A.V;
+        float x[2 * kChunk];
+        unpack(p.raw[0], x);
+        unpack(p.raw[1], x + kChunk);
+        if (bias) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            if (d == 0 || second) {
+              const float* bb = bias + v + d * kApart;
+              if (bias_vec) {
+                const float4 t = __ldg(reinterpret_cast<const float4*>(bb));
+                x[4 * d] += t.x; x[4 * d + 1] += t.y; x[4 * d + 2] += t.z; x[4 * d + 3] += t.w;
+              } else {
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) x[4 * d + e] += __ldg(bb + e);
+              }
+            }
+          }
+        }
+        uint32_t seen = 0;
+        if constexpr (FILTER) {
+          const int sh = v & 31;
+          uint32_t keep = 0xffu;
+          if (allowed) keep = (p.allow[0] >> sh & kNibble) | (p.allow[1] >> sh & kNibble) << kChunk;
+          if (hist) {
+            seen = seen_bits[at >> 5] >> sh & kNibble;
+            if (second) seen |= (seen_bits[(at + kApart) >> 5] >> sh & kNibble) << kChunk;
+          }
+          keep &= ~seen;
+#pragma unroll
+          for (int e = 0; e < 2 * kChunk; ++e) x[e] = keep & (1u << e) ? x[e] : -INFINITY;
+        }
+        if (!second) {
+#pragma unroll
+          for (int e = kChunk; e < 2 * kChunk; ++e) x[e] = -INFINITY;
+        }
+        f(x, seen, v, second);
+      };
+      int k = 0;
+      Pair p[2];
+      for (; k + 2 <= n_blocks && block_at(k + 1) + kBlock <= A.V; k += 2) {
+        load(p[0], k, std::false_type{});
+        load(p[1], k + 1, std::false_type{});
+        work(p[0], k, std::false_type{});
+        work(p[1], k + 1, std::false_type{});
+      }
+      for (; k < n_blocks; ++k) {
+        load(p[0], k, std::true_type{});
+        work(p[0], k, std::true_type{});
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at(k, e) < len) out[at(k, e)] = y[e];
+      for (int at = tid; at < n_blocks * kBlock; at += kThreads) {
+        const int v = logit_of(at);
+        if (v >= A.V) break;
+        const uint32_t seen = hist ? (seen_bits[at >> 5] >> (at & 31)) & 1u : 0u;
+        float x[1] = {(float)z[v]};
+        if (bias) x[0] += __ldg(bias + v);
+        if (seen || (FILTER && allowed && !((__ldg(allowed + (v >> 5)) >> (v & 31)) & 1u)))
+          x[0] = -INFINITY;
+        f(x, seen, v, false);
+      }
     }
+  };
+  // Seen elements of one window are written over what the sweep stores, after it;
+  // of more, the sweep leaves them out.
+  const bool over = n_seen <= kWindow;
+  // Writes what the sweep handed over.
+  auto store = [&](float* dst, const auto& y, uint32_t seen, bool second) {
+    if constexpr (VEC) {
+      if (!FILTER || over || seen == 0) {
+        st_global_cs_f4(dst, make_float4(y[0], y[1], y[2], y[3]));
+        if (second) st_global_cs_f4(dst + kApart, make_float4(y[4], y[5], y[6], y[7]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2 * kChunk; ++e)
+          if (!((seen >> e) & 1u) && (e < kChunk || second))
+            dst[(e / kChunk) * kApart + e % kChunk] = y[e];
+      }
+    } else {
+      if (over || !seen) dst[0] = y[0];
+    }
+  };
+  // The rows' results: `dense` for what the sweep hands over, in place, and
+  // `single(j, v)` for a listed element.
+  auto write = [&](int q, auto&& dense, auto&& single) {
+    float* const out = out0 + (uint32_t)q * V;
+    if (over && n_seen > 0) each_listed([&](int j, int v) { s_y[j] = single(j, v); });
+    if (!over) each_listed([&](int j, int v) { out[v] = single(j, v); });
+    sweep(q, [&](auto& x, uint32_t seen, int v, bool second) {
+      dense(x, v);
+      store(out + v, x, seen, second);
+    });
+    if (over && n_seen > 0) {
+      __syncthreads();
+      each_listed([&](int j, int v) { out[v] = s_y[j]; });
+    }
+  };
+  // Index of the sweep's value e.
+  auto index = [&](int v, int e) {
+    return v + (VEC ? (e / kChunk) * kApart + e % kChunk : 0);
   };
 
   if (A.raw) {
     if (P.C > 1) cluster_wait_acquire();
     const float t = temp > 0.f ? temp : 1.f;
+    for (int q = 0; q < n_rows; ++q)
+      write(q,
+            [&](auto& x, int) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] = __fdiv_rn(x[k][e], t);
-      store(k, x[k]);
-    }
+              for (auto& y : x) y = __fdiv_rn(y, t);
+            },
+            [&](int j, int) { return __fdiv_rn(listed(j, q), t); });
     return;
   }
 
-  // The CTA's maximum.
-  m = warp_max(m);
-  if ((tid & 31) == 0) s_red[tid >> 5] = m;
-  __syncthreads();
-  m = s_red[0];
-  for (int w = 1; w < warps; ++w) m = fmaxf(m, s_red[w]);
+  // ------------------------------------------------- statistics of the rows --
   const bool greedy = temp == 0.f;
-  float l = 0.f;
-  if (!greedy) {
-    // y - m as (x - m) / temperature: exact zeros at the maximum, whatever its size.
-    const float c = __fdiv_rn(kLog2E, temp), base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[k][e] = ex2((x[k][e] - base) * c);
-        l += x[k][e];
-      }
-    l = warp_sum(l);
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[tid >> 5] = l;
-    __syncthreads();
-    l = s_red[0];
-    for (int w = 1; w < warps; ++w) l += s_red[w];
-  }
-  if (P.C > 1) {
-    cluster_wait_acquire();
-    if (tid < P.C) st_cluster_f2(mapa_shared(smem_u32(&s_pair[rank]), (uint32_t)tid), m, l);
-    cluster_arrive_release();
-    cluster_wait_acquire();
-  } else {
-    if (tid == 0) s_pair[0] = make_float2(m, l);
-    __syncthreads();
-  }
-  float M = -INFINITY;
-  for (int c = 0; c < P.C; ++c) M = fmaxf(M, s_pair[c].x);
-
-  if (!greedy) {
-    const float c = __fdiv_rn(kLog2E, temp), base = M == -INFINITY ? 0.f : M;
-    float total = 0.f;
-    for (int q = 0; q < P.C; ++q) {
-      const float2 p = s_pair[q];
-      total += p.y == 0.f ? 0.f : p.y * ex2((p.x - base) * c);
+  const float c = greedy ? 1.f : __fdiv_rn(kLog2E, temp);
+  const Stat none = {-INFINITY, greedy ? __int_as_float(0x7fffffff) : 0.f};
+  auto gather = [&](auto greedy_c) {
+    constexpr bool G = decltype(greedy_c)::value;
+    for (int q = 0; q < n_rows; ++q) {
+      Stat st = none;
+      sweep(q, [&](const auto& x, uint32_t, int v, bool) {
+        add_values<G>(st, x, c, [&](int e) { return index(v, e); });
+      });
+      each_listed([&](int j, int v) {
+        const float x[1] = {listed(j, q)};
+        add_values<G>(st, x, c, [&](int) { return v; });
+      });
+      st = warp_stat(st, greedy, c);
+      if (lane == 0) s_warp[q][warp] = st;
     }
-    const float f = total == 0.f ? 0.f : ex2(((m == -INFINITY ? base : m) - base) * c) / total;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] *= f;
-      store(k, x[k]);
-    }
-    return;
-  }
-
-  // The lowest index of the row's largest value.
-  int best = 0x7fffffff;
-#pragma unroll
-  for (int k = NV - 1; k >= 0; --k)
-#pragma unroll
-    for (int e = 7; e >= 0; --e)
-      if (x[k][e] == M && at(k, e) < len) best = begin + at(k, e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if ((tid & 31) == 0) s_idx[tid >> 5] = best;
+  };
+  if (greedy) gather(std::true_type{});
+  else gather(std::false_type{});
   __syncthreads();
-  for (int w = 0; w < warps; ++w) best = min(best, s_idx[w]);
-  if (P.C > 1) {
-    // s_pair has been read by every CTA before anyone writes it again.
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    if (tid < P.C)
-      st_cluster_f2(mapa_shared(smem_u32(&s_pair[rank]), (uint32_t)tid), __int_as_float(best), 0.f);
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    for (int q = 0; q < P.C; ++q) best = min(best, __float_as_int(s_pair[q].x));
+  if (P.C > 1) cluster_wait_acquire();
+  if (warp < n_rows) {  // warp q: row q
+    const Stat s = warp_stat(lane < kWarps ? s_warp[warp][lane] : none, greedy, c);
+    const float4 p = make_float4(s.m, s.l, 0.f, 0.f);
+    if (P.C == 1) {
+      if (lane == 0) s_pair[warp][0] = p;
+    } else if (lane < P.C) {
+      st_async_f4(mapa_shared(smem_u32(&s_pair[warp][rank]), (uint32_t)lane), p,
+                  mapa_shared(smem_u32(&bar_pair), (uint32_t)lane));
+    }
   }
-  if (M == -INFINITY) best = -1;
+  if (P.C > 1) mbar_wait_cluster(&bar_pair, 0, STT_DEVERR_LOGITS_WAIT);
+  else __syncthreads();
+
+  // ------------------------------------------------------------ the results --
+  for (int q = 0; q < n_rows; ++q) {
+    const float4 p = s_pair[q][lane < P.C ? lane : 0];
+    const Stat s = warp_stat(lane < P.C ? Stat{p.x, p.y} : none, greedy, c);
+    if (greedy) {
+      const int best = s.m == -INFINITY ? -1 : __float_as_int(s.l);
+      write(q,
+            [&](auto& x, int v) {
+              int e = 0;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
+              for (auto& y : x) y = index(v, e++) == best ? 1.f : 0.f;
+            },
+            [&](int, int v) { return v == best ? 1.f : 0.f; });
+    } else {
+      const float top = s.m == -INFINITY ? 0.f : s.m, inv = s.l == 0.f ? 0.f : 1.f / s.l;
+      write(q,
+            [&](auto& x, int) {
+              exponentials(x, top, c, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[k][e] = begin + at(k, e) == best ? 1.f : 0.f;
-    store(k, x[k]);
+              for (auto& y : x) y *= inv;
+            },
+            [&](int j, int) { return ex2((listed(j, q) - top) * c) * inv; });
+    }
   }
 }
 
 using Kernel = void (*)(const Params);
 
-template <class T, bool VEC>
-Kernel pick(int nv) {
-  switch (nv) {
-    case 1: return logits_kernel<T, VEC, 1>;
-    case 2: return logits_kernel<T, VEC, 2>;
-    case 3: return logits_kernel<T, VEC, 3>;
-    case 4: return logits_kernel<T, VEC, 4>;
-    case 5: return logits_kernel<T, VEC, 5>;
-    default: return logits_kernel<T, VEC, 6>;
-  }
+// Raises a kernel's cluster limit, once per device (the first 64).
+cudaError_t allow(Kernel kern, int which, int dev) {
+  static std::atomic<uint64_t> done[8];
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done[which].load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done[which].fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s) {
-  // CTAs per row: the fewest whose slice a CTA's registers hold at two CTAs an SM;
-  // more while the rows alone leave SMs idle and a slice is worth splitting.
+  // CTAs per row: as few as leave a CTA ten blocks or less; more while the
+  // rows alone leave SMs idle.
+  const int blocks = (a.V + kBlock - 1) / kBlock;
+  auto blocks_of = [&](int c) { return (blocks + c - 1) / c; };
   int C = 1;
-  auto slice_of = [&](int c) { return ((a.V + c - 1) / c + 7) / 8 * 8; };
-  while (C < kMaxCluster && slice_of(C) > 5 * 8 * kMaxThreads) C *= 2;
-  while (C < kMaxCluster && (int64_t)a.N * C * 2 <= sm_count() && slice_of(C) >= 4096) C *= 2;
-  const int slice = slice_of(C);
-  int threads = kMaxThreads;
-  while (threads > 128 && slice <= 8 * (threads / 2)) threads /= 2;
-  const int nv = (slice + 8 * threads - 1) / (8 * threads);
-  if (nv > kMaxNv) return cudaErrorNotSupported;
+  while (C < kMaxCluster && blocks_of(C) > kBlocksMax) C *= 2;
+  while (C < kMaxCluster && (int64_t)a.N * C * 2 <= sm_count() && blocks_of(C) >= 2) C *= 2;
+  Params P{};
+  P.a = a;
+  P.C = C;
+  while ((1 << P.log_c) < C) ++P.log_c;
+  // Rows of a sequence that share its counts: up to eight, fewer while that makes less
+  // than kFill CTAs an SM (five rows together 147 us, one at a time 141, where B is 64).
+  const int64_t B = a.N / a.rows;
+  int most = std::min(kMaxRows, a.rows);
+  while (most > 1 && B * ((a.rows + most - 1) / most) * C < kFill * sm_count()) --most;
+  P.groups = (a.rows + most - 1) / most;
+  P.group_rows = (a.rows + P.groups - 1) / P.groups;
+  P.groups = (a.rows + P.group_rows - 1) / P.group_rows;
   const uintptr_t zo = reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.out);
-  const bool vec = a.V % 8 == 0 && (zo & 15u) == 0;
-  const Kernel kern = a.bf16 ? (vec ? pick<__nv_bfloat16, true>(nv) : pick<__nv_bfloat16, false>(nv))
-                             : (vec ? pick<float, true>(nv) : pick<float, false>(nv));
-  const int smem = (a.tokens || a.draft) ? slice * 4 : 0;
-  cudaError_t e;
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  if (C > 8) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  Params P{a, C, slice};
+  const bool vec = a.V % kChunk == 0 && (zo & 15u) == 0;
+  const bool filter = a.mask || a.tokens || a.draft;
+  const int which = (a.bf16 ? 4 : 0) + (vec ? 2 : 0) + (filter ? 1 : 0);
+  static const Kernel kernels[8] = {
+      logits_kernel<float, false, false>, logits_kernel<float, false, true>,
+      logits_kernel<float, true, false>, logits_kernel<float, true, true>,
+      logits_kernel<__nv_bfloat16, false, false>, logits_kernel<__nv_bfloat16, false, true>,
+      logits_kernel<__nv_bfloat16, true, false>, logits_kernel<__nv_bfloat16, true, true>};
+  const Kernel kern = kernels[which];
+  P.words = blocks_of(C) * (kBlock / 32);
+  const int smem = (a.tokens || a.draft) ? P.words * 8 : 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = allow(kern, which, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = B * P.groups * C;
+  if (ctas > 0x7fffffffll) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.N * C), 1, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -379,5 +570,8 @@ cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
+
+STT_DEFINE_ERROR_ACCESSOR(logits_error_word)
+STT_DEFINE_BUDGET_SETTER(logits_set_wait_budget)
 
 }  // namespace stt

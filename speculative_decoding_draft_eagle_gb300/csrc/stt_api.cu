@@ -229,6 +229,8 @@ int stt_device_error(void* stream, uint32_t* word) {
   w |= part;
   if (stt::paged_attn_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
   w |= part;
+  if (stt::logits_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
+  w |= part;
   *word = w;
   return (w & STT_DEVERR_WAIT_MASK) ? STT_ERR_TIMEOUT : STT_OK;
 }
@@ -246,6 +248,7 @@ int stt_debug_set_wait_budget(uint64_t ns) {
   if (e == cudaSuccess) e = stt::attn_bwd_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::lm_head_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::paged_attn_set_wait_budget(ns);
+  if (e == cudaSuccess) e = stt::logits_set_wait_budget(ns);
   return from_cuda(e);
 }
 
@@ -587,6 +590,7 @@ int stt_logits_process(const void* z, int64_t N, int64_t V, int rows, const stt_
     if (V > stt::kLogitsMaxV || N > 0x7fffffffll / 16) return STT_ERR_UNSUPPORTED;
     const stt_logits& p = *params;
     if (!p.tokens != !p.cu_tokens || (p.n_prompt && !p.tokens)) return STT_ERR_INVALID_ARG;
+    if (p.n_tokens < 0) return STT_ERR_INVALID_ARG;
     if (p.draft && p.draft_ld < rows - 1) return STT_ERR_INVALID_ARG;
     if (p.bias_rows < 0 || (p.bias_rows > 0) != (p.bias != nullptr)) return STT_ERR_INVALID_ARG;
     if (p.bias_rows > 1 && p.bias_rows != N / rows) return STT_ERR_INVALID_ARG;
@@ -621,6 +625,7 @@ int stt_logits_process(const void* z, int64_t N, int64_t V, int rows, const stt_
     a.mask = p.mask;
     a.draft_ld = p.draft_ld;
     a.bias_rows = p.bias_rows;
+    a.n_tokens = p.n_tokens;
     a.out = out;
     return from_cuda(stt::logits_launch(a, static_cast<cudaStream_t>(stream)));
   } catch (...) {

@@ -377,7 +377,7 @@ def stt_verify(p_target: torch.Tensor, p_draft: torch.Tensor, draft_tokens: torc
 # The structs of the C ABI are packed as bytes.
 _ROPE = struct.Struct("@PPPiIff")
 _PAGES = struct.Struct("@PPPPPqqqiiiiii")
-_LOGITS = struct.Struct("@PPPPPPPPPPii")
+_LOGITS = struct.Struct("@PPPPPPPPPPiii")
 
 
 def _current(stream):
@@ -750,7 +750,7 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
     p_p = 0 if presence is None else _arg(presence, "presence", f32, of, dev)
     if (tokens is None) != (cu_tokens is None):
         raise ValueError("tokens and cu_tokens go together")
-    p_tok = p_cu = p_np = p_dr = p_b = p_m = draft_ld = bias_rows = 0
+    p_tok = p_cu = p_np = p_dr = p_b = p_m = n_tok = draft_ld = bias_rows = 0
     if tokens is not None:
         if tokens.dim() != 1:
             raise ValueError("tokens must be [total]")
@@ -760,8 +760,10 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
         if tokens is None:
             raise ValueError("n_prompt is given without tokens")
         p_np = _arg(n_prompt, "n_prompt", i32, of, dev)
-    if tokens is not None and tokens.numel() == 0:  # an empty history has no address
-        p_tok = p_cu = p_np = 0
+    if tokens is not None:
+        n_tok = tokens.numel()
+        if n_tok == 0:  # an empty history has no address
+            p_tok = p_cu = p_np = 0
     if draft_tokens is not None:
         if draft_tokens.dim() != 2 or draft_tokens.shape[1] < rows - 1:
             raise ValueError(f"draft_tokens must be [B, at least {rows - 1}]")
@@ -776,8 +778,8 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
         p_m = _arg(mask, "mask", i32, (N, (V + 31) // 32), dev)
     if out is None:
         out = _new((N, V), f32, dev)
-    params = _LOGITS.pack(p_t, p_r, p_f, p_p, p_tok, p_cu, p_np, p_dr, p_b, p_m, draft_ld,
-                          bias_rows)
+    params = _LOGITS.pack(p_t, p_r, p_f, p_p, p_tok, p_cu, p_np, p_dr, p_b, p_m, n_tok,
+                          draft_ld, bias_rows)
     st = lib().stt_logits_process(
         p_z, N, V, rows, params,
         (STT_LOGITS_BF16 if t is torch.bfloat16 else 0) | (STT_LOGITS_RAW if raw else 0),
