@@ -8,6 +8,7 @@
 // heads through them, 32 / (D / 8) heads a step, 16-byte loads and stores, a few
 // steps' loads in flight at a time.
 #include <algorithm>
+#include <type_traits>
 
 #include "rope.cuh"
 
@@ -16,7 +17,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;     // forward; by registers
+constexpr int kBwdBlocksPerSm = 2;  // gradient
 constexpr int kUnroll = 4;  // steps whose loads are in flight together
 
 struct FwdP {
@@ -83,9 +85,11 @@ __device__ __forceinline__ bool append_dest(const FwdP& P, uint32_t t, int D, De
 }
 
 template <int D, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     qkv_rope_kernel(const __grid_constant__ FwdP P) {
   using L = RopeLane<D, INTER>;
+  __shared__ __align__(16) RopeTable<D> s_table[kWarps];
+  RopeTable<D>& table = s_table[threadIdx.x >> 5];
   L L_;
   L_.init(P.r.freq, P.r.R);
   const int nq = (P.H + L::kHeads - 1) / L::kHeads, nk = (P.H_kv + L::kHeads - 1) / L::kHeads;
@@ -101,49 +105,96 @@ __global__ void __launch_bounds__(kThreads)
     }
     const __nv_bfloat16* row = P.qkv + (int64_t)t * P.ld;
     const int lo = (int)(part * P.steps_per_part), hi = lo + (int)P.steps_per_part;
-    float c[8], s[8];
-    L_.angles(d.pos, P.r.amplitude, c, s);
+    if (P.r.R > 0) L_.fill(table, d.pos, P.r.amplitude);
 
     // Steps [lo, hi) of one kind of head: `first` its first step, `n` its heads.
-    auto run = [&](int first, int steps, int n, int head0, const __nv_bfloat16* w, bool rotate,
+    auto run = [&](int first, int steps, int n, int head0, const __nv_bfloat16* w, auto rotate,
                    __nv_bfloat16* dst, int64_t dst_head) {
+      constexpr bool kRotate = decltype(rotate)::value;
       const int from = max(lo, first) - first, to = min(hi, first + steps) - first;
       if (from >= to) return;
-      float a[8], b[8];
-      if (rotate) L_.tables(w, c, s, a, b);
-      for (int u0 = from; u0 < to; u0 += kUnroll) {
-        uint4 x[kUnroll];
+      Eight a, b;
+      if constexpr (kRotate) {
+        L_.factors(table, a, b);
+        if (w) {
+          const Eight own = L_.weight(w);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = (u0 + u) * L::kHeads + L_.sub;
-          x[u] = make_uint4(0, 0, 0, 0);
-          if (u0 + u < to && h < n)
-            x[u] = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)(head0 + h) * D) + L_.chunk);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          if (u0 + u >= to) break;
-          const int h = (u0 + u) * L::kHeads + L_.sub;
-          const uint4 y = rotate ? L_.apply(x[u], w != nullptr, P.r.eps, a, b) : x[u];
-          if (h < n) reinterpret_cast<uint4*>(dst + (int64_t)h * dst_head)[L_.chunk] = y;
+          for (int i = 0; i < 4; ++i) {
+            a.p[i] = mul_f32x2(a.p[i], own.p[i]);
+            b.p[i] = mul_f32x2(b.p[i], L::other(own, i));
+          }
         }
       }
+      const __nv_bfloat16* src = row + (head0 + from * L::kHeads + L_.sub) * D;
+      dst += (int64_t)(from * L::kHeads + L_.sub) * dst_head;
+      const int64_t dst_step = dst_head * L::kHeads;
+      // kUnroll steps from u0; `check`: there may be fewer, or fewer heads.
+      auto group = [&](int u0, auto check) {
+        constexpr bool kCheck = decltype(check)::value;
+        auto live = [&](int u) {
+          return !kCheck || (u0 + u < to && (u0 + u) * L::kHeads + L_.sub < n);
+        };
+        uint4 raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (live(u)) {
+            const __nv_bfloat16* p = src + u * L::kHeads * D;
+            raw[u] = kRotate ? L_.load(p) : __ldg(reinterpret_cast<const uint4*>(p) + L_.chunk);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (kCheck && u0 + u >= to) break;
+          if constexpr (kRotate) {
+            const Eight x = L::get(raw[u]);
+            Eight y = L_.turn(x, a, b);
+            if (w) {
+              uint64_t ss = mul_f32x2(x.p[0], x.p[0]);
+#pragma unroll
+              for (int i = 1; i < 4; ++i) ss = fma_f32x2(x.p[i], x.p[i], ss);
+              const float r = rsqrtf(L::head_sum(sum_pair(ss)) * (1.f / D) + P.r.eps);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y.p[i] = mul_f32x2(y.p[i], f32x2(r, r));
+            }
+            if (live(u)) L_.store(dst, y);
+          } else {
+            if (live(u)) reinterpret_cast<uint4*>(dst)[L_.chunk] = raw[u];
+          }
+          dst += dst_step;
+        }
+        src += kUnroll * L::kHeads * D;
+      };
+      int u0 = from;
+      for (; u0 + kUnroll <= to && (u0 + kUnroll) * L::kHeads <= n; u0 += kUnroll)
+        group(u0, std::false_type{});
+      for (; u0 < to; u0 += kUnroll) group(u0, std::true_type{});
     };
-    run(0, nq, P.H, 0, P.r.w_q, true, d.q, d.q_head);
+    run(0, nq, P.H, 0, P.r.w_q, std::true_type{}, d.q, d.q_head);
     if (d.kv) {
-      run(nq, nk, P.H_kv, P.H, P.r.w_k, true, d.k, d.kv_head);
-      run(nq + nk, nk, P.H_kv, P.H + P.H_kv, nullptr, false, d.v, d.kv_head);
+      run(nq, nk, P.H_kv, P.H, P.r.w_k, std::true_type{}, d.k, d.kv_head);
+      run(nq + nk, nk, P.H_kv, P.H + P.H_kv, nullptr, std::false_type{}, d.v, d.kv_head);
     }
   }
 }
 
-// Splits each token's steps over enough warps to fill the GPU, down to kUnroll
-// steps a warp.
-void split_items(int64_t N, int steps, int64_t warps_wanted, uint32_t* parts, uint32_t* per) {
-  int64_t p = std::max<int64_t>(1, warps_wanted / std::max<int64_t>(N, 1));
-  p = std::min<int64_t>(p, (steps + kUnroll - 1) / kUnroll);
-  *per = (uint32_t)((steps + p - 1) / p);
-  *parts = (uint32_t)((steps + *per - 1) / *per);
+// Splits each token's steps into the fewest parts that give the resident warps even
+// shares (within 7 %; 8192 tokens on 3648 warps would leave a quarter of them idle in
+// the last round), down to `least` steps a part; the evenest split where none does.
+void split_items(int64_t N, int steps, int64_t warps, int least, uint32_t* parts, uint32_t* per) {
+  double best = 0;
+  for (int p = 1; p <= (steps + least - 1) / least; ++p) {
+    const int64_t each = (steps + p - 1) / p, n = (steps + each - 1) / each;
+    const int64_t rounds = (N * n + warps - 1) / warps;
+    // Steps there are over steps the slowest warp's rounds have room for.
+    const double even = (double)(N * steps) / (double)(rounds * warps * each);
+    if (even > best) {
+      best = even;
+      *per = (uint32_t)each;
+      *parts = (uint32_t)n;
+      if (even > 0.93) break;
+    }
+  }
 }
 
 template <bool APPEND>
@@ -152,7 +203,7 @@ cudaError_t launch_fwd(FwdP& P, int D, cudaStream_t s) {
   const int heads = 32 / (D / 8);
   const int steps = (P.H + heads - 1) / heads + 2 * ((P.H_kv + heads - 1) / heads);
   const int64_t blocks_max = (int64_t)sm_count() * kBlocksPerSm;
-  split_items(P.N, steps, blocks_max * kWarps, &P.parts, &P.steps_per_part);
+  split_items(P.N, steps, blocks_max * kWarps, kUnroll, &P.parts, &P.steps_per_part);
   const int64_t items = (int64_t)P.N * P.parts;
   if (items > 0x7fffffffll) return cudaErrorNotSupported;
   P.items = (uint32_t)items;
@@ -183,129 +234,160 @@ struct BwdP {
   int S, H, H_kv;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  unpack8(__ldg(reinterpret_cast<const uint4*>(p)), x);
-}
+// A lane's elements of a gradient head as loaded.
+template <class T>
+struct RawGrad {
+  uint4 v[sizeof(T) / 2];
+  template <class L>
+  __device__ __forceinline__ void load(const L& l, const float* p) {
+    v[0] = __ldg(reinterpret_cast<const uint4*>(p + l.off0));
+    v[1] = __ldg(reinterpret_cast<const uint4*>(p + l.off1));
+  }
+  template <class L>
+  __device__ __forceinline__ void load(const L& l, const __nv_bfloat16* p) {
+    v[0] = l.load(p);
+  }
+  __device__ __forceinline__ Eight get() const {
+    if constexpr (sizeof(T) == 2)
+      return Eight{{pair_of(v[0].x), pair_of(v[0].y), pair_of(v[0].z), pair_of(v[0].w)}};
+    else
+      return Eight{{f32x2(__uint_as_float(v[0].x), __uint_as_float(v[0].y)),
+                    f32x2(__uint_as_float(v[0].z), __uint_as_float(v[0].w)),
+                    f32x2(__uint_as_float(v[1].x), __uint_as_float(v[1].y)),
+                    f32x2(__uint_as_float(v[1].z), __uint_as_float(v[1].w))}};
+  }
+};
 
-constexpr int kBwdUnroll = 2;
+constexpr int kBwdUnroll = 4;
 
 template <int D, bool INTER, class T>
-__global__ void __launch_bounds__(kThreads) qkv_rope_bwd_kernel(const __grid_constant__ BwdP P) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
+    qkv_rope_bwd_kernel(const __grid_constant__ BwdP P) {
   using L = RopeLane<D, INTER>;
-  __shared__ float s_dw[kWarps][2][D];
+  __shared__ __align__(16) float s_dw[kWarps][2][32][8];  // each lane's own, by kind
+  __shared__ __align__(16) RopeTable<D> s_table[kWarps];
   L L_;
   L_.init(P.r.freq, P.r.R);
   const int nq = (P.H + L::kHeads - 1) / L::kHeads, nk = (P.H_kv + L::kHeads - 1) / L::kHeads;
-  const int wib = threadIdx.x >> 5;
+  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  RopeTable<D>& table = s_table[wib];
   const uint32_t warp = blockIdx.x * kWarps + wib, warps = gridDim.x * kWarps;
-  float dwq[8], dwk[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
+  for (int e = 0; e < 8; ++e) s_dw[wib][0][lane][e] = s_dw[wib][1][lane][e] = 0.f;
 
   for (uint32_t item = warp; item < P.items; item += warps) {
     const uint32_t t = item / P.parts, part = item - t * P.parts;
     const uint32_t bi = t / (uint32_t)P.S, si = t - bi * (uint32_t)P.S;
     const int pos = P.positions ? __ldg(P.positions + t) : (int)si;
     const int lo = (int)(part * P.steps_per_part), hi = lo + (int)P.steps_per_part;
-    float c[8], s[8];
-    L_.angles(pos, P.r.amplitude, c, s);
+    if (P.r.R > 0) L_.fill(table, pos, P.r.amplitude);
     __nv_bfloat16* drow = P.dqkv + (int64_t)t * P.ld_d;
     const __nv_bfloat16* xrow = P.qkv + (int64_t)t * P.ld;
 
     auto run = [&](int first, int steps, int n, int head0, const void* dsrc,
-                   const __nv_bfloat16* w, bool rotate, float (&dw)[8]) {
+                   const __nv_bfloat16* w, auto rotate, int kind) {
+      constexpr bool kRotate = decltype(rotate)::value;
       const int from = max(lo, first) - first, to = min(hi, first + steps) - first;
       if (from >= to) return;
-      const T* dy0 = static_cast<const T*>(dsrc) + ((int64_t)bi * n * P.S + si) * D + L_.chunk * 8;
-      float wv[8];
-      if (w) L_.weight(w, wv);
-      for (int u0 = from; u0 < to; u0 += kBwdUnroll) {
-        float dy[kBwdUnroll][8];
+      const int64_t step = (int64_t)L::kHeads * P.S * D;
+      const T* dy = static_cast<const T*>(dsrc) +
+                    (((int64_t)bi * n + from * L::kHeads + L_.sub) * P.S + si) * D;
+      const int col = (head0 + from * L::kHeads + L_.sub) * D;
+      const __nv_bfloat16* xp = xrow + col;
+      __nv_bfloat16* dst = drow + col;
+      Eight a, b, wv, dw;
+      if constexpr (kRotate) {
+        L_.factors(table, a, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b.p[i] ^= 0x8000000080000000ull;  // the transpose
+        if (w) wv = L_.weight(w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dw.p[i] = 0;
+      auto group = [&](int u0, auto check) {
+        constexpr bool kCheck = decltype(check)::value;
+        auto live = [&](int u) {
+          return !kCheck || (u0 + u < to && (u0 + u) * L::kHeads + L_.sub < n);
+        };
+        RawGrad<T> raw[kBwdUnroll];
         uint4 xr[kBwdUnroll];
 #pragma unroll
         for (int u = 0; u < kBwdUnroll; ++u) {
-          const int h = (u0 + u) * L::kHeads + L_.sub;
-          const bool live = u0 + u < to && h < n;
+          raw[u] = RawGrad<T>{};
           xr[u] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dy[u][e] = 0.f;
-          if (live) {
-            load8(dy0 + (int64_t)h * P.S * D, dy[u]);
-            if (w)
-              xr[u] = __ldg(reinterpret_cast<const uint4*>(xrow + (int64_t)(head0 + h) * D) +
-                            L_.chunk);
+          if (live(u)) {
+            raw[u].load(L_, dy);
+            if (kRotate && w) xr[u] = L_.load(xp + u * L::kHeads * D);
           }
+          dy += step;
         }
 #pragma unroll
         for (int u = 0; u < kBwdUnroll; ++u) {
-          if (u0 + u >= to) break;
-          const int h = (u0 + u) * L::kHeads + L_.sub;
-          float g[8];
-          if (rotate) {
-            float o[8];
-            L_.other(dy[u], o);
+          if (kCheck && u0 + u >= to) break;
+          Eight g = raw[u].get();
+          if constexpr (kRotate) {
+            g = L_.turn(g, a, b);
+            if (w) {
+              // dx = r u w - x r^2 (r sum(u w x) / D): both sums go over the lanes together.
+              const Eight x = L::get(xr[u]);
+              Eight gw;
+              uint64_t s2 = 0, d2 = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              g[e] = L_.rot ? fmaf(dy[u][e], c[e], -(o[e] * s[e])) : dy[u][e];
-          } else {
+              for (int i = 0; i < 4; ++i) {
+                gw.p[i] = mul_f32x2(g.p[i], wv.p[i]);
+                s2 = fma_f32x2(x.p[i], x.p[i], s2);
+                d2 = fma_f32x2(gw.p[i], x.p[i], d2);
+              }
+              float ss = sum_pair(s2), sd = sum_pair(d2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = dy[u][e];
-          }
-          if (w) {
-            float x[8], ss = 0.f, sd = 0.f;
-            unpack8(xr[u], x);
+              for (int m = L::kLanes / 2; m > 0; m >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                sd += __shfl_xor_sync(0xffffffffu, sd, m);
+              }
+              const float r = rsqrtf(ss * (1.f / D) + P.r.eps), k = -(r * r * (r * sd) * (1.f / D));
+              const uint64_t r2 = f32x2(r, r), k2 = f32x2(k, k);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            const float r = rsqrtf(L::head_sum(ss) * (1.f / D) + P.r.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] *= r;
-              dw[e] = fmaf(g[e], x[e], dw[e]);
-              g[e] *= wv[e];
-              sd = fmaf(g[e], x[e], sd);
+              for (int i = 0; i < 4; ++i) {
+                dw.p[i] = fma_f32x2(mul_f32x2(g.p[i], r2), x.p[i], dw.p[i]);
+                g.p[i] = fma_f32x2(x.p[i], k2, mul_f32x2(gw.p[i], r2));
+              }
             }
-            sd = L::head_sum(sd) * (1.f / D);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-x[e], sd, g[e]);
           }
-          if (h < n) reinterpret_cast<uint4*>(drow + (int64_t)(head0 + h) * D)[L_.chunk] = pack8(g);
+          if (live(u)) L_.store(dst + u * L::kHeads * D, g);
         }
+        xp += kBwdUnroll * L::kHeads * D;
+        dst += kBwdUnroll * L::kHeads * D;
+      };
+      int u0 = from;
+      for (; u0 + kBwdUnroll <= to && (u0 + kBwdUnroll) * L::kHeads <= n; u0 += kBwdUnroll)
+        group(u0, std::false_type{});
+      for (; u0 < to; u0 += kBwdUnroll) group(u0, std::true_type{});
+      if (kRotate && w) {
+        uint64_t* acc = reinterpret_cast<uint64_t*>(s_dw[wib][kind][lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = add_f32x2(acc[i], dw.p[i]);
       }
     };
-    float none[8];
-    run(0, nq, P.H, 0, P.dq, P.r.w_q, true, dwq);
-    run(nq, nk, P.H_kv, P.H, P.dk, P.r.w_k, true, dwk);
-    run(nq + nk, nk, P.H_kv, P.H + P.H_kv, P.dv, nullptr, false, none);
+    run(0, nq, P.H, 0, P.dq, P.r.w_q, std::true_type{}, 0);
+    run(nq, nk, P.H_kv, P.H, P.dk, P.r.w_k, std::true_type{}, 1);
+    run(nq + nk, nk, P.H_kv, P.H + P.H_kv, P.dv, nullptr, std::false_type{}, 0);
   }
 
   if (P.r.w_q || P.r.w_k) {
-    // Heads of one warp step, then the block's warps, in fixed order.
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-      for (int o = L::kLanes; o < 32; o <<= 1) {
-        dwq[e] += __shfl_xor_sync(0xffffffffu, dwq[e], o);
-        dwk[e] += __shfl_xor_sync(0xffffffffu, dwk[e], o);
-      }
-    }
-    if (L_.sub == 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s_dw[wib][0][L_.chunk * 8 + e] = dwq[e];
-        s_dw[wib][1][L_.chunk * 8 + e] = dwk[e];
-      }
-    }
+    // The block's warps and the heads of one warp step, in fixed order.
     __syncthreads();
     for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+      const int kind = x / D, e = x % D, half = P.r.R / 2;
+      int c = e / 8, slot = e % 8;  // the lane of the head that holds element e, and where
+      if (!INTER && e < P.r.R) {
+        c = (e < half ? e : e - half) / 4;
+        slot = e % 4 + (e < half ? 0 : 4);
+      }
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += (&s_dw[w][0][0])[x];
+      for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+        for (int h = 0; h < L::kHeads; ++h) v += s_dw[w][kind][h * L::kLanes + c][slot];
       P.partial[(int64_t)blockIdx.x * 2 * D + x] = v;
     }
   }
@@ -318,6 +400,7 @@ __global__ void __launch_bounds__(1024) qkv_rope_dw_kernel(const float* partial,
   __shared__ float sm[8][128];
   const int x = threadIdx.x & 127, y = threadIdx.x >> 7;
   float* const dst = blockIdx.x ? dw_k : dw_q;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!dst) return;
   float v = 0.f;
   if (x < D)
@@ -396,8 +479,9 @@ cudaError_t qkv_rope_bwd_launch(const RopeArgs& r, const void* dq, const void* d
   const int64_t N = (int64_t)B * S;
   const int heads = 32 / (D / 8);
   const int steps = (H + heads - 1) / heads + 2 * ((H_kv + heads - 1) / heads);
-  const int64_t blocks_max = std::min<int64_t>((int64_t)sm_count() * 3, kRopeBwdMaxGrid);
-  split_items(N, steps, blocks_max * kWarps, &P.parts, &P.steps_per_part);
+  const int64_t blocks_max = std::min<int64_t>((int64_t)sm_count() * kBwdBlocksPerSm, kRopeBwdMaxGrid);
+  split_items(N, steps, blocks_max * kWarps, kBwdUnroll, &P.parts, &P.steps_per_part);
+  if (N == 0) P.parts = P.steps_per_part = 1;
   const int64_t items = N * P.parts;
   if (items > 0x7fffffffll) return cudaErrorNotSupported;
   P.items = (uint32_t)items;
@@ -413,9 +497,21 @@ cudaError_t qkv_rope_bwd_launch(const RopeArgs& r, const void* dq, const void* d
     }
   }
   // No tokens: the weights' gradients are zero.
-  if (dw_q || dw_k) qkv_rope_dw_kernel<<<2, 1024, 0, s>>>(P.partial, (int)grid, D, dw_q, dw_k);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && (dw_q || dw_k)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, qkv_rope_dw_kernel, (const float*)P.partial, (int)grid, D, dw_q, dw_k);
+  }
   prof_after(s);
-  return cudaGetLastError();
+  return e;
 }
 
 STT_DEFINE_ERROR_ACCESSOR(qkv_rope_error_word)

@@ -1,19 +1,17 @@
-// rope.cuh -- pieces shared by the rotation kernels (qkv_rope.cu):
-// angles, and the per-lane tables of the fused norm + rotation.
+// rope.cuh -- pieces shared by the rotation kernels (qkv_rope.cu): angles, and what a
+// lane holds of a head.
 //
-// A lane holds 8 consecutive elements of a head (one 16-byte load), so a head
-// takes D / 8 lanes.  With x the raw elements, r = (mean x^2 + eps)^(-1/2) (1
-// without a weight), and x' the other element of each one's pair,
-//     y[e] = r (x[e] a[e] + x'[e] b[e]),
-// a = amplitude w cos, b = -+ amplitude w' sin for rotated elements, a = w,
-// b = 0 for the rest: two multiply-adds an element once the token's tables are
-// made, and the tables serve every head of the token.  x' is in the lane itself
-// for interleaved pairs, and in the lane R / 16 further (or back) for halves.
+// A head takes D / 8 lanes, a lane 8 of its elements, and both elements of each of
+// its pairs: lane c has elements 8 c .. 8 c + 7 for interleaved pairs and for elements
+// that are not rotated, and 4 c .. 4 c + 3 with R / 2 + 4 c .. for halves.  A lane has
+// four pairs either way, whose cosines and sines it reads from its warp's table, and
+// nothing of the rotation crosses lanes.  Elements are kept as four pairs of floats
+// (the instructions that take two at a time halve what the kernels issue, which bound
+// them before).
 #pragma once
 
 #include "../../include/stt.h"
-#include "internal.h"
-#include "ptx.cuh"
+#include "attn_common.cuh"
 
 namespace stt {
 
@@ -47,31 +45,43 @@ __device__ __forceinline__ void turn_sincos(uint64_t frac, int pos, float& c, fl
   sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &s, &c);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+// Eight elements as four pairs.
+struct Eight {
+  uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t pair_of(uint32_t v) { return f32x2(bf16lo(v), bf16hi(v)); }
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  return f32x2(b, a);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                    pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  return pack_bf16(a, b);
 }
-__device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
-  return make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
-                    __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
+__device__ __forceinline__ float sum_pair(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  return a + b;
 }
 
-// What one lane knows of its chunk for the whole kernel.
+// A warp's table of its token's cosines and sines (amplitude applied), in shared
+// memory: each pair's angle is taken once.
+template <int D>
+struct RopeTable {
+  float cos[D / 2], sin[D / 2];
+};
+
+// What one lane knows of its elements for the whole kernel.
 template <int D, bool INTER>
 struct RopeLane {
   static constexpr int kLanes = D / 8;         // lanes per head
   static constexpr int kHeads = 32 / kLanes;   // heads per warp step
-  static constexpr int kAngles = INTER ? 4 : 8;
-  int chunk, sub, partner;  // chunk of the head, head of the warp step, lane of x'
-  bool rot, first;          // rotated; first half (of halves)
+  static constexpr int kAngles = D / 64;       // pairs whose angles a lane takes
+  int chunk, sub;   // lane of the head, head of the warp step
+  int off0, off1;   // first of its two runs of four elements
+  bool rot;         // rotated
   uint64_t frac[kAngles];
 
   __device__ __forceinline__ void init(const double* freq, int R) {
@@ -79,65 +89,93 @@ struct RopeLane {
     chunk = lane % kLanes;
     sub = lane / kLanes;
     rot = chunk * 8 < R;
-    const int half = R / 16;
-    first = INTER || chunk < half;
-    partner = lane;
-    if (!INTER && rot) partner = first ? lane + half : lane - half;
+    off0 = !INTER && rot ? chunk * 4 : chunk * 8;
+    off1 = !INTER && rot ? R / 2 + chunk * 4 : chunk * 8 + 4;
 #pragma unroll
-    for (int i = 0; i < kAngles; ++i) {
-      const int pair = INTER ? chunk * 4 + i : (first ? chunk : chunk - half) * 8 + i;
-      frac[i] = rot ? turn_fraction(__ldg(freq + pair)) : 0;
-    }
+    for (int i = 0; i < kAngles; ++i)
+      frac[i] = lane + 32 * i < R / 2 ? turn_fraction(__ldg(freq + lane + 32 * i)) : 0;
   }
 
-  // cos and +-sin of this lane's elements at a position (amplitude applied); the
-  // sign is that of x' in y.  Unrotated elements: 1 and 0.
-  __device__ __forceinline__ void angles(int pos, float amplitude, float (&c)[8],
-                                         float (&s)[8]) const {
+  // Fills the warp's table for a position.
+  __device__ __forceinline__ void fill(RopeTable<D>& t, int pos, float amplitude) const {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();  // the last token's readers
 #pragma unroll
     for (int i = 0; i < kAngles; ++i) {
-      float ci = 1.f, si = 0.f;
-      if (rot) {
-        turn_sincos(frac[i], pos, ci, si);
-        ci *= amplitude;
-        si *= amplitude;
-      }
-      if (INTER) {
-        c[2 * i] = c[2 * i + 1] = ci;
-        s[2 * i] = -si;
-        s[2 * i + 1] = si;
-      } else {
-        c[i] = ci;
-        s[i] = first ? -si : si;
-      }
+      float c, s;
+      turn_sincos(frac[i], pos, c, s);
+      t.cos[lane + 32 * i] = c * amplitude;
+      t.sin[lane + 32 * i] = s * amplitude;
     }
+    __syncwarp();
   }
 
-  // This chunk of a weight (ones without one), and of its pair elements.
-  __device__ __forceinline__ void weight(const __nv_bfloat16* w, float (&own)[8]) const {
-    if (w) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + chunk), own);
+  // Factors of a rotation: y = x a + x' b, x' the other element of each one's pair.
+  // Elements that are not rotated: a = 1, and no x'.
+  __device__ __forceinline__ void factors(const RopeTable<D>& t, Eight& a, Eight& b) const {
+    if (!rot) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a.p[i] = f32x2(1.f, 1.f);
+        b.p[i] = 0;
+      }
+      return;
+    }
+    const float4 c = *reinterpret_cast<const float4*>(t.cos + chunk * 4);
+    const float4 s = *reinterpret_cast<const float4*>(t.sin + chunk * 4);
+    if (INTER) {
+      a.p[0] = f32x2(c.x, c.x); a.p[1] = f32x2(c.y, c.y);
+      a.p[2] = f32x2(c.z, c.z); a.p[3] = f32x2(c.w, c.w);
+      b.p[0] = f32x2(-s.x, s.x); b.p[1] = f32x2(-s.y, s.y);
+      b.p[2] = f32x2(-s.z, s.z); b.p[3] = f32x2(-s.w, s.w);
+    } else {
+      a.p[0] = a.p[2] = f32x2(c.x, c.y);
+      a.p[1] = a.p[3] = f32x2(c.z, c.w);
+      b.p[0] = f32x2(-s.x, -s.y); b.p[1] = f32x2(-s.z, -s.w);
+      b.p[2] = f32x2(s.x, s.y); b.p[3] = f32x2(s.z, s.w);
+    }
+  }
+  // The other element of each pair.
+  __device__ __forceinline__ static uint64_t other(const Eight& x, int i) {
+    return INTER ? swapped(x.p[i]) : x.p[i ^ 2];
+  }
+  // x a + x' b (unrotated: x a; not 0 times an infinity).
+  __device__ __forceinline__ Eight turn(const Eight& x, const Eight& a, const Eight& b) const {
+    Eight y;
+    if (rot) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y.p[i] = fma_f32x2(x.p[i], a.p[i], mul_f32x2(other(x, i), b.p[i]));
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) own[e] = 1.f;
+      for (int i = 0; i < 4; ++i) y.p[i] = mul_f32x2(x.p[i], a.p[i]);
     }
-  }
-  __device__ __forceinline__ void other(const float (&x)[8], float (&o)[8]) const {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = INTER ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], partner);
+    return y;
   }
 
-  // a = w cos, b = w' sin.
-  __device__ __forceinline__ void tables(const __nv_bfloat16* w, const float (&c)[8],
-                                         const float (&s)[8], float (&a)[8], float (&b)[8]) const {
-    float own[8], oth[8];
-    weight(w, own);
-    other(own, oth);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = own[e] * c[e];
-      b[e] = oth[e] * s[e];
+  // This lane's elements of a bf16 head at p, as loaded; and its elements.
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16* p) const {
+    if (INTER) return __ldg(reinterpret_cast<const uint4*>(p + off0));
+    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p + off0));
+    const uint2 hi = __ldg(reinterpret_cast<const uint2*>(p + off1));
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  __device__ __forceinline__ static Eight get(const uint4& v) {
+    return Eight{{pair_of(v.x), pair_of(v.y), pair_of(v.z), pair_of(v.w)}};
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, const Eight& y) const {
+    const uint4 v = make_uint4(pack_pair(y.p[0]), pack_pair(y.p[1]), pack_pair(y.p[2]),
+                               pack_pair(y.p[3]));
+    if (INTER) {
+      *reinterpret_cast<uint4*>(p + off0) = v;
+    } else {
+      *reinterpret_cast<uint2*>(p + off0) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2*>(p + off1) = make_uint2(v.z, v.w);
     }
+  }
+  // A weight's elements (ones without a weight).
+  __device__ __forceinline__ Eight weight(const __nv_bfloat16* w) const {
+    if (w) return get(load(w));
+    return Eight{{f32x2(1.f, 1.f), f32x2(1.f, 1.f), f32x2(1.f, 1.f), f32x2(1.f, 1.f)}};
   }
 
   // Sum over the lanes of a head.
@@ -145,33 +183,6 @@ struct RopeLane {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-  }
-
-  // y of one 16-byte chunk x; every lane of the warp calls it.
-  __device__ __forceinline__ uint4 apply(const uint4& raw, bool norm, float eps,
-                                         const float (&a)[8], const float (&b)[8]) const {
-    float x[8], o[8], y[8];
-    unpack8(raw, x);
-    if constexpr (INTER) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-    } else {
-      unpack8(shfl4(raw, partner), o);
-    }
-    if (!rot) {  // b is 0 there, but 0 times an infinity is not
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 0.f;
-    }
-    float r = 1.f;
-    if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      r = rsqrtf(head_sum(ss) * (1.f / D) + eps);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = r * fmaf(x[e], a[e], o[e] * b[e]);
-    return pack8(y);
   }
 };
 
