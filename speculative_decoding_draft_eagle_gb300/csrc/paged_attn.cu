@@ -28,6 +28,7 @@
 // Barrier phases count S products, stage uses and units over the CTA's whole share.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/stt.h"
 #include "attn_common.cuh"
@@ -92,6 +93,12 @@ __device__ __forceinline__ int unit_keys(const Params& P, int n, int len, int j)
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 
+// a / b; in 32 bits where both fit, which is a fraction of the instructions.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // Part of one unit in a CTA's share: key tiles [t0, t1) of `tiles`.
 struct Seg {
   int b, h, j, t0, t1, tiles, keys;
@@ -106,8 +113,8 @@ struct Walk {
   __device__ __forceinline__ void init(const Params& P, const Batch& S, long long c, long long n) {
     const int B = P.g.B;
     const long long W = S.pref[B];
-    pos = W * c / n;
-    end = W * (c + 1) / n;
+    pos = div_ll(W * c, n);
+    end = div_ll(W * (c + 1), n);
     if (pos >= end) return;
     int lo = 0, hi = B - 1;  // last sequence with pref <= pos and tiles of its own
     while (lo < hi) {
@@ -116,8 +123,8 @@ struct Walk {
     }
     b = lo;
     long long rem = pos - S.pref[b];
-    const long long per_head = (S.pref[b + 1] - S.pref[b]) / P.g.H_kv;
-    h = (int)(rem / per_head);
+    const long long per_head = div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
+    h = (int)div_ll(rem, per_head);
     rem -= h * per_head;
     for (j = 0;; ++j) {
       const int cost = max(tiles_of(unit_keys(P, S.n[b], S.len[b], j)), 1);
@@ -189,7 +196,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = P.g.B;
+  // The join's blocks may take their places as CTAs leave; they wait for the rest.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  if (lane == 0 && (warp == kWarpK || warp == kWarpV)) {
+    tma_prefetch_desc(warp == kWarpK ? &tmK : &tmV);
+    if (warp == kWarpK) tma_prefetch_desc(&tmQ);
+  }
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar_q_full[x], 1);
@@ -272,10 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int page = 1 << P.g.page_shift;
     const int box = min(page, kTile);      // keys a copy brings
     const int copies = kTile / box;        // copies a tile takes, one lane each
-    if (lane == 0) {
-      tma_prefetch_desc(tm);
-      if (is_k) tma_prefetch_desc(&tmQ);
-    }
     uint32_t g = 0, i = 0, q_issued = 0;
     bool ok = true;
     while (ok && walk.next(P, S, s)) {
@@ -406,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         joined = true;
         const long long last = s.u0 + s.tiles - 1;
         JoinDesc d;
-        d.c0 = (int)(((s.u0 + 1) * ctas - 1) / W);
-        d.c1 = (int)(((last + 1) * ctas - 1) / W);
+        d.c0 = (int)div_ll((s.u0 + 1) * ctas - 1, W);
+        d.c1 = (int)div_ll((last + 1) * ctas - 1, W);
         d.tok0 = s.tok0;
         d.ntok = s.ntok;
         d.kvh = s.h;
@@ -610,12 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the units cut by share borders.  The CTAs c0 + 1 .. c1 whose
-// shares begin inside a unit divide its rows among their blocks; the warps of a
-// block take a row each, or several share a row's parts when there are few rows.
+// shares begin inside a unit divide its rows among their blocks.  A warp takes four rows
+// at a time, so that their loads are in flight together; with few rows, several warps
+// share a row's parts.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_constant__ Params P) {
-  constexpr int E = D / 32, kW = kJoinThreads / 32;
-  __shared__ float s_o[kW][D], s_l[kW];
+  constexpr int E = D / 32, kW = kJoinThreads / 32, R = 4;
+  __shared__ __align__(16) float s_o[kW][D];
+  __shared__ float s_l[kW];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinDesc d = P.join[blockIdx.x];
   if (d.c0 < 0) return;
@@ -624,69 +635,91 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_con
   const int share = parts - 1, first = (int)blockIdx.x - d.c0 - 1;
   const int mine = first < rows ? (rows - first + share - 1) / share : 0;
   if (mine == 0) return;
+
+  // Part p's slot.
+  auto slot = [&](int p) { return P.part + (int64_t)(2 * (d.c0 + p) + (p == 0 ? 1 : 0)) * P.slot; };
+  using V = typename std::conditional<E == 4, float4, float2>::type;
+  struct Sum {
+    float acc[E], l, m;
+  };
+  auto add = [&](Sum& s, float lse, const V& v) {
+    if (lse != -INFINITY) {
+      const float mn = fmaxf(s.m, lse), a = ex2(s.m - mn), w = ex2(lse - mn);
+      s.l = s.l * a + w;
+      const float* x = reinterpret_cast<const float*>(&v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) s.acc[e] = fmaf(w, x[e], s.acc[e] * a);
+      s.m = mn;
+    }
+  };
+  auto write = [&](const Sum& s, int r) {
+    const int t = r / P.G, g = r - t * P.G;
+    const int64_t at = (int64_t)(d.tok0 + t) * P.H + d.kvh * P.G + g;
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + at * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(s.acc[e] * inv, s.acc[e + 1] * inv);
+    if (P.lse && lane == 0) P.lse[at] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
+  };
+
   int wpr = 1;  // warps per row
   while (wpr * 2 * mine <= kW && wpr * 2 <= parts) wpr *= 2;
-  const int sub = warp % wpr;
-  for (int x0 = 0; x0 < mine; x0 += kW / wpr) {
-    const int x = x0 + warp / wpr;
-    const int r = first + x * share;
-    float acc[E], l = 0.f, m = -INFINITY;
+  if (wpr == 1) {
+    for (int x0 = warp * R; x0 < mine; x0 += kW * R) {
+      Sum s[R];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (x < mine) {
+      for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[i].acc[e] = 0.f;
+        s[i].l = 0.f;
+        s[i].m = -INFINITY;
+      }
+      for (int p = 0; p < parts; ++p) {
+        const float* src = slot(p);
+        float lse[R];
+        V v[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int r = first + min(x0 + i, mine - 1) * share;
+          lse[i] = src[(int64_t)P.slot_rows * D + r];
+          v[i] = reinterpret_cast<const V*>(src + (int64_t)r * D)[lane];
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) add(s[i], lse[i], v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (x0 + i < mine) write(s[i], first + (x0 + i) * share);
+    }
+    return;
+  }
+  // One row to each wpr warps.
+  const int sub = warp % wpr, x = warp / wpr, r = first + x * share;
+  Sum s;
+#pragma unroll
+  for (int e = 0; e < E; ++e) s.acc[e] = 0.f;
+  s.l = 0.f;
+  s.m = -INFINITY;
+  if (x < mine) {
 #pragma unroll 4
-      for (int p = sub; p < parts; p += wpr) {
-        const float* src = P.part + (int64_t)(2 * (d.c0 + p) + (p == 0 ? 1 : 0)) * P.slot;
-        const float lse = src[(int64_t)P.slot_rows * D + r];
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 f = reinterpret_cast<const float4*>(src + (int64_t)r * D)[lane];
-          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-        } else {
-          const float2 f = reinterpret_cast<const float2*>(src + (int64_t)r * D)[lane];
-          v[0] = f.x; v[1] = f.y;
-        }
-        if (lse != -INFINITY) {
-          const float mn = fmaxf(m, lse), a = ex2(m - mn), w = ex2(lse - mn);
-          l = l * a + w;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e] * a);
-          m = mn;
-        }
-      }
+    for (int p = sub; p < parts; p += wpr) {
+      const float* src = slot(p);
+      add(s, src[(int64_t)P.slot_rows * D + r], reinterpret_cast<const V*>(src + (int64_t)r * D)[lane]);
     }
-    if (wpr > 1) {
-      // The row's warps, in order, relative to the largest.
-      const float part_inv = l == 0.f ? 0.f : 1.f / l;
-      __syncthreads();
+  }
+  const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e] * part_inv;
-      if (lane == 0) s_l[warp] = l == 0.f ? -INFINITY : m + log2f(l);
-      __syncthreads();
-      if (sub == 0) {
-        m = -INFINITY;
-        l = 0.f;
-        for (int y = 0; y < wpr; ++y) m = fmaxf(m, s_l[warp + y]);
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = s.acc[e] * inv;
+  if (lane == 0) s_l[warp] = s.l == 0.f ? -INFINITY : s.m + log2f(s.l);
+  __syncthreads();
+  if (sub == 0 && x < mine) {  // the row's warps, in order
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int y = 0; y < wpr; ++y) {
-          if (s_l[warp + y] == -INFINITY) continue;
-          const float w = ex2(s_l[warp + y] - m);
-          l += w;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, s_o[warp + y][lane * E + e], acc[e]);
-        }
-      }
-    }
-    if (x < mine && sub == 0) {
-      const int t = r / P.G, g = r - t * P.G;
-      const int64_t at = (int64_t)(d.tok0 + t) * P.H + d.kvh * P.G + g;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + at * D) + lane * (E / 2);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-      if (P.lse && lane == 0) P.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    }
+    for (int e = 0; e < E; ++e) s.acc[e] = 0.f;
+    s.l = 0.f;
+    s.m = -INFINITY;
+    for (int y = 0; y < wpr; ++y)
+      add(s, s_l[warp + y], reinterpret_cast<const V*>(s_o[warp + y])[lane]);
+    write(s, r);
   }
 }
 

@@ -94,9 +94,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   L_.init(P.r.freq, P.r.R);
   const int nq = (P.H + L::kHeads - 1) / L::kHeads, nk = (P.H_kv + L::kHeads - 1) / L::kHeads;
   const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
+  const int lane = threadIdx.x & 31;
 
   for (uint32_t item = warp; item < P.items; item += warps) {
     const uint32_t t = item / P.parts, part = item - t * P.parts;
+    // Where the row goes takes a few dependent loads; the row is fetched meanwhile.
+    for (int line = lane; line < (int)P.steps_per_part * 4; line += 32) {
+      const int64_t at = ((int64_t)part * P.steps_per_part * 4 + line) * 64;
+      if (at < (int64_t)(P.H + 2 * P.H_kv) * D)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(P.qkv + (int64_t)t * P.ld + at));
+    }
     Dest d;
     if constexpr (APPEND) {
       if (!append_dest(P, t, D, d)) continue;
@@ -263,6 +270,7 @@ constexpr int kBwdUnroll = 4;
 template <int D, bool INTER, class T>
 __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
     qkv_rope_bwd_kernel(const __grid_constant__ BwdP P) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using L = RopeLane<D, INTER>;
   __shared__ __align__(16) float s_dw[kWarps][2][32][8];  // each lane's own, by kind
   __shared__ __align__(16) RopeTable<D> s_table[kWarps];
@@ -404,6 +412,7 @@ __global__ void __launch_bounds__(1024) qkv_rope_dw_kernel(const float* partial,
   if (!dst) return;
   float v = 0.f;
   if (x < D)
+#pragma unroll 8
     for (int r = y; r < rows; r += 8) v += partial[((int64_t)r * 2 + blockIdx.x) * D + x];
   sm[y][x] = v;
   __syncthreads();
