@@ -6,21 +6,24 @@
 // every C-th block of 2048 logits (tokens crowd at the low end of a vocabulary, and
 // contiguous slices would leave most of the history to one CTA).  It counts the
 // sequence's history over its blocks in shared memory (whole numbers: the atomics'
-// order does not matter), goes over its elements for each row's maximum m and sum l
-// of e^(y - m), exchanges the pairs of all its rows with the other CTAs at once, and
-// goes over its elements again to write e^(y - M) / L.  The second reading comes from
-// L2: HBM sees 2 or 4 bytes read and 4 written per logit.  320 bf16 rows of 151936
-// with histories, bias and mask take 141 us, 69 us without them; what bounds both is
-// the issue of instructions (87 and 34 million), not HBM (44 us).  Keeping a row in
-// registers between the two passes halves the loads but left fewer warps to cover
-// the exchange: 136 to 205 us, with one row in flight, two, or a ring of bulk copies.
+// order does not matter).  A first pass over a row applies everything, writes the
+// processed logits to the output and takes their maximum m and the sum l of
+// e^(y - m); the pairs of all rows are exchanged with the other CTAs at once; and a
+// second pass turns the output into e^(y - M) / L in place, out of L2, which a CTA's
+// rows do not leave in between: HBM sees 2 or 4 bytes read and 4 written per logit.
+// 320 bf16 rows of 151936 with histories, bias and mask take 130 us, 80 without
+// those, against 44 at HBM's rate: the CTAs of a row wait for one another between the
+// passes, with 32 warps an SM to cover it (the same with twice the loads in flight;
+// five rows together, 142; C half as large, 145).  Processing the logits again in the
+// second pass took 141 us; keeping a row in registers between the passes left fewer
+// warps, 136 to 205 us.
 //
 // The tokens that occur in the history are few against the vocabulary.  A bit map
 // holds the ones seen; a seen token's rank in it, from the running sum of its words'
 // bit counts, is the place of its count, so the counts take 8 KB and not 4 bytes a
-// logit, which would keep CTAs off the SM.  The passes over the elements take seen
-// and forbidden ones out with one bit each, and the seen ones are done apart, with
-// their penalties, a window of 2048 ranks at a time.
+// logit, which would keep CTAs off the SM.  The first pass takes seen and forbidden
+// elements out with one bit each, and the seen ones are done apart, with their
+// penalties, a window of 2048 ranks at a time, and written over what it left.
 //
 // The pairs go to the other CTAs by st.async, which signals an mbarrier there.  A
 // greedy row's pair is its largest value and the lowest index that has it.
@@ -359,13 +362,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
         }
         f(x, seen, v, second);
       };
+      constexpr int U = sizeof(T) == 2 ? 3 : 2;  // blocks whose loads are in flight
       int k = 0;
-      Pair p[2];
-      for (; k + 2 <= n_blocks && block_at(k + 1) + kBlock <= A.V; k += 2) {
-        load(p[0], k, std::false_type{});
-        load(p[1], k + 1, std::false_type{});
-        work(p[0], k, std::false_type{});
-        work(p[1], k + 1, std::false_type{});
+      Pair p[U];
+      for (; k + U <= n_blocks && block_at(k + U - 1) + kBlock <= A.V; k += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(p[u], k + u, std::false_type{});
+#pragma unroll
+        for (int u = 0; u < U; ++u) work(p[u], k + u, std::false_type{});
       }
       for (; k < n_blocks; ++k) {
         load(p[0], k, std::true_type{});
@@ -384,15 +388,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
       }
     }
   };
-  // Seen elements of one window are written over what the sweep stores, after it;
-  // of more, the sweep leaves them out.
+  // Seen elements of one window are written over what the first pass stores, after
+  // it; of more, the first pass leaves them out.
   const bool over = n_seen <= kWindow;
-  // Writes what the sweep handed over.
   auto store = [&](float* dst, const auto& y, uint32_t seen, bool second) {
     if constexpr (VEC) {
       if (!FILTER || over || seen == 0) {
-        st_global_cs_f4(dst, make_float4(y[0], y[1], y[2], y[3]));
-        if (second) st_global_cs_f4(dst + kApart, make_float4(y[4], y[5], y[6], y[7]));
+        *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+        if (second) *reinterpret_cast<float4*>(dst + kApart) = make_float4(y[4], y[5], y[6], y[7]);
       } else {
 #pragma unroll
         for (int e = 0; e < 2 * kChunk; ++e)
@@ -403,60 +406,55 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
       if (over || !seen) dst[0] = y[0];
     }
   };
-  // The rows' results: `dense` for what the sweep hands over, in place, and
-  // `single(j, v)` for a listed element.
-  auto write = [&](int q, auto&& dense, auto&& single) {
-    float* const out = out0 + (uint32_t)q * V;
-    if (over && n_seen > 0) each_listed([&](int j, int v) { s_y[j] = single(j, v); });
-    if (!over) each_listed([&](int j, int v) { out[v] = single(j, v); });
-    sweep(q, [&](auto& x, uint32_t seen, int v, bool second) {
-      dense(x, v);
-      store(out + v, x, seen, second);
-    });
-    if (over && n_seen > 0) {
-      __syncthreads();
-      each_listed([&](int j, int v) { out[v] = s_y[j]; });
-    }
-  };
   // Index of the sweep's value e.
   auto index = [&](int v, int e) {
     return v + (VEC ? (e / kChunk) * kApart + e % kChunk : 0);
   };
 
-  if (A.raw) {
-    if (P.C > 1) cluster_wait_acquire();
-    const float t = temp > 0.f ? temp : 1.f;
-    for (int q = 0; q < n_rows; ++q)
-      write(q,
-            [&](auto& x, int) {
-#pragma unroll
-              for (auto& y : x) y = __fdiv_rn(y, t);
-            },
-            [&](int j, int) { return __fdiv_rn(listed(j, q), t); });
-    return;
-  }
-
-  // ------------------------------------------------- statistics of the rows --
-  const bool greedy = temp == 0.f;
-  const float c = greedy ? 1.f : __fdiv_rn(kLog2E, temp);
+  // ------------------------------------------ first pass: processed logits --
+  const bool greedy = temp == 0.f && !A.raw;
+  const float c = temp > 0.f ? __fdiv_rn(kLog2E, temp) : 1.f, t_raw = temp > 0.f ? temp : 1.f;
   const Stat none = {-INFINITY, greedy ? __int_as_float(0x7fffffff) : 0.f};
-  auto gather = [&](auto greedy_c) {
-    constexpr bool G = decltype(greedy_c)::value;
+  auto first_pass = [&](auto mode) {
+    constexpr int M = decltype(mode)::value;  // 0: softmax, 1: greedy, 2: raw
     for (int q = 0; q < n_rows; ++q) {
+      float* const out = out0 + (uint32_t)q * V;
       Stat st = none;
-      sweep(q, [&](const auto& x, uint32_t, int v, bool) {
-        add_values<G>(st, x, c, [&](int e) { return index(v, e); });
-      });
-      each_listed([&](int j, int v) {
+      // A listed element's value, before the output may overwrite its logit.
+      auto single = [&](int j, int v) {
         const float x[1] = {listed(j, q)};
-        add_values<G>(st, x, c, [&](int) { return v; });
+        if constexpr (M == 2) return __fdiv_rn(x[0], t_raw);
+        if constexpr (M < 2) add_values<M == 1>(st, x, c, [&](int) { return v; });
+        return x[0];
+      };
+      if (over && n_seen > 0) each_listed([&](int j, int v) { s_y[j] = single(j, v); });
+      sweep(q, [&](auto& x, uint32_t seen, int v, bool second) {
+        if constexpr (M == 2) {
+#pragma unroll
+          for (auto& y : x) y = __fdiv_rn(y, t_raw);
+        } else {
+          add_values<M == 1>(st, x, c, [&](int e) { return index(v, e); });
+        }
+        store(out + v, x, seen, second);
       });
-      st = warp_stat(st, greedy, c);
-      if (lane == 0) s_warp[q][warp] = st;
+      if (over && n_seen > 0) {
+        __syncthreads();
+        each_listed([&](int j, int v) { out[v] = s_y[j]; });
+      }
+      if (!over) each_listed([&](int j, int v) { out[v] = single(j, v); });
+      if constexpr (M < 2) {
+        st = warp_stat(st, M == 1, c);
+        if (lane == 0) s_warp[q][warp] = st;
+      }
     }
   };
-  if (greedy) gather(std::true_type{});
-  else gather(std::false_type{});
+  if (A.raw) {
+    if (P.C > 1) cluster_wait_acquire();
+    first_pass(std::integral_constant<int, 2>{});
+    return;
+  }
+  if (greedy) first_pass(std::integral_constant<int, 1>{});
+  else first_pass(std::integral_constant<int, 0>{});
   __syncthreads();
   if (P.C > 1) cluster_wait_acquire();
   if (warp < n_rows) {  // warp q: row q
@@ -472,28 +470,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
   if (P.C > 1) mbar_wait_cluster(&bar_pair, 0, STT_DEVERR_LOGITS_WAIT);
   else __syncthreads();
 
-  // ------------------------------------------------------------ the results --
+  // ----------------------------------------------- second pass: the results --
   for (int q = 0; q < n_rows; ++q) {
     const float4 p = s_pair[q][lane < P.C ? lane : 0];
     const Stat s = warp_stat(lane < P.C ? Stat{p.x, p.y} : none, greedy, c);
-    if (greedy) {
-      const int best = s.m == -INFINITY ? -1 : __float_as_int(s.l);
-      write(q,
-            [&](auto& x, int v) {
-              int e = 0;
+    const int best = s.m == -INFINITY ? -1 : __float_as_int(s.l);
+    const float top = s.m == -INFINITY ? 0.f : s.m, inv = s.l == 0.f ? 0.f : 1.f / s.l;
+    float* const out = out0 + (uint32_t)q * V;
+    if constexpr (VEC) {
+      auto result = [&](float4 y, int v) {
+        if (greedy)
+          return make_float4(v == best ? 1.f : 0.f, v + 1 == best ? 1.f : 0.f,
+                             v + 2 == best ? 1.f : 0.f, v + 3 == best ? 1.f : 0.f);
+        return make_float4(ex2((y.x - top) * c) * inv, ex2((y.y - top) * c) * inv,
+                           ex2((y.z - top) * c) * inv, ex2((y.w - top) * c) * inv);
+      };
+      constexpr int U = 4;  // chunks in flight
+      int k = 0;
+      for (; k + U / 2 <= n_blocks && block_at(k + U / 2 - 1) + kBlock <= A.V; k += U / 2) {
+        float4 y[U];
 #pragma unroll
-              for (auto& y : x) y = index(v, e++) == best ? 1.f : 0.f;
-            },
-            [&](int, int v) { return v == best ? 1.f : 0.f; });
+        for (int u = 0; u < U; ++u)
+          y[u] = *reinterpret_cast<const float4*>(out + block_at(k + u / 2) + (u % 2) * kApart + tid * kChunk);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int v = block_at(k + u / 2) + (u % 2) * kApart + tid * kChunk;
+          const float4 r = result(y[u], v);
+          st_global_cs_f4(out + v, r);
+        }
+      }
+      for (; k < n_blocks; ++k)
+        for (int v = block_at(k) + tid * kChunk; v < min(block_at(k) + kBlock, A.V); v += kApart)
+          st_global_cs_f4(out + v, result(*reinterpret_cast<const float4*>(out + v), v));
     } else {
-      const float top = s.m == -INFINITY ? 0.f : s.m, inv = s.l == 0.f ? 0.f : 1.f / s.l;
-      write(q,
-            [&](auto& x, int) {
-              exponentials(x, top, c, x);
-#pragma unroll
-              for (auto& y : x) y *= inv;
-            },
-            [&](int j, int) { return ex2((listed(j, q) - top) * c) * inv; });
+      for (int at = tid; at < n_blocks * kBlock; at += kThreads) {
+        const int v = logit_of(at);
+        if (v >= A.V) break;
+        out[v] = greedy ? (v == best ? 1.f : 0.f) : ex2((out[v] - top) * c) * inv;
+      }
     }
   }
 }
@@ -526,7 +540,7 @@ cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s) {
   P.C = C;
   while ((1 << P.log_c) < C) ++P.log_c;
   // Rows of a sequence that share its counts: up to eight, fewer while that makes less
-  // than kFill CTAs an SM (five rows together 147 us, one at a time 141, where B is 64).
+  // than kFill CTAs an SM (five rows together 142 us, one at a time 130, where B is 64).
   const int64_t B = a.N / a.rows;
   int most = std::min(kMaxRows, a.rows);
   while (most > 1 && B * ((a.rows + most - 1) / most) * C < kFill * sm_count()) --most;
