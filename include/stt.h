@@ -447,7 +447,7 @@ STT_API int stt_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, con
  *           token i of n is key seq_len - n + i.
  *  B        0 <= B <= STT_MAX_BATCH.   H_kv >= 1.   D 64 or 128.
  *  page_size a power of two, 8..1024 (STT_ERR_UNSUPPORTED otherwise).
- *  num_pages >= 1, max_pages >= 1; max_pages * page_size < 2^31.
+ *  num_pages >= 1, max_pages >= 1; max_pages * page_size <= 2^30.
  *
  * A page outside [0, num_pages), or a key at or past max_pages * page_size or
  * before 0, is never read or written: it is skipped and reported as
@@ -496,6 +496,9 @@ STT_API size_t stt_paged_attn_workspace_size(int64_t N, int B, int H, int H_kv, 
  *           own bit is set).  New tokens from 32 tree_words on are not seen.
  *  out      bf16 [N, H, D], rounded to nearest even; zeros for a row that sees
  *           nothing.  May not overlap q.
+ * Slots behind a sequence's last key may hold anything.  The values of its own keys
+ * must be finite even where a row does not see them (they meet a zero probability);
+ * keys that a row does not see may hold anything.
  *  lse      fp32 [N, H] or NULL: natural logarithm of the sum of exponentials
  *           of the visible scaled scores, -inf for a row that sees nothing.
  *  workspace at least stt_paged_attn_workspace_size() bytes, 256-byte aligned;

@@ -160,7 +160,7 @@ int check_pages(const stt_pages* p, int64_t N, stt::PagesArgs* g) {
   int shift = 3;
   while (shift < 10 && (1 << shift) != p->page_size) ++shift;
   if ((1 << shift) != p->page_size) return STT_ERR_UNSUPPORTED;
-  if ((int64_t)p->max_pages * p->page_size > 0x7fffffffll) return STT_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages * p->page_size > (1ll << 30)) return STT_ERR_UNSUPPORTED;
   if (p->B > 0 && N > 0) {
     if (!p->k || !p->v || !p->table || !p->cu_q || !p->seq_lens) return STT_ERR_INVALID_ARG;
     if (!aligned16(p->k) || !aligned16(p->v) || !aligned(p->table, 4) || !aligned(p->cu_q, 4) ||

@@ -102,6 +102,11 @@ def _case(B, rows, V, bf16=False, hist=0, draft=False, bias=0, mask=False, pens=
     dict(B=1, rows=2, V=393216, hist=100, draft=True),
     dict(B=6, rows=1, V=4096, pens=False), dict(B=2, rows=3, V=515, pens=False, draft=True),
     dict(B=700, rows=1, V=640, hist=20),
+    dict(B=2, rows=20, V=9000, hist=300, draft=True, mask=True),      # more rows than are taken together
+    dict(B=900, rows=6, V=72, hist=30, draft=True, mask=True, bias=1),  # rows taken together
+    dict(B=900, rows=5, V=70, hist=30, draft=True, greedy=True),
+    dict(B=1, rows=3, V=50000, hist=60000, draft=True, mask=True, bias=1),  # windows of seen tokens
+    dict(B=1, rows=2, V=40001, bf16=True, hist=50000, draft=True, greedy=True),
 ], ids=str)
 @pytest.mark.parametrize("raw", [False, True])
 def test_parity(kw, raw):
@@ -112,6 +117,9 @@ def test_in_place():
     _case(3, 2, 5001, hist=30, draft=True, mask=True, inplace=True)
     _case(3, 2, 5001, hist=30, draft=True, mask=True, inplace=True, raw=True)
     _case(2, 2, 100000, hist=30, draft=True, inplace=True)
+    for raw in (False, True):
+        _case(1, 2, 50000, hist=60000, draft=True, mask=True, inplace=True, raw=raw)
+        _case(900, 5, 72, hist=30, draft=True, inplace=True, raw=raw)
 
 
 def test_plain_softmax_without_arguments():
@@ -168,6 +176,15 @@ def test_visible_infinities():
     assert torch.allclose(out[3], torch.full((1000,), 1e-3))
     hot = ops.stt_logits_process(z.to(DEV), temperature=torch.zeros(4, device=DEV)).cpu()
     assert hot.argmax(1).tolist() == [0, 0, 7, 0] and bool((hot.sum(1) == 1).all())
+
+
+def test_history_lengths_are_kept_within_the_tokens():
+    """cu_tokens past the array's end reads nothing there."""
+    z = torch.randn(2, 500, generator=gen(5)).to(DEV)
+    kw = dict(tokens=_i32([1, 2, 3]), repetition=torch.full((2,), 2.0, device=DEV))
+    a = ops.stt_logits_process(z, cu_tokens=_i32([0, 1, 3]), **kw)
+    b = ops.stt_logits_process(z, cu_tokens=_i32([0, 1, 3000]), **kw)
+    assert torch.equal(a, b)
 
 
 def test_refusals():

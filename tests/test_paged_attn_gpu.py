@@ -117,6 +117,24 @@ def test_more_new_tokens_than_keys():
     assert not out[:6].any() and bool(torch.isinf(lse[:6]).all())
 
 
+def test_many_sequences():
+    """The largest batch, some of it idle, at a head size whose partial rows are odd."""
+    new = [(b * 7) % 4 for b in range(1024)]
+    bt = Batch(new, [n + (b * 13) % 40 for b, n in enumerate(new)], 8, 1, 64, 3, pad=1)
+    _run(bt, 3)
+
+
+def test_a_batch_without_new_tokens():
+    bt = Batch([0, 0], [5, 0], 16, 1, 64, 3, pad=4)
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 5)
+    lse = torch.full((4, 2), 5.0, device=DEV)
+    ops.stt_paged_attn(q, *bt.caches(), *bt.lists(), None, None, out, lse)
+    assert ops.stt_device_error() == 0 and bool((out == 5).all()) and bool((lse == 5).all())
+    none = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    assert ops.stt_paged_attn(none, *bt.caches(), *bt.lists())[0].shape == (0, 2, 64)
+
+
 def test_scale_and_large_scores():
     _run(Batch([4], [500], 32, 2, 128, 4), 4, scale=0.003)
     _run(Batch([4], [500], 32, 2, 128, 4), 4, scale=0.25, std=0.5)
@@ -260,6 +278,40 @@ def test_graph_follows_the_batch_and_streams_do_not_share():
     torch.cuda.synchronize()
     n = int(bt.cu[-1])
     assert all(torch.equal(o[:n], want[0][:n]) and torch.equal(l[:n], want[1][:n]) for o, l in got)
+
+
+def test_first_call_inside_a_capture():
+    """In a fresh process, with nothing of the library loaded on the device before."""
+    import subprocess
+    import sys
+    code = """
+import sys; sys.path.insert(0, "tests"); sys.path.insert(0, ".")
+import torch
+from _serving import Batch, gen, randn
+from speculative_decoding_draft_eagle_gb300 import ops
+bt = Batch([3, 2], [150, 70], 16, 2, 128, 6)
+kc, vc = bt.caches()
+lists = bt.lists()
+qkv = randn(gen(1), bt.N, 12 * 128).cuda()
+freq = ops.rope_frequencies(128)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q = ops.stt_kv_append(qkv, 8, kc, vc, *lists, None, freq)
+    out, lse = ops.stt_paged_attn(q, kc, vc, *lists)
+    p = ops.stt_logits_process(out.flatten(1).float())
+g.replay()
+q2 = ops.stt_kv_append(qkv, 8, kc, vc, *lists, None, freq)
+o2, l2 = ops.stt_paged_attn(q2, kc, vc, *lists)
+assert torch.equal(o2, out) and torch.equal(l2, lse)
+assert torch.equal(ops.stt_logits_process(o2.flatten(1).float()), p)
+assert ops.stt_device_error() == 0
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_refusals():

@@ -198,11 +198,12 @@ APPEND = [([1], [1], 16, "heads", 4, 2, 128, 128, False, True),
           ([3, 0, 5], [3, 9, 40], 16, "tokens", 4, 2, 64, 32, True, False),
           ([17, 1, 130], [100, 129, 130], 8, "both", 7, 1, 128, 128, False, True),
           ([33] * 40, [33 + 7 * b for b in range(40)], 32, "heads", 2, 2, 64, 64, False, True),
-          ([0, 0, 9, 0], [0, 5, 300, 0], 1024, "tokens", 8, 1, 128, 64, True, True)]
+          ([0, 0, 9, 0], [0, 5, 300, 0], 1024, "tokens", 8, 1, 128, 64, True, True),
+          ([1, 0, 2] * 341 + [700], [9, 0, 40] * 341 + [900], 16, "heads", 5, 3, 64, 48, False, True)]
 
 
 @pytest.mark.parametrize("explicit", [False, True])
-@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"{c[2]}-{c[3]}")
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"{len(c[0])}x{sum(c[0])}p{c[2]}-{c[3]}")
 def test_append(case, explicit):
     new, lens, page, layout, H, H_kv, D, R, inter, norm = case
     bt = Batch(new, lens, page, H_kv, D, 3, pad=4, layout=layout)
