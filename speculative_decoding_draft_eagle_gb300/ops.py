@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+import threading
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -431,7 +432,23 @@ def _rows(t, name, shape, dev):
 
 
 def _new(shape, dtype, dev):
-    return torch.empty(shape, device=torch.device("cuda", dev), dtype=dtype)
+    return torch.empty(shape, device=dev, dtype=dtype)
+
+
+_scratch_of = threading.local()
+
+
+def _scratch(n: int, dev: int, raw: int, stream) -> torch.Tensor:
+    """A workspace of n bytes for one call.  Eager calls of a thread on its current
+    stream follow one another there and share one, kept from call to call; a call that
+    is captured, or goes to another stream, has its own."""
+    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
+        return _new((n,), torch.uint8, dev)
+    kept = _scratch_of.__dict__
+    t = kept.get((dev, raw))
+    if t is None or t.numel() < n:
+        t = kept[dev, raw] = _new((n,), torch.uint8, dev)
+    return t
 
 
 def _keep(stream, *ts):
@@ -576,9 +593,12 @@ def stt_qkv_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
         p_wk = _arg(dw_k, "dw_k", torch.float32, (D,), dev)
     if norm:
         if workspace is None:
-            workspace = _new((stt_qkv_rope_bwd_workspace_size(D),), torch.uint8, dev)
-        p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
-        n_ws = workspace.numel() * workspace.element_size()
+            n_ws = lib().stt_qkv_rope_bwd_workspace_size(D)
+            workspace = _scratch(n_ws, dev, raw, stream)
+            p_ws = workspace.data_ptr()
+        else:
+            p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+            n_ws = workspace.numel() * workspace.element_size()
     st = lib().stt_qkv_rope_bwd(
         p_dq, p_dk, p_dv, x, ld,
         None if positions is None else _arg(positions, "positions", torch.int32, (B, S), dev),
@@ -691,13 +711,16 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         lse = _new((N, H), torch.float32, dev)
     L = lib()
     if workspace is None:
-        workspace = _new((L.stt_paged_attn_workspace_size(N, B, H, H_kv, D),), torch.uint8, dev)
+        n_ws = L.stt_paged_attn_workspace_size(N, B, H, H_kv, D)
+        workspace = _scratch(n_ws, dev, raw, stream)
+        p_ws = workspace.data_ptr()
+    else:
+        p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        n_ws = workspace.numel() * workspace.element_size()
     st = L.stt_paged_attn(
         q.data_ptr(), ld, N, H, pages, D ** -0.5 if scale is None else scale, tree, words,
         _arg(out, "out", torch.bfloat16, (N, H, D), dev),
-        _arg(lse, "lse", torch.float32, (N, H), dev),
-        _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
-        workspace.numel() * workspace.element_size(), raw)
+        _arg(lse, "lse", torch.float32, (N, H), dev), p_ws, n_ws, raw)
     if st:
         check("stt_paged_attn", st)
     if stream is not None:
