@@ -3,10 +3,16 @@
 // queries and a paged KV cache (serving), and the training form's gradient.
 //
 // All three are one pass over memory: a warp takes a token (or a part of its
-// heads, where there are too few tokens to fill the GPU), makes the token's
-// tables of cosines, sines and weights once (rope.cuh), and streams the token's
-// heads through them, 32 / (D / 8) heads a step, 16-byte loads and stores, a few
-// steps' loads in flight at a time.
+// heads), fills its table of cosines and sines, and streams the token's heads, 32 / (D
+// / 8) of them a step, four steps' loads in flight.  HBM bounds them where there are
+// many tokens: 8192 tokens of 32 + 16 heads of 128 take 37 us forward (5.5 TB/s, 0.81 of
+// the copy rate; 41 with norms), 2 x 4096 tokens of 64 + 16 heads 113 us backward with
+// norms and fp32 gradients (5.8 TB/s, 0.86).  What moved them there was fewer
+// instructions, not more bytes in flight: 185 a step became about 80 when both elements
+// of a pair came to one lane and arithmetic went in pairs of floats (166 to 113 us
+// backward), while a ring of bulk copies ahead of the warps took 166 to 276 us, and
+// tiles of eight tokens with the warps dividing the heads 147.  Few tokens are bound
+// by the launch and a chain of dependent loads (8 us for 64 sequences of 8 tokens).
 #include <algorithm>
 #include <type_traits>
 
@@ -401,26 +407,24 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   }
 }
 
-// dw = sum of the blocks' partials, in a fixed order: thread (y, x) adds rows y,
-// y + 8, ..., then the eight of an element are added.
+// dw = sum of the blocks' partials, in a fixed order: block (kind, 32 elements); warp w
+// adds rows w, w + 32, ..., then the 32 sums of an element are added.
 __global__ void __launch_bounds__(1024) qkv_rope_dw_kernel(const float* partial, int rows, int D,
                                                            float* dw_q, float* dw_k) {
-  __shared__ float sm[8][128];
-  const int x = threadIdx.x & 127, y = threadIdx.x >> 7;
+  __shared__ float sm[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = blockIdx.y * 32 + lane;
   float* const dst = blockIdx.x ? dw_k : dw_q;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!dst) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.f;
-  if (x < D)
 #pragma unroll 8
-    for (int r = y; r < rows; r += 8) v += partial[((int64_t)r * 2 + blockIdx.x) * D + x];
-  sm[y][x] = v;
+  for (int r = warp; r < rows; r += 32) v += partial[((int64_t)r * 2 + blockIdx.x) * D + x];
+  sm[warp][lane] = v;
   __syncthreads();
-  if (y == 0 && x < D) {
+  v = sm[lane][warp];  // warp w: element w's sums
 #pragma unroll
-    for (int j = 1; j < 8; ++j) v += sm[j][x];
-    dst[x] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) dst[blockIdx.y * 32 + warp] = v;
 }
 
 template <int D, class T>
@@ -509,7 +513,7 @@ cudaError_t qkv_rope_bwd_launch(const RopeArgs& r, const void* dq, const void* d
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && (dw_q || dw_k)) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, 1, 1);
+    cfg.gridDim = dim3(2, (unsigned)(D / 32), 1);
     cfg.blockDim = dim3(1024, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute la[1];
