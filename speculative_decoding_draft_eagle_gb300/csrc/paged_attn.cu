@@ -8,10 +8,15 @@
 // in tensor memory), keys and values brought page by page by TMA into swizzled
 // shared memory, softmax with a running maximum and sum in between.
 //
-// Persistent, one CTA per SM.  Every key tile of every unit counts one, and CTA c
-// takes the tiles [c W / G, (c + 1) W / G) of all W in the order (sequence, KV
-// head, query tile, key tile): whatever the lengths, the CTAs' shares differ by
-// one tile at most.  A unit cut by a share's border leaves partial results
+// Persistent, one CTA per SM.  Every key tile of every unit counts one, and a share
+// is a run of tiles in the order (sequence, KV head, query tile, key tile), cut where
+// it comes: CTA c takes the tiles [c W / G, (c + 1) W / G) of all W, so that whatever
+// the lengths, the shares differ by one tile at most.  Where there are two units or
+// more to a CTA, whole ones are dealt first, a round of G neighbours at a time: they
+// are query tiles of a few heads, which go through the same keys side by side, out of
+// L2 (dealt in runs alone, chunks on 170 MB of keys read 1.9 GB from HBM, 0.18 this
+// way).  The units left, between one and two to a CTA, go in runs that make the CTAs'
+// totals even.  A unit cut by a share's border leaves partial results
 // (normalised rows and their logarithms of the sum) in the workspace, at most two
 // per CTA, and a second small kernel, launched as a programmatic dependent, joins
 // them in a fixed order.  The lengths are read on the device: nothing here depends
@@ -20,8 +25,7 @@
 // What bounds it: HBM for few new tokens (six tokens on each of four contexts of 90 to
 // 131 thousand keys, 32 query and 8 KV heads of 128: 260 us, 6.68 TB/s, 0.98 of the copy
 // rate), the tensor cores with the softmax between them for chunks (500 to 2048 tokens
-// on 4 to 16 thousand keys: 623 us, 1156 TFLOP/s, 0.60 of cuBLAS's burst; 1256 with the
-// keys in L2).  With units of a few tiles, each one's end (the last product, the rows
+// on 4 to 16 thousand keys: 599 us, 1202 TFLOP/s, 0.63 of cuBLAS's burst).  With units of a few tiles, each one's end (the last product, the rows
 // out, at most three pipelines refilled) shows: trees of 16 tokens on 32 sequences of
 // 500 to 4000 keys take 65 us, 0.64 of the copy rate.  One token on 777 keys takes 14 us,
 // 10 of them this kernel's chain for a single tile and 4 the join's.  The same kernel
@@ -91,8 +95,23 @@ struct Smem {
 // The batch in shared memory.
 struct Batch {
   long long pref[kMaxBatch + 1];  // tiles before each sequence
+  int units[kMaxBatch + 1];       // units before each sequence
   int first[kMaxBatch], n[kMaxBatch], len[kMaxBatch];
+  long long start[kMaxCtas + 1];  // the CTAs' runs of tiles
+  unsigned long long dealt[kMaxCtas];  // tiles of the whole units dealt to each CTA
+  int rounds;                     // rounds of whole units
 };
+
+// The last sequence whose entry of a running sum is not above x.
+template <class T>
+__device__ __forceinline__ int seq_of(const T* sums, int B, T x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sums[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
 
 // Keys the query tile j of a sequence needs.
 __device__ __forceinline__ int unit_keys(const Params& P, int n, int len, int j) {
@@ -116,28 +135,44 @@ struct Seg {
   long long u0;  // the unit's first tile in the order of all
 };
 
+__device__ __forceinline__ int unit_cost(const Params& P, const Batch& S, int b, int j) {
+  return max(tiles_of(unit_keys(P, S.n[b], S.len[b], j)), 1);
+}
+// Unit u in the order of all: its sequence, head and query tile.
+__device__ __forceinline__ void unit_at(const Params& P, const Batch& S, int u, int& b, int& h,
+                                        int& j) {
+  b = seq_of(S.units, P.g.B, u);
+  const int tiles = (S.n[b] + P.TT - 1) / P.TT, r = u - S.units[b];
+  h = r / tiles;
+  j = r - h * tiles;
+}
+// Unit that CTA c of n takes in a round (snake order).
+__device__ __forceinline__ int dealt_unit(int round, int c, int n) {
+  return round * n + ((round & 1) ? n - 1 - c : c);
+}
+
+// A CTA's segments: the whole units dealt to it, then its run of tiles.
 struct Walk {
   long long pos, end;
-  int b, h, j, off;
+  int b, h, j, off, round, c, n;
 
-  __device__ __forceinline__ void init(const Params& P, const Batch& S, long long c, long long n) {
-    const int B = P.g.B;
-    const long long W = S.pref[B];
-    pos = div_ll(W * c, n);
-    end = div_ll(W * (c + 1), n);
-    if (pos >= end) return;
-    int lo = 0, hi = B - 1;  // last sequence with pref <= pos and tiles of its own
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (S.pref[mid] <= pos) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
+  __device__ __forceinline__ void init(const Batch& S, int cta, int ctas) {
+    c = cta;
+    n = ctas;
+    round = 0;
+    pos = S.start[c];
+    end = S.start[c + 1];
+    off = -1;  // its place is looked up when the run begins
+  }
+
+  __device__ __forceinline__ void locate(const Params& P, const Batch& S) {
+    b = seq_of(S.pref, P.g.B, pos);
     long long rem = pos - S.pref[b];
     const long long per_head = div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
     h = (int)div_ll(rem, per_head);
     rem -= h * per_head;
     for (j = 0;; ++j) {
-      const int cost = max(tiles_of(unit_keys(P, S.n[b], S.len[b], j)), 1);
+      const int cost = unit_cost(P, S, b, j);
       if (rem < cost) break;
       rem -= cost;
     }
@@ -145,30 +180,43 @@ struct Walk {
   }
 
   __device__ __forceinline__ bool next(const Params& P, const Batch& S, Seg& s) {
-    if (pos >= end) return false;
-    s.b = b;
-    s.h = h;
-    s.j = j;
-    s.n = S.n[b];
-    s.ctx = S.len[b] - s.n;
-    s.keys = unit_keys(P, s.n, S.len[b], j);
-    s.tiles = tiles_of(s.keys);
-    s.tok0 = S.first[b] + j * P.TT;
-    s.ntok = min(P.TT, s.n - j * P.TT);
-    s.u0 = pos - off;
-    const int cost = max(s.tiles, 1);
-    const long long left = end - pos;
-    s.t0 = off;
-    s.t1 = (long long)(cost - off) <= left ? cost : off + (int)left;
-    pos += s.t1 - s.t0;
-    off = 0;
-    if ((j + 1) * P.TT < s.n) {
-      ++j;
+    const bool whole = round < S.rounds;
+    if (whole) {
+      unit_at(P, S, dealt_unit(round, c, n), s.b, s.h, s.j);
+      ++round;
     } else {
-      j = 0;
-      if (++h == P.g.H_kv) {
-        h = 0;
-        do ++b; while (b < P.g.B && S.n[b] <= 0);
+      if (pos >= end) return false;
+      if (off < 0) locate(P, S);
+      s.b = b;
+      s.h = h;
+      s.j = j;
+    }
+    s.n = S.n[s.b];
+    s.ctx = S.len[s.b] - s.n;
+    s.keys = unit_keys(P, s.n, S.len[s.b], s.j);
+    s.tiles = tiles_of(s.keys);
+    s.tok0 = S.first[s.b] + s.j * P.TT;
+    s.ntok = min(P.TT, s.n - s.j * P.TT);
+    const int cost = max(s.tiles, 1);
+    if (whole) {
+      s.t0 = 0;
+      s.t1 = cost;
+      s.u0 = 0;  // of cut units only
+    } else {
+      s.u0 = pos - off;
+      const long long left = end - pos;
+      s.t0 = off;
+      s.t1 = (long long)(cost - off) <= left ? cost : off + (int)left;
+      pos += s.t1 - s.t0;
+      off = 0;
+      if ((j + 1) * P.TT < s.n) {
+        ++j;
+      } else {
+        j = 0;
+        if (++h == P.g.H_kv) {
+          h = 0;
+          do ++b; while (b < P.g.B && S.n[b] <= 0);
+        }
       }
     }
     if (s.tiles == 0) s.t0 = s.t1 = 0;  // its place in the order is not a tile
@@ -183,6 +231,57 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
   const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? __ldg(row + w) : 0u);
   const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? __ldg(row + w + 1) : 0u);
   return __funnelshift_r(lo, hi, o & 31);
+}
+
+// The CTAs' runs over the units that are left when `rounds` rounds of whole ones are
+// dealt: each gets what its dealt units leave of an even total (one tile at least).
+// Every CTA works the same plan out; the whole block calls this.
+__device__ __noinline__ void plan_runs(const Params& P, Batch& S, long long W, int n, int rounds) {
+  const int tid = threadIdx.x;
+  for (int c = tid; c < n; c += kThreads) S.dealt[c] = 0;
+  __syncthreads();
+  for (int u = tid; u < rounds * n; u += kThreads) {
+    int b, h, j;
+    unit_at(P, S, u, b, h, j);
+    const int round = u / n, x = u - round * n;
+    atomicAdd(&S.dealt[(round & 1) ? n - 1 - x : x], (unsigned long long)unit_cost(P, S, b, j));
+  }
+  __syncthreads();
+  if (tid < 32) {
+    long long first;  // tiles before the units left
+    {
+      int b, h, j;
+      unit_at(P, S, rounds * n, b, h, j);
+      first = S.pref[b] + div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv) * h;
+      for (int x = 0; x < j; ++x) first += unit_cost(P, S, b, x);
+    }
+    const long long left = W - first, even = div_ll(W, n);
+    constexpr int kPer = (kMaxCtas + 31) / 32;
+    long long need[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = tid * kPer + i;
+      need[i] = c < n ? max(even - (long long)S.dealt[c] - 1, 0ll) : 0;
+      sum += need[i];
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    const long long all = __shfl_sync(0xffffffffu, incl, 31);
+    long long before = incl - sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = tid * kPer + i;
+      if (c < n)
+        S.start[c] = first + c +
+                     (all > 0 ? (long long)((double)before / (double)all * (double)(left - n)) : 0);
+      before += need[i];
+    }
+    if (tid == 0) S.start[n] = W;
+  }
 }
 
 template <int D>
@@ -254,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long t = 0;
     for (long long j = lane; j * P.TT < n; j += 32)
       t += max(tiles_of(unit_keys(P, n, len, (int)j)), 1);
+    if (lane == 0) S.units[b + 1] = (n + P.TT - 1) / P.TT * P.g.H_kv;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
@@ -261,17 +361,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     long long carry = 0;
-    if (lane == 0) S.pref[0] = 0;
+    int carry_u = 0;
+    if (lane == 0) {
+      S.pref[0] = 0;
+      S.units[0] = 0;
+    }
     for (int b0 = 0; b0 < B; b0 += 32) {
       long long v = b0 + lane < B ? S.pref[b0 + lane + 1] : 0;
+      int u = b0 + lane < B ? S.units[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        const long long v1 = __shfl_up_sync(0xffffffffu, v, o);
+        const int u1 = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) {
+          v += v1;
+          u += u1;
+        }
       }
       v += carry;
-      if (b0 + lane < B) S.pref[b0 + lane + 1] = v;
+      u += carry_u;
+      if (b0 + lane < B) {
+        S.pref[b0 + lane + 1] = v;
+        S.units[b0 + lane + 1] = u;
+      }
       carry = __shfl_sync(0xffffffffu, v, 31);
+      carry_u = __shfl_sync(0xffffffffu, u, 31);
     }
   }
   tc_fence_before();
@@ -280,9 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base;
   const long long W = S.pref[B];
   const int ctas = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
+  const int rounds = S.units[B] >= 2 * (int)gridDim.x ? S.units[B] / (int)gridDim.x - 1 : 0;
+  if (rounds == 0) {
+    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = div_ll(W * c, max(ctas, 1));
+  } else {
+    plan_runs(P, S, W, ctas, rounds);
+  }
+  if (tid == 0) S.rounds = rounds;
+  __syncthreads();
   Walk walk;
   walk.pos = walk.end = 0;
-  if ((int)blockIdx.x < ctas) walk.init(P, S, blockIdx.x, ctas);
+  walk.round = rounds;
+  if ((int)blockIdx.x < ctas) walk.init(S, blockIdx.x, ctas);
   Seg s;
 
   if (warp == kWarpK || warp == kWarpV) {
@@ -425,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         joined = true;
         const long long last = s.u0 + s.tiles - 1;
         JoinDesc d;
-        d.c0 = (int)div_ll((s.u0 + 1) * ctas - 1, W);
-        d.c1 = (int)div_ll((last + 1) * ctas - 1, W);
+        d.c0 = seq_of(S.start, ctas, s.u0);
+        d.c1 = seq_of(S.start, ctas, last);
         d.tok0 = s.tok0;
         d.ntok = s.ntok;
         d.kvh = s.h;

@@ -124,6 +124,14 @@ def test_many_sequences():
     _run(bt, 3)
 
 
+def test_trees_with_whole_units_dealt():
+    """Enough units for rounds of whole ones, under a mask, every row checked."""
+    n = 20
+    bt = Batch([n] * 24, [n + 37 * b for b in range(24)], 16, 8, 64, 5)
+    rng = np.random.default_rng(2)
+    _run(bt, 16 * 8, rng.random((bt.N, n)) < 0.5)
+
+
 def test_a_batch_without_new_tokens():
     bt = Batch([0, 0], [5, 0], 16, 1, 64, 3, pad=4)
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)
@@ -140,15 +148,20 @@ def test_scale_and_large_scores():
     _run(Batch([4], [500], 32, 2, 128, 4), 4, scale=0.25, std=0.5)
 
 
-def test_long_prompt_and_many_items():
+@pytest.mark.parametrize("new,lens,H_kv", [
+    ([1300, 257, 1], [1700, 2048, 3000], 4),               # runs of tiles alone
+    ([1300, 0, 257, 1, 900], [1700, 5, 2048, 3000, 900], 8),  # whole units dealt first
+    ([2500, 40], [2500, 4000], 8)])
+def test_long_prompt_and_many_items(new, lens, H_kv):
     """More tiles than SMs, ragged, with rows checked on a sample of heads."""
-    new, lens = [1300, 257, 1], [1700, 2048, 3000]
-    bt = Batch(new, lens, 64, 4, 128, 11)
-    H, D = 16, 128
+    bt = Batch(new, lens, 64, H_kv, 128, 11)
+    H, D = 4 * H_kv, 128
     q = randn(gen(3), bt.N, H, D)
     out, lse = ops.stt_paged_attn(q.to(DEV), *bt.caches(), *bt.lists())
     assert ops.stt_device_error() == 0
     for b, (first, n, L) in enumerate(zip(bt.cu, new, lens)):
+        if n == 0:
+            continue
         k, v = opg.gather(f64(bt.k), bt.table[b], L), opg.gather(f64(bt.v), bt.table[b], L)
         for h in range(0, H, 5):
             s = f64(q)[first: first + n, h] @ k[:, h // 4].T / math.sqrt(D)
