@@ -16,7 +16,10 @@
 // are query tiles of a few heads, which go through the same keys side by side, out of
 // L2 (dealt in runs alone, chunks on 170 MB of keys read 1.9 GB from HBM, 0.18 this
 // way).  The units left, between one and two to a CTA, go in runs that make the CTAs'
-// totals even.  A unit cut by a share's border leaves partial results
+// totals even.  With 0.8 to 2 units to a CTA one round is dealt if the keys that several
+// query tiles read are more than L2 keeps and the units are about as long as one
+// another (500 tokens on 120 thousand keys: 888 TFLOP/s in runs, ROUND_TF dealt).  A unit
+// cut by a share's border leaves partial results
 // (normalised rows and their logarithms of the sum) in the workspace, at most two
 // per CTA, and a second small kernel, launched as a programmatic dependent, joins
 // them in a fixed order.  The lengths are read on the device: nothing here depends
@@ -55,6 +58,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpPv = 10, kWarpV = 11;
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;  // CTAs the workspace has room for
+constexpr unsigned long long kL2Keeps = 64ull << 20;  // bytes of keys and values, about
 constexpr int kJoinThreads = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 2^8 between rescales
 constexpr uint32_t kTmemCols = 512;
@@ -99,6 +103,8 @@ struct Batch {
   int first[kMaxBatch], n[kMaxBatch], len[kMaxBatch];
   long long start[kMaxCtas + 1];  // the CTAs' runs of tiles
   unsigned long long dealt[kMaxCtas];  // tiles of the whole units dealt to each CTA
+  unsigned long long most;        // the largest of them
+  unsigned long long shared;      // keys that several query tiles read
   int rounds;                     // rounds of whole units
 };
 
@@ -233,29 +239,47 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
   return __funnelshift_r(lo, hi, o & 31);
 }
 
-// The CTAs' runs over the units that are left when `rounds` rounds of whole ones are
-// dealt: each gets what its dealt units leave of an even total (one tile at least).
-// Every CTA works the same plan out; the whole block calls this.
-__device__ __noinline__ void plan_runs(const Params& P, Batch& S, long long W, int n, int rounds) {
+// Deals `rounds` rounds of whole units to n CTAs, and gives the units left to their runs:
+// each gets what its dealt units leave of an even total (one tile at least).  False if
+// the dealt units are too uneven for that (one round only).  Every CTA works the same
+// plan out; the whole block calls this.
+__device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int rounds) {
   const int tid = threadIdx.x;
+  const long long W = S.pref[P.g.B], units = S.units[P.g.B];
   for (int c = tid; c < n; c += kThreads) S.dealt[c] = 0;
+  if (tid == 0) S.most = 0;
   __syncthreads();
   for (int u = tid; u < rounds * n; u += kThreads) {
     int b, h, j;
     unit_at(P, S, u, b, h, j);
     const int round = u / n, x = u - round * n;
-    atomicAdd(&S.dealt[(round & 1) ? n - 1 - x : x], (unsigned long long)unit_cost(P, S, b, j));
+    const unsigned long long cost = (unsigned long long)unit_cost(P, S, b, j);
+    atomicAdd(&S.dealt[(round & 1) ? n - 1 - x : x], cost);
+    if (rounds == 1) atomicMax(&S.most, cost);
   }
   __syncthreads();
+  const long long even = div_ll(W, n);
+  const bool none_left = units == (long long)rounds * n;
+  long long first = W;  // tiles before the units left
+  if (!none_left) {
+    int b, h, j;
+    unit_at(P, S, rounds * n, b, h, j);
+    first = S.pref[b] + div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv) * h;
+    for (int x = 0; x < j; ++x) first += unit_cost(P, S, b, x);
+  }
+  const long long left = W - first;
+  if (rounds == 1) {
+    // One unit each: no longer than a quarter over an even share of all SMs.  A unit each
+    // and a run: within a tenth of an even total.
+    if (none_left ? (long long)S.most * gridDim.x * 4 > W * 5
+                  : left < n || (long long)S.most * 10 > even * 11)
+      return false;
+  }
+  if (none_left) {
+    for (int c = tid; c <= n; c += kThreads) S.start[c] = W;
+    return true;
+  }
   if (tid < 32) {
-    long long first;  // tiles before the units left
-    {
-      int b, h, j;
-      unit_at(P, S, rounds * n, b, h, j);
-      first = S.pref[b] + div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv) * h;
-      for (int x = 0; x < j; ++x) first += unit_cost(P, S, b, x);
-    }
-    const long long left = W - first, even = div_ll(W, n);
     constexpr int kPer = (kMaxCtas + 31) / 32;
     long long need[kPer], sum = 0;
 #pragma unroll
@@ -282,6 +306,7 @@ __device__ __noinline__ void plan_runs(const Params& P, Batch& S, long long W, i
     }
     if (tid == 0) S.start[n] = W;
   }
+  return true;
 }
 
 template <int D>
@@ -313,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpK) tma_prefetch_desc(&tmQ);
   }
   if (tid == 0) {
+    S.shared = 0;
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar_q_full[x], 1);
       mbar_init(&bar_q_empty[x], 1);
@@ -353,7 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long t = 0;
     for (long long j = lane; j * P.TT < n; j += 32)
       t += max(tiles_of(unit_keys(P, n, len, (int)j)), 1);
-    if (lane == 0) S.units[b + 1] = (n + P.TT - 1) / P.TT * P.g.H_kv;
+    if (lane == 0) {
+      S.units[b + 1] = (n + P.TT - 1) / P.TT * P.g.H_kv;
+      if (n > 3 * P.TT && len > 0) atomicAdd(&S.shared, (unsigned long long)len);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
@@ -393,13 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const long long W = S.pref[B];
-  const int ctas = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
-  const int rounds = S.units[B] >= 2 * (int)gridDim.x ? S.units[B] / (int)gridDim.x - 1 : 0;
-  if (rounds == 0) {
-    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = div_ll(W * c, max(ctas, 1));
-  } else {
-    plan_runs(P, S, W, ctas, rounds);
+  const int grid = (int)gridDim.x, units = S.units[B];
+  int ctas = (int)(W < (long long)grid ? W : (long long)grid), rounds = 0;
+  if (units >= 2 * grid) {
+    rounds = units / grid - 1;
+  } else if ((long long)units * 5 >= (long long)grid * 4 &&
+             S.shared * (unsigned long long)(P.g.H_kv * D * 4) > kL2Keeps) {
+    rounds = 1;
   }
+  if (rounds > 0) {
+    const int n = min(units, grid);
+    if (plan_rounds(P, S, n, rounds)) ctas = n;
+    else rounds = 0;
+  }
+  if (rounds == 0)
+    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = div_ll(W * c, max(ctas, 1));
   if (tid == 0) S.rounds = rounds;
   __syncthreads();
   Walk walk;
@@ -558,11 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int live = s.ntok * P.G;             // live rows of the tile
       const bool dead = quarter * 32 >= live;    // none in this quarter
       const bool row_live = r < live;
-      const int q_tok = s.j * P.TT + t_row;      // new token of this row
-      int lim = P.tree ? s.keys - 1 : min(s.ctx + q_tok, s.keys - 1);
-      if (!row_live) lim = -1;
+      // Rows behind the live ones go with the last of them, so that a warp that has both
+      // stays on one path (masked on their own they cost every tile a second one, half
+      // as long again); nothing of them is written.
+      const int t_seen = min(t_row, s.ntok - 1);
+      const int q_tok = s.j * P.TT + t_seen;     // new token of this row
+      const int lim = P.tree ? s.keys - 1 : min(s.ctx + q_tok, s.keys - 1);
       const uint32_t* tree_row =
-          P.tree && row_live ? P.tree + (int64_t)(s.tok0 + t_row) * P.tree_words : nullptr;
+          P.tree ? P.tree + (int64_t)(s.tok0 + t_seen) * P.tree_words : nullptr;
 
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = s.t0; ok && t < s.t1; ++t, ++g) {

@@ -151,7 +151,9 @@ def test_scale_and_large_scores():
 @pytest.mark.parametrize("new,lens,H_kv", [
     ([1300, 257, 1], [1700, 2048, 3000], 4),               # runs of tiles alone
     ([1300, 0, 257, 1, 900], [1700, 5, 2048, 3000, 900], 8),  # whole units dealt first
-    ([2500, 40], [2500, 4000], 8)])
+    ([2500, 40], [2500, 4000], 8),
+    ([500], [33000], 8),                                   # a unit to most CTAs
+    ([700], [33000], 8)])                                  # a unit each, and runs
 def test_long_prompt_and_many_items(new, lens, H_kv):
     """More tiles than SMs, ragged, with rows checked on a sample of heads."""
     bt = Batch(new, lens, 64, H_kv, 128, 11)
