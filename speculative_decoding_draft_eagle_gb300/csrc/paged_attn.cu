@@ -137,6 +137,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 // Part of one unit in a CTA's share: key tiles [t0, t1) of `tiles`.
 struct Seg {
   int b, h, j, t0, t1, tiles, keys;
+  int have;  // keys of the sequence; `keys` are those that the unit sees
   int tok0, ntok, n, ctx;
   long long u0;  // the unit's first tile in the order of all
 };
@@ -200,6 +201,7 @@ struct Walk {
     s.n = S.n[s.b];
     s.ctx = S.len[s.b] - s.n;
     s.keys = unit_keys(P, s.n, S.len[s.b], s.j);
+    s.have = max(min(S.len[s.b], P.key_cap), 0);
     s.tiles = tiles_of(s.keys);
     s.tok0 = S.first[s.b] + s.j * P.TT;
     s.ntok = min(P.TT, s.n - s.j * P.TT);
@@ -285,7 +287,9 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int c = tid * kPer + i;
-      need[i] = c < n ? max(even - (long long)S.dealt[c] - 1, 0ll) : 0;
+      // (One over the quotient, less the one that every run has: where the quotient has
+      // lost a fraction, all of them stay in proportion.)
+      need[i] = c < n ? max(even - (long long)S.dealt[c], 0ll) : 0;
       sum += need[i];
     }
     long long incl = sum;
@@ -472,17 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_issued = i + 1;
       }
       const int32_t* table = P.g.table + (int64_t)s.b * P.g.max_pages;
-      // This lane's page of a tile (-1: past the unit's keys).
+      // This lane's page of a tile (-1: past the sequence's keys).
       auto look = [&](int t) {
         const int key = t * kTile + lane * box;
-        return lane < copies && t < s.t1 && key < s.keys ? __ldg(table + (key >> P.g.page_shift))
+        return lane < copies && t < s.t1 && key < s.have ? __ldg(table + (key >> P.g.page_shift))
                                                           : -1;
       };
       int pg = look(s.t0);
       for (int t = s.t0; t < s.t1; ++t, ++g) {
         const int st = g & 1;
         const int key = t * kTile + lane * box;
-        const bool mine = lane < copies && key < s.keys;
+        const bool mine = lane < copies && key < s.have;
         int p = pg;
         pg = look(t + 1);
         if (mine && (p < 0 || p >= P.g.num_pages)) {
@@ -609,13 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sb = (int)(g % kSBufs);
         ok = warp_wait(&bar_s_full[sb], (g / kSBufs) & 1u, kSite);
         if (!ok) break;
-        // Values behind the unit's last key may be anything: zeros, so that the
+        // Values behind the sequence's last key may be anything: zeros, so that the
         // products with their zero probabilities vanish.  These warps do not follow
         // v_full's phases in turn, so they make sure first that the phase before
         // V(g)'s is over: O += P(g-2) V, which consumed that stage's last values.
         // (S(g) is there, so O += P(g-3) V and all before it are complete, and the
         // phase of o_done waited for is its barrier's current or latest one.)
-        const int behind = s.keys - t * kTile;
+        const int behind = s.have - t * kTile;
         if (behind < kTile) {
           const int st = g & 1;
           if (g >= (uint32_t)kStages) ok = warp_wait(&bar_o_done[g & 1], ((g >> 1) - 1u) & 1u, kSite);
