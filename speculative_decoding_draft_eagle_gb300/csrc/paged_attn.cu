@@ -18,7 +18,7 @@
 // way).  The units left, between one and two to a CTA, go in runs that make the CTAs'
 // totals even.  With 0.8 to 2 units to a CTA one round is dealt if the keys that several
 // query tiles read are more than L2 keeps and the units are about as long as one
-// another (500 tokens on 120 thousand keys: 888 TFLOP/s in runs, ROUND_TF dealt).  A unit
+// another (500 tokens on 120 thousand keys: 888 TFLOP/s in runs, 1157 dealt).  A unit
 // cut by a share's border leaves partial results
 // (normalised rows and their logarithms of the sum) in the workspace, at most two
 // per CTA, and a second small kernel, launched as a programmatic dependent, joins
@@ -102,10 +102,11 @@ struct Batch {
   int units[kMaxBatch + 1];       // units before each sequence
   int first[kMaxBatch], n[kMaxBatch], len[kMaxBatch];
   long long start[kMaxCtas + 1];  // the CTAs' runs of tiles
-  unsigned long long dealt[kMaxCtas];  // tiles of the whole units dealt to each CTA
-  unsigned long long most;        // the largest of them
+  long long dealt[2][kMaxCtas];   // tiles of the whole units dealt to each CTA, in halves
   unsigned long long shared;      // keys that several query tiles read
+  int most;                       // tiles of the longest unit dealt (one round)
   int rounds;                     // rounds of whole units
+  int at_b, at_h, at_j, at_off;   // where this CTA's run begins
 };
 
 // The last sequence whose entry of a running sum is not above x.
@@ -138,8 +139,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 struct Seg {
   int b, h, j, t0, t1, tiles, keys;
   int have;  // keys of the sequence; `keys` are those that the unit sees
-  int tok0, ntok, n, ctx;
-  long long u0;  // the unit's first tile in the order of all
+  int tok0, ntok, ctx;
 };
 
 __device__ __forceinline__ int unit_cost(const Params& P, const Batch& S, int b, int j) {
@@ -160,66 +160,45 @@ __device__ __forceinline__ int dealt_unit(int round, int c, int n) {
 
 // A CTA's segments: the whole units dealt to it, then its run of tiles.
 struct Walk {
-  long long pos, end;
-  int b, h, j, off, round, c, n;
+  long long left;  // tiles of the run to come
+  int b, h, j, off, round;
 
-  __device__ __forceinline__ void init(const Batch& S, int cta, int ctas) {
-    c = cta;
-    n = ctas;
+  __device__ __forceinline__ void init(const Batch& S) {
     round = 0;
-    pos = S.start[c];
-    end = S.start[c + 1];
-    off = -1;  // its place is looked up when the run begins
+    left = S.start[blockIdx.x + 1] - S.start[blockIdx.x];
+    b = S.at_b;
+    h = S.at_h;
+    j = S.at_j;
+    off = S.at_off;
   }
 
-  __device__ __forceinline__ void locate(const Params& P, const Batch& S) {
-    b = seq_of(S.pref, P.g.B, pos);
-    long long rem = pos - S.pref[b];
-    const long long per_head = div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
-    h = (int)div_ll(rem, per_head);
-    rem -= h * per_head;
-    for (j = 0;; ++j) {
-      const int cost = unit_cost(P, S, b, j);
-      if (rem < cost) break;
-      rem -= cost;
-    }
-    off = (int)rem;
-  }
-
-  __device__ __forceinline__ bool next(const Params& P, const Batch& S, Seg& s) {
+  __device__ __forceinline__ bool next(const Params& P, const Batch& S, int ctas, Seg& s) {
     const bool whole = round < S.rounds;
     if (whole) {
-      unit_at(P, S, dealt_unit(round, c, n), s.b, s.h, s.j);
+      unit_at(P, S, dealt_unit(round, blockIdx.x, ctas), s.b, s.h, s.j);
       ++round;
     } else {
-      if (pos >= end) return false;
-      if (off < 0) locate(P, S);
+      if (left <= 0) return false;
       s.b = b;
       s.h = h;
       s.j = j;
     }
-    s.n = S.n[s.b];
-    s.ctx = S.len[s.b] - s.n;
-    s.keys = unit_keys(P, s.n, S.len[s.b], s.j);
-    s.have = max(min(S.len[s.b], P.key_cap), 0);
+    const int n = S.n[s.b], len = S.len[s.b];
+    s.ctx = len - n;
+    s.keys = unit_keys(P, n, len, s.j);
+    s.have = max(min(len, P.key_cap), 0);
     s.tiles = tiles_of(s.keys);
     s.tok0 = S.first[s.b] + s.j * P.TT;
-    s.ntok = min(P.TT, s.n - s.j * P.TT);
+    s.ntok = min(P.TT, n - s.j * P.TT);
     const int cost = max(s.tiles, 1);
-    if (whole) {
-      s.t0 = 0;
-      s.t1 = cost;
-      s.u0 = 0;  // of cut units only
-    } else {
-      s.u0 = pos - off;
-      const long long left = end - pos;
+    s.t0 = 0;
+    s.t1 = cost;
+    if (!whole) {
       s.t0 = off;
-      s.t1 = (long long)(cost - off) <= left ? cost : off + (int)left;
-      pos += s.t1 - s.t0;
+      if (cost - off > left) s.t1 = off + (int)left;
+      left -= s.t1 - s.t0;
       off = 0;
-      if ((j + 1) * P.TT < s.n) {
-        ++j;
-      } else {
+      if (++j * P.TT >= n) {
         j = 0;
         if (++h == P.g.H_kv) {
           h = 0;
@@ -241,23 +220,67 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
   return __funnelshift_r(lo, hi, o & 31);
 }
 
+// Tiles of the query tiles before the first `count` of a sequence, for one KV head (the
+// whole warp calls this).
+__device__ __forceinline__ long long tiles_before(const Params& P, const Batch& S, int b,
+                                                  int count) {
+  long long t = 0;
+  for (int x = threadIdx.x & 31; x < count; x += 32) t += unit_cost(P, S, b, x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+// Where the run that begins at tile `pos` does (one warp).
+__device__ __forceinline__ void locate(const Params& P, Batch& S, long long pos) {
+  const int lane = threadIdx.x & 31;
+  const int b = seq_of(S.pref, P.g.B, pos);
+  long long rem = pos - S.pref[b];
+  const long long per_head = div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
+  const int h = (int)div_ll(rem, per_head), tiles = div_ll(S.units[b + 1] - S.units[b], P.g.H_kv);
+  rem -= h * per_head;
+  for (int j0 = 0; j0 < tiles; j0 += 32) {
+    const int cost = j0 + lane < tiles ? unit_cost(P, S, b, j0 + lane) : 0;
+    int incl = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, rem < incl);
+    if (past) {
+      if (lane == __ffs(past) - 1) {
+        S.at_b = b;
+        S.at_h = h;
+        S.at_j = j0 + lane;
+        S.at_off = (int)rem - (incl - cost);
+      }
+      return;
+    }
+    rem -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
 // Deals `rounds` rounds of whole units to n CTAs, and gives the units left to their runs:
 // each gets what its dealt units leave of an even total (one tile at least).  False if
 // the dealt units are too uneven for that (one round only).  Every CTA works the same
-// plan out; the whole block calls this.
+// plan out; the whole block calls this.  A CTA's rounds are summed by two threads (sums
+// in shared memory by 64-bit atomics, and runs in doubles, took 10 us of 64 x 128 tokens).
 __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int rounds) {
+  static_assert(kThreads >= 2 * kMaxCtas, "two threads to a CTA");
   const int tid = threadIdx.x;
   const long long W = S.pref[P.g.B], units = S.units[P.g.B];
-  for (int c = tid; c < n; c += kThreads) S.dealt[c] = 0;
-  if (tid == 0) S.most = 0;
-  __syncthreads();
-  for (int u = tid; u < rounds * n; u += kThreads) {
-    int b, h, j;
-    unit_at(P, S, u, b, h, j);
-    const int round = u / n, x = u - round * n;
-    const unsigned long long cost = (unsigned long long)unit_cost(P, S, b, j);
-    atomicAdd(&S.dealt[(round & 1) ? n - 1 - x : x], cost);
-    if (rounds == 1) atomicMax(&S.most, cost);
+  if (tid < 2 * n) {
+    const int part = tid >= n, c = tid - part * n;
+    long long sum = 0;
+    for (int r = part; r < rounds; r += 2) {
+      int b, h, j;
+      unit_at(P, S, dealt_unit(r, c, n), b, h, j);
+      const int cost = unit_cost(P, S, b, j);
+      if (rounds == 1) atomicMax(&S.most, cost);
+      sum += cost;
+    }
+    S.dealt[part][c] = sum;
   }
   __syncthreads();
   const long long even = div_ll(W, n);
@@ -266,8 +289,8 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
   if (!none_left) {
     int b, h, j;
     unit_at(P, S, rounds * n, b, h, j);
-    first = S.pref[b] + div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv) * h;
-    for (int x = 0; x < j; ++x) first += unit_cost(P, S, b, x);
+    first = S.pref[b] + div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv) * h +
+            tiles_before(P, S, b, j);
   }
   const long long left = W - first;
   if (rounds == 1) {
@@ -289,7 +312,7 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
       const int c = tid * kPer + i;
       // (One over the quotient, less the one that every run has: where the quotient has
       // lost a fraction, all of them stay in proportion.)
-      need[i] = c < n ? max(even - (long long)S.dealt[c], 0ll) : 0;
+      need[i] = c < n ? max(even - (S.dealt[0][c] + S.dealt[1][c]), 0ll) : 0;
       sum += need[i];
     }
     long long incl = sum;
@@ -300,12 +323,13 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
     }
     const long long all = __shfl_sync(0xffffffffu, incl, 31);
     long long before = incl - sum;
+    // In floats: the shares need not be exact, only in order (and each step here keeps it).
+    const float spare = (float)(left - n), scale = all > 0 ? 1.f / (float)all : 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int c = tid * kPer + i;
       if (c < n)
-        S.start[c] = first + c +
-                     (all > 0 ? (long long)((double)before / (double)all * (double)(left - n)) : 0);
+        S.start[c] = first + c + min((long long)((float)before * scale * spare), left - n);
       before += need[i];
     }
     if (tid == 0) S.start[n] = W;
@@ -342,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpK) tma_prefetch_desc(&tmQ);
   }
   if (tid == 0) {
-    S.shared = 0;
+    S.most = 0;
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar_q_full[x], 1);
-      mbar_init(&bar_q_empty[x], 1);
+      mbar_init(&bar_q_empty[x], 1 + kSoftmaxWarps);
       mbar_init(&bar_o_done[x], 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -368,32 +392,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  // The batch: rows and lengths, each sequence's tiles (a warp each), their sums.
+  // The batch: rows and lengths, each sequence's tiles (by a warp where it has more than a
+  // few query tiles), their sums.
+  int many = 0;
   for (int b = tid; b < B; b += kThreads) {
     const int lo = max(0, min(__ldg(P.g.cu_q + b), P.N));
     const int hi = max(lo, min(__ldg(P.g.cu_q + b + 1), P.N));
+    const int n = hi - lo, len = __ldg(P.g.seq_lens + b), tiles = (n + P.TT - 1) / P.TT;
     S.first[b] = lo;
-    S.n[b] = hi - lo;
-    S.len[b] = __ldg(P.g.seq_lens + b);
-    if (hi > lo && S.len[b] > P.key_cap) record_error(STT_DEVERR_PAGE);
-  }
-  __syncthreads();
-  for (int b = warp; b < B; b += kThreads / 32) {
-    const int n = S.n[b], len = S.len[b];
-    long long t = 0;
-    for (long long j = lane; j * P.TT < n; j += 32)
-      t += max(tiles_of(unit_keys(P, n, len, (int)j)), 1);
-    if (lane == 0) {
-      S.units[b + 1] = (n + P.TT - 1) / P.TT * P.g.H_kv;
-      if (n > 3 * P.TT && len > 0) atomicAdd(&S.shared, (unsigned long long)len);
+    S.n[b] = n;
+    S.len[b] = len;
+    if (n > 0 && len > P.key_cap) record_error(STT_DEVERR_PAGE);
+    long long t = -1;
+    if (tiles <= 4) {
+      t = 0;
+      for (int j = 0; j < tiles; ++j) t += max(tiles_of(unit_keys(P, n, len, j)), 1);
+    } else {
+      many = 1;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
+    S.units[b + 1] = tiles * P.g.H_kv;
+    S.pref[b + 1] = t * P.g.H_kv;
   }
-  __syncthreads();
+  if (__syncthreads_or(many)) {
+    for (int b = warp; b < B; b += kThreads / 32)
+      if (S.pref[b + 1] < 0) {
+        const long long t = tiles_before(P, S, b, (S.n[b] + P.TT - 1) / P.TT);
+        __syncwarp();
+        if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
+      }
+    __syncthreads();
+  }
   if (warp == 1) {
     long long carry = 0;
+    unsigned long long shared = 0;
     int carry_u = 0;
     if (lane == 0) {
       S.pref[0] = 0;
@@ -402,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b0 = 0; b0 < B; b0 += 32) {
       long long v = b0 + lane < B ? S.pref[b0 + lane + 1] : 0;
       int u = b0 + lane < B ? S.units[b0 + lane + 1] : 0;
+      if (b0 + lane < B && S.n[b0 + lane] > 3 * P.TT) shared += max(S.len[b0 + lane], 0);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long v1 = __shfl_up_sync(0xffffffffu, v, o);
@@ -420,6 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       carry = __shfl_sync(0xffffffffu, v, 31);
       carry_u = __shfl_sync(0xffffffffu, u, 31);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) shared += __shfl_xor_sync(0xffffffffu, shared, o);
+    if (lane == 0) S.shared = shared;
   }
   tc_fence_before();
   __syncthreads();
@@ -439,15 +474,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (plan_rounds(P, S, n, rounds)) ctas = n;
     else rounds = 0;
   }
+  const auto border = [&](int c) { return div_ll(W * c, max(ctas, 1)); };
   if (rounds == 0)
-    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = div_ll(W * c, max(ctas, 1));
-  if (tid == 0) S.rounds = rounds;
+    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = border(c);
+  if (warp == 0) {  // (the borders were written by this warp if there are rounds)
+    __syncwarp();
+    if (lane == 0) S.rounds = rounds;
+    const long long pos =
+        (int)blockIdx.x >= ctas ? W : (rounds == 0 ? border(blockIdx.x) : S.start[blockIdx.x]);
+    if (pos < W) locate(P, S, pos);
+  }
   __syncthreads();
   Walk walk;
-  walk.pos = walk.end = 0;
+  walk.left = 0;
   walk.round = rounds;
-  if ((int)blockIdx.x < ctas) walk.init(S, blockIdx.x, ctas);
-  Seg s;
+  if ((int)blockIdx.x < ctas) walk.init(S);
+  Seg s, nx;
 
   if (warp == kWarpK || warp == kWarpV) {
     // --------------------------------------------------- page producers ----
@@ -461,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int copies = kTile / box;        // copies a tile takes, one lane each
     uint32_t g = 0, i = 0, q_issued = 0;
     bool ok = true;
-    while (ok && walk.next(P, S, s)) {
+    while (ok && walk.next(P, S, ctas, s)) {
       if (s.tiles == 0) continue;
       if (is_k) {
         const int qs = i & 1;
@@ -524,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dV0 = sdesc_sw128(smem_u32(smem + L::v0), kTile * 128, 1024);
       uint32_t g = 0, i = 0;
       bool ok = true;
-      while (ok && walk.next(P, S, s)) {
+      while (ok && walk.next(P, S, ctas, s)) {
         if (s.tiles == 0) continue;
         if (warp == kWarpMma) {
           ok = mbar_wait(&bar_q_full[i & 1], (i >> 1) & 1u, kSite);
@@ -580,16 +622,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = P.scale_log2;
     const int t_row = r / P.G, g_row = r - t_row * P.G;
     uint32_t quad_uses = 0, g = 0, n_final = 0;
+    const int row_off = t_row * P.H + g_row;  // in rows of `out`
+    // Where this warp turns rows held by lanes into rows held by chunks: its eighth of
+    // the unit's query buffer, which its last S has read.
+    constexpr int kChunks = DH / 8, kRowsAt = 32 / kChunks;  // 16-byte chunks, rows a pass
+    const int put_x = D == 128 ? lane & 7 : (lane >> 1) & 3;
+    const int get_r = lane / kChunks, get_c = lane % kChunks;
     bool ok = true, joined = false;
-    for (uint32_t i = 0; ok && walk.next(P, S, s);) {
+    s = Seg{};
+    s.b = -1;  // none yet
+    for (uint32_t i = 0;;) {
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       // A share's first segment that begins inside its unit leaves what the join
       // needs to know.
       if (!whole && s.t0 > 0 && tid == 0) {
         joined = true;
-        const long long last = s.u0 + s.tiles - 1;
+        const long long first = S.start[blockIdx.x] - s.t0, last = first + s.tiles - 1;
         JoinDesc d;
-        d.c0 = seq_of(S.start, ctas, s.u0);
+        d.c0 = seq_of(S.start, ctas, first);
         d.c1 = seq_of(S.start, ctas, last);
         d.tok0 = s.tok0;
         d.ntok = s.ntok;
@@ -731,15 +781,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&bar_p_full[sb]);
       }
       if (!ok) break;
+      const bool more = walk.next(P, S, ctas, nx);  // while the last product runs
+      if (s.b < 0) {
+        if (!more) break;
+        s = nx;
+        continue;
+      }
 
       // ------------------------------------------------------- results ----
+      // In a unit without keys there is no query buffer, nor a part to leave.
       float o[DH];
-      if (s.tiles > 0) {
+      unsigned char* const turn = smem + L::q + (int)(i & 1) * L::kQ + warp * (L::kQ / kSoftmaxWarps);
+      uint64_t* const q_empty = &bar_q_empty[i & 1];
+      if (s.tiles == 0) {
+#pragma unroll
+        for (int x = 0; x < DH; ++x) o[x] = 0.f;
+      } else {
         ok = warp_wait(&bar_o_final, n_final & 1u, kSite);
         ++n_final;
         ++i;
         if (!ok) break;
-        if (dead) continue;
+        if (dead) {
+          warp_arrive(q_empty);
+          if (!more) break;
+          s = nx;
+          continue;
+        }
         tc_fence_after();
         const uint32_t ocol = tmem + lane_off + kColO + part * DH;
 #pragma unroll
@@ -754,35 +821,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = group_sync(&bar_quad[quarter], quad_uses, kSite);
         if (!ok) break;
         l_run += s_sum[i & 1][part ^ 1][r];
-      } else {
-        if (dead) continue;
-#pragma unroll
-        for (int x = 0; x < DH; ++x) o[x] = 0.f;
       }
-      if (row_live) {
-        // A row that saw nothing has l = 0 and O = 0.
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
-        if (whole) {
-          const int64_t at = (int64_t)(s.tok0 + t_row) * P.H + s.h * P.G + g_row;
-          uint4* dst = reinterpret_cast<uint4*>(P.out + at * D + part * DH);
+      // A row that saw nothing has l = 0 and O = 0.
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
+      // Rows go out through shared memory: stored by the lanes that hold them, each
+      // store would touch 32 rows, and the eight warps' took 2.9 thousand cycles a unit,
+      // 1.9 now.  Chunks are placed by an exclusive or, so that neither side meets a bank
+      // twice.
+      auto put = [&](int c, const uint4& v) {
+        *reinterpret_cast<uint4*>(turn + (lane * kChunks + (c ^ put_x)) * 16) = v;
+      };
+      auto get = [&](int row) {
+        const int x = D == 128 ? row & 7 : (row >> 1) & 3;
+        return *reinterpret_cast<const uint4*>(turn + (row * kChunks + (get_c ^ x)) * 16);
+      };
+      const int64_t first = (int64_t)s.tok0 * P.H + s.h * P.G;
+      if (s.tiles == 0) {
+        if (row_live) {
+          uint4* dst = reinterpret_cast<uint4*>(P.out + (first + row_off) * D + part * DH);
 #pragma unroll
-          for (int c = 0; c < DH / 8; ++c)
-            dst[c] = make_uint4(pack_bf16(o[c * 8 + 0] * inv, o[c * 8 + 1] * inv),
-                                pack_bf16(o[c * 8 + 2] * inv, o[c * 8 + 3] * inv),
-                                pack_bf16(o[c * 8 + 4] * inv, o[c * 8 + 5] * inv),
-                                pack_bf16(o[c * 8 + 6] * inv, o[c * 8 + 7] * inv));
-          if (part == 0 && P.lse) P.lse[at] = lse2 * kLn2;
-        } else {
-          float* slot = P.part + (int64_t)(2 * blockIdx.x + (s.t0 > 0 ? 0 : 1)) * P.slot;
-          float4* dst = reinterpret_cast<float4*>(slot + (int64_t)r * D + part * DH);
-#pragma unroll
-          for (int c = 0; c < DH / 4; ++c)
-            dst[c] = make_float4(o[c * 4] * inv, o[c * 4 + 1] * inv, o[c * 4 + 2] * inv,
-                                 o[c * 4 + 3] * inv);
-          if (part == 0) slot[(int64_t)P.slot_rows * D + r] = lse2;
+          for (int c = 0; c < kChunks; ++c) dst[c] = make_uint4(0, 0, 0, 0);
         }
+      } else if (whole) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          put(c, make_uint4(pack_bf16(o[c * 8 + 0] * inv, o[c * 8 + 1] * inv),
+                            pack_bf16(o[c * 8 + 2] * inv, o[c * 8 + 3] * inv),
+                            pack_bf16(o[c * 8 + 4] * inv, o[c * 8 + 5] * inv),
+                            pack_bf16(o[c * 8 + 6] * inv, o[c * 8 + 7] * inv)));
+        __syncwarp();
+        uint4 v[kChunks];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) v[k] = get(k * kRowsAt + get_r);
+        fence_proxy_async_smem();  // the next queries come here by TMA
+        warp_arrive(q_empty);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const int row = k * kRowsAt + get_r;
+          const int off = __shfl_sync(0xffffffffu, row_off, row);
+          if (quarter * 32 + row < live)
+            *reinterpret_cast<uint4*>(P.out + (first + off) * D + part * DH + get_c * 8) = v[k];
+        }
+      } else {
+        float* slot = P.part + (int64_t)(2 * blockIdx.x + (s.t0 > 0 ? 0 : 1)) * P.slot;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          constexpr int kHalf = DH / 2;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const float* v = o + half * kHalf + c * 4;
+            put(c, make_uint4(__float_as_uint(v[0] * inv), __float_as_uint(v[1] * inv),
+                              __float_as_uint(v[2] * inv), __float_as_uint(v[3] * inv)));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            const int row = k * kRowsAt + get_r;
+            if (quarter * 32 + row < live)
+              *reinterpret_cast<uint4*>(slot + (int64_t)(quarter * 32 + row) * D + part * DH +
+                                        half * kHalf + get_c * 4) = get(row);
+          }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(q_empty);
+        if (row_live && part == 0) slot[(int64_t)P.slot_rows * D + r] = lse2;
       }
+      if ((whole || s.tiles == 0) && row_live && part == 0 && P.lse)
+        P.lse[first + row_off] = lse2 * kLn2;
+      if (!more) break;
+      s = nx;
     }
     if (tid == 0 && !joined) P.join[blockIdx.x].c0 = -1;
   }
