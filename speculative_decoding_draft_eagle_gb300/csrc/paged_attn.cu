@@ -99,7 +99,7 @@ struct Smem {
 // The batch in shared memory.
 struct Batch {
   long long pref[kMaxBatch + 1];  // tiles before each sequence
-  int units[kMaxBatch + 1];       // units before each sequence
+  int qt[kMaxBatch + 1];          // query tiles before each sequence (a unit: one per KV head)
   int first[kMaxBatch], n[kMaxBatch], len[kMaxBatch];
   long long start[kMaxCtas + 1];  // the CTAs' runs of tiles
   long long dealt[2][kMaxCtas];   // tiles of the whole units dealt to each CTA, in halves
@@ -148,10 +148,20 @@ __device__ __forceinline__ int unit_cost(const Params& P, const Batch& S, int b,
 // Unit u in the order of all: its sequence, head and query tile.
 __device__ __forceinline__ void unit_at(const Params& P, const Batch& S, int u, int& b, int& h,
                                         int& j) {
-  b = seq_of(S.units, P.g.B, u);
-  const int tiles = (S.n[b] + P.TT - 1) / P.TT, r = u - S.units[b];
-  h = r / tiles;
+  b = 0;
+  for (int step = kMaxBatch / 2; step > 0; step >>= 1)
+    if (b + step < P.g.B && (long long)S.qt[b + step] * P.g.H_kv <= u) b += step;
+  const int tiles = S.qt[b + 1] - S.qt[b], r = u - S.qt[b] * P.g.H_kv;
+  // r / tiles is a head: few enough for a quotient of floats to be off by one at most.
+  h = (int)__fdividef((float)r, (float)tiles);
   j = r - h * tiles;
+  if (j < 0) {
+    --h;
+    j += tiles;
+  } else if (j >= tiles) {
+    ++h;
+    j -= tiles;
+  }
 }
 // Unit that CTA c of n takes in a round (snake order).
 __device__ __forceinline__ int dealt_unit(int round, int c, int n) {
@@ -236,9 +246,21 @@ __device__ __forceinline__ void locate(const Params& P, Batch& S, long long pos)
   const int lane = threadIdx.x & 31;
   const int b = seq_of(S.pref, P.g.B, pos);
   long long rem = pos - S.pref[b];
-  const long long per_head = div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
-  const int h = (int)div_ll(rem, per_head), tiles = div_ll(S.units[b + 1] - S.units[b], P.g.H_kv);
+  const int tiles = S.qt[b + 1] - S.qt[b];
+  const bool one = tiles == 1;  // as for single tokens: half of the time
+  const long long per_head = one ? (long long)unit_cost(P, S, b, 0)
+                                 : div_ll(S.pref[b + 1] - S.pref[b], P.g.H_kv);
+  const int h = (int)div_ll(rem, per_head);
   rem -= h * per_head;
+  if (one) {
+    if (lane == 0) {
+      S.at_b = b;
+      S.at_h = h;
+      S.at_j = 0;
+      S.at_off = (int)rem;
+    }
+    return;
+  }
   for (int j0 = 0; j0 < tiles; j0 += 32) {
     const int cost = j0 + lane < tiles ? unit_cost(P, S, b, j0 + lane) : 0;
     int incl = cost;
@@ -269,10 +291,11 @@ __device__ __forceinline__ void locate(const Params& P, Batch& S, long long pos)
 __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int rounds) {
   static_assert(kThreads >= 2 * kMaxCtas, "two threads to a CTA");
   const int tid = threadIdx.x;
-  const long long W = S.pref[P.g.B], units = S.units[P.g.B];
+  const long long W = S.pref[P.g.B], units = (long long)S.qt[P.g.B] * P.g.H_kv;
   if (tid < 2 * n) {
     const int part = tid >= n, c = tid - part * n;
     long long sum = 0;
+#pragma unroll 1
     for (int r = part; r < rounds; r += 2) {
       int b, h, j;
       unit_at(P, S, dealt_unit(r, c, n), b, h, j);
@@ -306,25 +329,27 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
   }
   if (tid < 32) {
     constexpr int kPer = (kMaxCtas + 31) / 32;
-    long long need[kPer], sum = 0;
+    const int shift = max(0, 34 - __clzll(W));  // sums below 2^30
+    int need[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int c = tid * kPer + i;
       // (One over the quotient, less the one that every run has: where the quotient has
       // lost a fraction, all of them stay in proportion.)
-      need[i] = c < n ? max(even - (S.dealt[0][c] + S.dealt[1][c]), 0ll) : 0;
+      need[i] =
+          c < n ? (int)(max(even - (S.dealt[0][c] + S.dealt[1][c]), 0ll) >> shift) : 0;
       sum += need[i];
     }
-    long long incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (tid >= o) incl += v;
     }
-    const long long all = __shfl_sync(0xffffffffu, incl, 31);
-    long long before = incl - sum;
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    int before = incl - sum;
     // In floats: the shares need not be exact, only in order (and each step here keeps it).
-    const float spare = (float)(left - n), scale = all > 0 ? 1.f / (float)all : 0.f;
+    const float spare = (float)(left - n), scale = all > 0 ? __fdividef(1.f, (float)all) : 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int c = tid * kPer + i;
@@ -410,13 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       many = 1;
     }
-    S.units[b + 1] = tiles * P.g.H_kv;
+    S.qt[b + 1] = tiles;
     S.pref[b + 1] = t * P.g.H_kv;
   }
-  if (__syncthreads_or(many)) {
+  many = __syncthreads_or(many);
+  if (many) {
     for (int b = warp; b < B; b += kThreads / 32)
       if (S.pref[b + 1] < 0) {
-        const long long t = tiles_before(P, S, b, (S.n[b] + P.TT - 1) / P.TT);
+        const long long t = tiles_before(P, S, b, S.qt[b + 1]);
         __syncwarp();
         if (lane == 0) S.pref[b + 1] = t * P.g.H_kv;
       }
@@ -428,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int carry_u = 0;
     if (lane == 0) {
       S.pref[0] = 0;
-      S.units[0] = 0;
+      S.qt[0] = 0;
     }
     for (int b0 = 0; b0 < B; b0 += 32) {
       long long v = b0 + lane < B ? S.pref[b0 + lane + 1] : 0;
-      int u = b0 + lane < B ? S.units[b0 + lane + 1] : 0;
-      if (b0 + lane < B && S.n[b0 + lane] > 3 * P.TT) shared += max(S.len[b0 + lane], 0);
+      int u = b0 + lane < B ? S.qt[b0 + lane + 1] : 0;
+      if (many && b0 + lane < B && S.n[b0 + lane] > 4 * P.TT) shared += max(S.len[b0 + lane], 0);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long v1 = __shfl_up_sync(0xffffffffu, v, o);
@@ -447,13 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       u += carry_u;
       if (b0 + lane < B) {
         S.pref[b0 + lane + 1] = v;
-        S.units[b0 + lane + 1] = u;
+        S.qt[b0 + lane + 1] = u;
       }
       carry = __shfl_sync(0xffffffffu, v, 31);
       carry_u = __shfl_sync(0xffffffffu, u, 31);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) shared += __shfl_xor_sync(0xffffffffu, shared, o);
+    for (int o = many ? 16 : 0; o > 0; o >>= 1) shared += __shfl_xor_sync(0xffffffffu, shared, o);
     if (lane == 0) S.shared = shared;
   }
   tc_fence_before();
@@ -461,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const long long W = S.pref[B];
-  const int grid = (int)gridDim.x, units = S.units[B];
+  const int grid = (int)gridDim.x, units = S.qt[B] * P.g.H_kv;
   int ctas = (int)(W < (long long)grid ? W : (long long)grid), rounds = 0;
   if (units >= 2 * grid) {
     rounds = units / grid - 1;
@@ -475,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     else rounds = 0;
   }
   const auto border = [&](int c) { return div_ll(W * c, max(ctas, 1)); };
-  if (rounds == 0)
-    for (int c = tid; c <= ctas; c += kThreads) S.start[c] = border(c);
+  if (rounds == 0 && warp > 0)
+    for (int c = tid - 32; c <= ctas; c += kThreads - 32) S.start[c] = border(c);
   if (warp == 0) {  // (the borders were written by this warp if there are rounds)
     __syncwarp();
     if (lane == 0) S.rounds = rounds;
