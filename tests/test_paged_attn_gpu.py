@@ -132,6 +132,13 @@ def test_trees_with_whole_units_dealt():
     _run(bt, 16 * 8, rng.random((bt.N, n)) < 0.5)
 
 
+@pytest.mark.parametrize("G,D", [(4, 128), (4, 64), (3, 128)])
+def test_many_short_units(G, D):
+    """Rounds of whole units of a tile or two, some without a key, and runs after them."""
+    bt = Batch([128, 1, 0, 33, 70, 7] * 12, [128, 3, 0, 20, 300, 0] * 12, 16, 8, D, 6)
+    _run(bt, 8 * G)
+
+
 def test_a_batch_without_new_tokens():
     bt = Batch([0, 0], [5, 0], 16, 1, 64, 3, pad=4)
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)
