@@ -11,12 +11,11 @@
 // e^(y - m); the pairs of all rows are exchanged with the other CTAs at once; and a
 // second pass turns the output into e^(y - M) / L in place, out of L2, which a CTA's
 // rows do not leave in between: HBM sees 2 or 4 bytes read and 4 written per logit.
-// 320 bf16 rows of 151936 with histories, bias and mask take 130 us, 80 without
+// 320 bf16 rows of 151936 with histories, bias and mask take 124 us, 66 without
 // those, against 44 at HBM's rate: the CTAs of a row wait for one another between the
 // passes, with 32 warps an SM to cover it (the same with twice the loads in flight;
-// five rows together, 142; C half as large, 145).  Processing the logits again in the
-// second pass took 141 us; keeping a row in registers between the passes left fewer
-// warps, 136 to 205 us.
+// five rows together 137; C half as large, 145).  Keeping a row in registers between
+// the passes left fewer warps, 136 to 205 us.
 //
 // The tokens that occur in the history are few against the vocabulary.  A bit map
 // holds the ones seen; a seen token's rank in it, from the running sum of its words'
@@ -185,6 +184,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
     fence_mbar_init();
     if (P.C > 1) mbar_arrive_expect_tx(&bar_pair, (uint32_t)(P.C * n_rows * 16));
   }
+  // The first row's logits into L2 while the history is counted (129 -> 124 us).
+  if (FILTER && VEC && tid < n_blocks) {
+    const int first = block_at(tid), n = min(kBlock, A.V - first) * (int)sizeof(T) & ~15;
+    const T* const at = static_cast<const T*>(A.z) + r0 * A.V + first;
+    if (n > 0 && (reinterpret_cast<uintptr_t>(at) & 15u) == 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(n) : "memory");
+  }
   const int32_t* const draft = A.draft ? A.draft + (int64_t)b * A.draft_ld : nullptr;
   if (hist)
     for (int w = tid; w < P.words; w += kThreads) seen_bits[w] = 0;
@@ -322,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
         }
       };
       auto work = [&](const Pair& p, int k, auto tail) {
-        const int v = block_at(k) + tid * kChunk, at = k * kBlock + tid * kChunk;
+        const int v = block_at(k) + tid * kChunk;
+        [[maybe_unused]] const int at = k * kBlock + tid * kChunk;  // its place
         if (decltype(tail)::value && v >= A.V) return;
         const bool second = !decltype(tail)::value || v + kApart < A.V;
         float x[2 * kChunk];
@@ -415,6 +422,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
   const bool greedy = temp == 0.f && !A.raw;
   const float c = temp > 0.f ? __fdiv_rn(kLog2E, temp) : 1.f, t_raw = temp > 0.f ? temp : 1.f;
   const Stat none = {-INFINITY, greedy ? __int_as_float(0x7fffffff) : 0.f};
+  // Without mask and history the second pass takes the logits again, which are in L2 as
+  // well: nothing is written twice (320 bf16 rows of 151936: 80 -> 66 us, with a bias 91 ->
+  // 83, fp32 97 -> 80).  With them, applying them twice costs more than the writes (130 ->
+  // 149 us).
+  constexpr bool again = !FILTER;
   auto first_pass = [&](auto mode) {
     constexpr int M = decltype(mode)::value;  // 0: softmax, 1: greedy, 2: raw
     for (int q = 0; q < n_rows; ++q) {
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
         } else {
           add_values<M == 1>(st, x, c, [&](int e) { return index(v, e); });
         }
-        store(out + v, x, seen, second);
+        if constexpr (M == 2 || !again) store(out + v, x, seen, second);
       });
       if (over && n_seen > 0) {
         __syncthreads();
@@ -477,7 +489,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
     const int best = s.m == -INFINITY ? -1 : __float_as_int(s.l);
     const float top = s.m == -INFINITY ? 0.f : s.m, inv = s.l == 0.f ? 0.f : 1.f / s.l;
     float* const out = out0 + (uint32_t)q * V;
-    if constexpr (VEC) {
+    if constexpr (again) {
+      sweep(q, [&](auto& x, uint32_t seen, int v, bool second) {
+#pragma unroll
+        for (int e = 0; e < (int)(sizeof(x) / sizeof(float)); ++e)
+          x[e] = greedy ? (index(v, e) == best ? 1.f : 0.f) : ex2((x[e] - top) * c) * inv;
+        store(out + v, x, seen, second);
+      });
+    } else if constexpr (VEC) {
       auto result = [&](float4 y, int v) {
         if (greedy)
           return make_float4(v == best ? 1.f : 0.f, v + 1 == best ? 1.f : 0.f,
@@ -540,7 +559,8 @@ cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s) {
   P.C = C;
   while ((1 << P.log_c) < C) ++P.log_c;
   // Rows of a sequence that share its counts: up to eight, fewer while that makes less
-  // than kFill CTAs an SM (five rows together 142 us, one at a time 130, where B is 64).
+  // than kFill CTAs an SM (64 sequences of five rows: one at a time or two together 129 us,
+  // three 137).
   const int64_t B = a.N / a.rows;
   int most = std::min(kMaxRows, a.rows);
   while (most > 1 && B * ((a.rows + most - 1) / most) * C < kFill * sm_count()) --most;

@@ -122,6 +122,17 @@ def test_in_place():
         _case(900, 5, 72, hist=30, draft=True, inplace=True, raw=raw)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("greedy", [False, True])
+@pytest.mark.parametrize("V", [5001, 50000, 151936])
+def test_without_mask_and_history(V, greedy, bf16):
+    """The logits are read twice and written once; in place too."""
+    _case(3, 2, V, bf16=bf16, greedy=greedy, bias=1)
+    _case(2, 3, V, bf16=bf16, greedy=greedy)
+    if not bf16:
+        _case(2, 3, V, greedy=greedy, bias=2, inplace=True)
+
+
 def test_plain_softmax_without_arguments():
     z = torch.randn(5, 777, generator=gen(1))
     got = ops.stt_logits_process(z.to(DEV))
