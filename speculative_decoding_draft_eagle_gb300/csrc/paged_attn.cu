@@ -18,7 +18,7 @@
 // way).  The units left, between one and two to a CTA, go in runs that make the CTAs'
 // totals even.  With 0.8 to 2 units to a CTA one round is dealt if the keys that several
 // query tiles read are more than L2 keeps and the units are about as long as one
-// another (500 tokens on 120 thousand keys: 888 TFLOP/s in runs, 1157 dealt).  A unit
+// another (500 tokens on 120 thousand keys: 888 TFLOP/s in runs, 1232 dealt).  A unit
 // cut by a share's border leaves partial results
 // (normalised rows and their logarithms of the sum) in the workspace, at most two
 // per CTA, and a second small kernel, launched as a programmatic dependent, joins
@@ -28,10 +28,13 @@
 // What bounds it: HBM for few new tokens (six tokens on each of four contexts of 90 to
 // 131 thousand keys, 32 query and 8 KV heads of 128: 260 us, 6.68 TB/s, 0.98 of the copy
 // rate), the tensor cores with the softmax between them for chunks (500 to 2048 tokens
-// on 4 to 16 thousand keys: 599 us, 1202 TFLOP/s, 0.63 of cuBLAS's burst).  With units of a few tiles, each one's end (the last product, the rows
-// out, at most three pipelines refilled) shows: trees of 16 tokens on 32 sequences of
-// 500 to 4000 keys take 65 us, 0.64 of the copy rate.  One token on 777 keys takes 14 us,
-// 10 of them this kernel's chain for a single tile and 4 the join's.  The same kernel
+// on 4 to 16 thousand keys: 562 us, 1282 TFLOP/s, 0.67 of cuBLAS's burst; 520 repeated
+// on one state).  With units of a few tiles the fixed parts show (4 us until the batch is
+// laid out, 3 to the first scores, 5 for the join; a unit's end of 2 us passes while the
+// next tiles load): trees of 16 tokens on 32 sequences of 500 to 4000 keys take 65 us, 0.64
+// of the copy rate, although the tiles themselves pass at all of it; 64 prompts of 128
+// tokens, units of one tile, 72 us.  One token on 777 keys takes 14 us, 10 of them this
+// kernel's chain for a single tile and 4 the join's.  The same kernel
 // with one warp per row and head took 130, 154, 6.7 and 0.4 ms on these.
 //
 // Warp roles (384 threads), as in the training forward (attn_fwd.cu):

@@ -6,7 +6,7 @@
 // heads), fills its table of cosines and sines, and streams the token's heads, 32 / (D
 // / 8) of them a step, four steps' loads in flight.  HBM bounds them where there are
 // many tokens: 8192 tokens of 32 + 16 heads of 128 take 37 us forward (5.5 TB/s, 0.81 of
-// the copy rate; 41 with norms), 2 x 4096 tokens of 64 + 16 heads 113 us backward with
+// the copy rate; 41 with norms), 2 x 4096 tokens of 64 + 16 heads 110 us backward with
 // norms and fp32 gradients (5.8 TB/s, 0.86).  What moved them there was fewer
 // instructions, not more bytes in flight: 185 a step became about 80 when both elements
 // of a pair came to one lane and arithmetic went in pairs of floats (166 to 113 us
