@@ -420,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  // What was launched before is complete from here on; all above ran beside its end.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // The batch: rows and lengths, each sequence's tiles (by a warp where it has more than a
   // few query tiles), their sums.
   int many = 0;
@@ -941,6 +943,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join(const __grid_con
   constexpr int E = D / 32, kW = kJoinThreads / 32, R = 4;
   __shared__ __align__(16) float s_o[kW][D];
   __shared__ float s_l[kW];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinDesc d = P.join[blockIdx.x];
   if (d.c0 < 0) return;
@@ -1122,18 +1125,22 @@ cudaError_t launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s) 
   }
   const unsigned grid = (unsigned)std::min(sm_count(), kMaxCtas);
   prof_before(s, STT_KERNEL_PAGED_ATTN);
-  paged_attn_kernel<D><<<grid, kThreads, Smem<D>::alloc, s>>>(P, tmQ, tmK, tmV);
-  e = cudaGetLastError();
+  // Both as programmatic dependents: this kernel's set-up overlaps the end of what came
+  // before, the join's launch this kernel.
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::alloc;
+  cfg.stream = s;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, P, tmQ, tmK, tmV);
   if (e == cudaSuccess) {
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    la[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = la;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, paged_attn_join<D>, P);
   }
   prof_after(s);

@@ -302,6 +302,57 @@ def test_graph_follows_the_batch_and_streams_do_not_share():
     assert all(torch.equal(o[:n], want[0][:n]) and torch.equal(l[:n], want[1][:n]) for o, l in got)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_what_came_before_is_seen(captured):
+    """Calls back to back, each after copies and kernels (one on a side stream) that write
+    what it reads and read what it wrote: the set-up that overlaps them touches none of it."""
+    sizes = [([4, 0, 9], [400, 9, 130]), ([1, 11, 1], [2000, 300, 77]), ([13, 0, 0], [40, 0, 0])]
+    bts = [Batch(n, ln, 16, 2, 128, 12, max_pages=130) for n, ln in sizes]
+    bt, H = bts[1], 8
+    kc, vc = (torch.zeros_like(x) for x in bt.caches())
+    cu, lens, table = (torch.zeros_like(x) for x in bt.lists())
+    q = torch.zeros(13, H, 128, dtype=torch.bfloat16, device=DEV)
+    qs = [randn(gen(s), 13, H, 128).to(DEV) for s in range(3)]
+    src = [(b.caches(), b.lists()) for b in bts]
+    want = [ops.stt_paged_attn(x, *c, *ls) for x, (c, ls) in zip(qs, src)]
+    side = torch.cuda.Stream()
+    out, lse = torch.zeros_like(q), torch.zeros(13, H, device=DEV)
+    got = [(torch.zeros_like(out), torch.zeros_like(lse)) for _ in range(9)]
+
+    def work():
+        main = torch.cuda.current_stream()
+        for i, (o, l) in enumerate(got):
+            (k1, v1), (c1, n1, t1) = src[i % 3]
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                kc[: k1.shape[0]].copy_(k1)
+                torch.add(qs[i % 3], 0, out=q)
+            vc[: v1.shape[0]].copy_(v1)
+            table.copy_(t1)
+            cu.copy_(c1)
+            main.wait_stream(side)
+            torch.add(n1, 0, out=lens)
+            ops.stt_paged_attn(q, kc, vc, cu, lens, table, out=out, lse=lse)
+            o.copy_(out)
+            l.copy_(lse)
+
+    work()
+    if captured:
+        torch.cuda.synchronize()
+        for o, l in got:
+            o.zero_()
+            l.zero_()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            work()
+        gr.replay()
+        gr.replay()
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        n = int(bts[i % 3].cu[-1])
+        assert torch.equal(o[:n], want[i % 3][0][:n]) and torch.equal(l[:n], want[i % 3][1][:n])
+
+
 def test_first_call_inside_a_capture():
     """In a fresh process, with nothing of the library loaded on the device before."""
     import subprocess
