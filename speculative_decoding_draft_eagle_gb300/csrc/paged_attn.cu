@@ -26,16 +26,18 @@
 // on what the host knows of the batch.
 //
 // What bounds it: HBM for few new tokens (six tokens on each of four contexts of 90 to
-// 131 thousand keys, 32 query and 8 KV heads of 128: 260 us, 6.68 TB/s, 0.98 of the copy
+// 131 thousand keys, 32 query and 8 KV heads of 128: 255 us, 6.79 TB/s, all of the copy
 // rate), the tensor cores with the softmax between them for chunks (500 to 2048 tokens
-// on 4 to 16 thousand keys: 562 us, 1282 TFLOP/s, 0.67 of cuBLAS's burst; 520 repeated
-// on one state).  With units of a few tiles the fixed parts show (4 us until the batch is
-// laid out, 3 to the first scores, 5 for the join; a unit's end of 2 us passes while the
-// next tiles load): trees of 16 tokens on 32 sequences of 500 to 4000 keys take 65 us, 0.64
-// of the copy rate, although the tiles themselves pass at all of it; 64 prompts of 128
-// tokens, units of one tile, 72 us.  One token on 777 keys takes 14 us, 10 of them this
-// kernel's chain for a single tile and 4 the join's.  The same kernel
-// with one warp per row and head took 130, 154, 6.7 and 0.4 ms on these.
+// on 4 to 16 thousand keys: 561 us, 1284 TFLOP/s, 0.67 of cuBLAS's burst; 520 repeated
+// on one state.  A row's two warps taking whole tiles in turn, not halves, made that 510,
+// and units of few tiles 5 to 20 % longer).  With units of a few tiles the fixed parts
+// show (4 us until the batch is laid out, 3 to the first scores, 5 for the join; a unit's
+// end of 2 us passes while the next tiles load): trees of 16 tokens on 32 sequences of 500
+// to 4000 keys take 63 us, 0.67 of the copy rate, although the tiles themselves pass at
+// all of it; 64 prompts of 128 tokens, units of one tile, 72 us.  One token on 777 keys
+// takes 13 us (14.5 launched behind what came before, not beside its end): this kernel's
+// chain for a single tile, and 4 the join's.  With one warp per row and head, and no
+// tensor cores, these took 130, 154, 6.7 and 0.4 ms.
 //
 // Warp roles (384 threads), as in the training forward (attn_fwd.cu):
 //   warps 0-7  softmax: warps w and w + 4 own the 32 rows of TMEM lane quarter
