@@ -12,10 +12,10 @@
 // second pass turns the output into e^(y - M) / L in place, out of L2, which a CTA's
 // rows do not leave in between: HBM sees 2 or 4 bytes read and 4 written per logit.
 // 320 bf16 rows of 151936 with histories, bias and mask take 124 us (127 among other
-// work), 66 without those, against 44 at HBM's rate: the CTAs of a row wait for one another between the
-// passes, with 32 warps an SM to cover it (the same with twice the loads in flight;
-// five rows together 137; C half as large, 145).  Keeping a row in registers between
-// the passes left fewer warps, 136 to 205 us.
+// work), 66 without those, against 44 at HBM's rate: the CTAs of a row wait for one
+// another between the passes, with 32 warps an SM to cover it (the same with twice the
+// loads in flight; five rows together 137; C half as large, 145).  Keeping a row in
+// registers between the passes left fewer warps, 136 to 205 us.
 //
 // The tokens that occur in the history are few against the vocabulary.  A bit map
 // holds the ones seen; a seen token's rank in it, from the running sum of its words'

@@ -230,8 +230,8 @@ struct Walk {
 // ones before the context's end.
 __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int o) {
   const int w = o >> 5;
-  const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? __ldg(row + w) : 0u);
-  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? __ldg(row + w + 1) : 0u);
+  const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? row[w] : 0u);
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? row[w + 1] : 0u);
   return __funnelshift_r(lo, hi, o & 31);
 }
 
@@ -422,15 +422,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  // What was launched before is complete from here on; all above ran beside its end.
+  // What was launched before is complete from here on; all above ran beside its end.  (It
+  // may have written the lists while this kernel ran: they are read by ordinary loads, not
+  // as constant data.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The batch: rows and lengths, each sequence's tiles (by a warp where it has more than a
   // few query tiles), their sums.
   int many = 0;
   for (int b = tid; b < B; b += kThreads) {
-    const int lo = max(0, min(__ldg(P.g.cu_q + b), P.N));
-    const int hi = max(lo, min(__ldg(P.g.cu_q + b + 1), P.N));
-    const int n = hi - lo, len = __ldg(P.g.seq_lens + b), tiles = (n + P.TT - 1) / P.TT;
+    const int lo = max(0, min(P.g.cu_q[b], P.N));
+    const int hi = max(lo, min(P.g.cu_q[b + 1], P.N));
+    const int n = hi - lo, len = P.g.seq_lens[b], tiles = (n + P.TT - 1) / P.TT;
     S.first[b] = lo;
     S.n[b] = n;
     S.len[b] = len;
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // This lane's page of a tile (-1: past the sequence's keys).
       auto look = [&](int t) {
         const int key = t * kTile + lane * box;
-        return lane < copies && t < s.t1 && key < s.have ? __ldg(table + (key >> P.g.page_shift))
+        return lane < copies && t < s.t1 && key < s.have ? table[key >> P.g.page_shift]
                                                           : -1;
       };
       int pg = look(s.t0);
