@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
   // Seen elements of one window are written over what the first pass stores, after
   // it; of more, the first pass leaves them out.
   const bool over = n_seen <= kWindow;
+  const bool in_place = A.z == static_cast<const void*>(A.out);
   auto store = [&](float* dst, const auto& y, uint32_t seen, bool second) {
     if constexpr (VEC) {
       if (!FILTER || over || seen == 0) {
@@ -432,14 +433,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
     for (int q = 0; q < n_rows; ++q) {
       float* const out = out0 + (uint32_t)q * V;
       Stat st = none;
-      // A listed element's value, before the output may overwrite its logit.
+      // A listed element's value.
       auto single = [&](int j, int v) {
         const float x[1] = {listed(j, q)};
         if constexpr (M == 2) return __fdiv_rn(x[0], t_raw);
         if constexpr (M < 2) add_values<M == 1>(st, x, c, [&](int) { return v; });
         return x[0];
       };
-      if (over && n_seen > 0) each_listed([&](int j, int v) { s_y[j] = single(j, v); });
+      if (over && n_seen > 0) {
+        each_listed([&](int j, int v) { s_y[j] = single(j, v); });
+        if (in_place) __syncthreads();  // the sweep below writes over those logits
+      }
       sweep(q, [&](auto& x, uint32_t seen, int v, bool second) {
         if constexpr (M == 2) {
 #pragma unroll

@@ -242,3 +242,40 @@ def test_stream_and_graph():
     tok.copy_(_i32([9, 8, 7, 6, 5]))
     gr.replay()
     assert torch.equal(got, ops.stt_logits_process(z.flip(0).contiguous(), **kw))
+
+
+@pytest.mark.parametrize("kind", ["softmax", "greedy", "raw"])
+@pytest.mark.parametrize("distinct", [1, 33, 300, 2000])
+@pytest.mark.parametrize("B,rows,V", [(2, 1, 33000), (2, 9, 33000), (2, 9, 33001), (900, 6, 4100)])
+def test_in_place_on_long_histories(B, rows, V, distinct, kind):
+    """Seen tokens crowded in the first block of the vocabulary, so that the threads of one
+    CTA have very different shares of them: the same bits in place as out of place, rows
+    alone and taken together, aligned and not, and as the oracle's."""
+    g, rng = gen(distinct + V), np.random.default_rng(distinct + V + B)
+    N, raw = B * rows, kind == "raw"
+    z = torch.randn(N, V, generator=g) * 4
+    lists = [list(rng.permutation(2048)[:distinct]) + list(rng.integers(0, V, 3)) for _ in range(B)]
+    n_prompt = [len(x) // 3 for x in lists]
+    dr = np.concatenate([np.asarray([x[:4] for x in lists]), rng.integers(0, V, (B, 4))], 1)
+    one = lambda v: torch.full((B,), v)  # noqa: E731
+    T = one(0.0 if kind == "greedy" else 0.7)
+    kw = dict(rows=rows, temperature=T.to(DEV), repetition=one(1.3).to(DEV),
+              frequency=one(0.2).to(DEV), presence=one(0.1).to(DEV),
+              tokens=_i32(np.concatenate(lists)),
+              cu_tokens=_i32(np.concatenate([[0], np.cumsum([len(x) for x in lists])])),
+              n_prompt=_i32(n_prompt), draft_tokens=_i32(dr), raw=raw)
+    zd = z.to(DEV)
+    want = ops.stt_logits_process(zd, **kw)
+    for _ in range(10):
+        got = zd.clone()
+        assert ops.stt_logits_process(got, out=got, **kw) is got
+        assert torch.equal(got, want)
+    few = slice(0, min(N, 2 * rows))  # the oracle takes its time
+    b = few.stop // rows
+    ref, M = ol.process(f64(z[few]), rows, T.double().numpy()[:b], np.full(b, np.float32(1.3)),
+                        np.full(b, np.float32(0.2)), np.full(b, np.float32(0.1)), lists[:b],
+                        n_prompt[:b], dr[:b], None, None, raw)
+    tol = 6 * FP32 * M[:, None] + 1e-30
+    if kind == "softmax":
+        tol = np.maximum((2 * tol + 2.0 ** -20) * np.abs(ref), 1e-36)
+    within(want[few], ref, 0.0 if kind == "greedy" else tol, kind)
