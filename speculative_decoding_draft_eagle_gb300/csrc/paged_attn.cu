@@ -329,7 +329,8 @@ __device__ __noinline__ bool plan_rounds(const Params& P, Batch& S, int n, int r
       return false;
   }
   if (none_left) {
-    for (int c = tid; c <= n; c += kThreads) S.start[c] = W;
+    if (tid < 32)  // the warp that reads a border before the next barrier
+      for (int c = tid; c <= n; c += 32) S.start[c] = W;
     return true;
   }
   if (tid < 32) {

@@ -410,3 +410,23 @@ def test_refusals():
     with pytest.raises(RuntimeError, match="WORKSPACE"):
         ops.stt_paged_attn(q, kc, vc, *lists, workspace=torch.empty(8, dtype=torch.uint8,
                                                                     device=DEV))
+
+
+def test_one_round_of_whole_units_is_repeatable():
+    """As many units as CTAs that take one, none left for runs, behind a sequence without
+    any: the plan's borders are read once they are all written, so launches agree."""
+    bt = Batch([0, 500], [9, 33000], 64, 8, 128, 13)
+    q = randn(gen(6), bt.N, 32, 128).to(DEV)
+    caches, lists = bt.caches(), bt.lists()
+    want = ops.stt_paged_attn(q, *caches, *lists)
+    for _ in range(5):
+        got = ops.stt_paged_attn(q, *caches, *lists)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    row = 137
+    k, v = (opg.gather(f64(c), bt.table[1], 33000 - 500 + row + 1)[:, 3] for c in (bt.k, bt.v))
+    s = k @ f64(q)[row, 13] / math.sqrt(128)
+    p = np.exp(s - s.max())
+    o = p / p.sum() @ v
+    within(f64(want[0])[row, 13], o,
+           BF16 * np.abs(o) + (BF16 + 2.0 ** -11) * (p / p.sum() @ np.abs(v)), "out")
+    assert ops.stt_device_error() == 0
