@@ -2,7 +2,8 @@
 
 Every computation runs in the CUDA library; torch supplies device memory,
 streams and output allocation.  Functions take torch CUDA tensors and enqueue
-on the current torch stream (or ``stream=``).
+on the current torch stream (or ``stream=``, which the caller orders after what
+its inputs come from, and before what reads its results).
 """
 
 from __future__ import annotations
@@ -381,12 +382,29 @@ _PAGES = struct.Struct("@PPPPPqqqiiiiii")
 _LOGITS = struct.Struct("@PPPPPPPPPPiii")
 
 
-def _current(stream):
-    """The current device, and the raw stream the call goes to."""
+def _current():
+    """The current device, and its current stream's handle."""
     dev = torch.cuda.current_device()
-    if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
-    return dev, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(stream, call, *args, held=()):
+    """`call` with `stream` (a torch stream or a handle) current: what it allocates belongs
+    to that stream.  Memory of the caller's stream may still be in use by work that was
+    queued there before; the other stream would write it without waiting for that.  The
+    caller's stream is recorded on the results, which it goes on to use, and `stream` on
+    what the caller gave to be written (the results, `held`)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    for t in (*(result if isinstance(result, tuple) else (result,)), *held):
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(here)
+    return result
 
 
 def _refuse(t, name, dtype, shape, dev):
@@ -438,30 +456,17 @@ def _new(shape, dtype, dev):
 _scratch_of = threading.local()
 
 
-def _scratch(n: int, dev: int, raw: int, stream) -> torch.Tensor:
-    """A workspace of n bytes for one call.  Eager calls of a thread on its current
-    stream follow one another there and share one, kept from call to call; a call that
-    is captured, or goes to another stream, has its own."""
-    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
+def _scratch(n: int, dev: int, raw: int) -> torch.Tensor:
+    """A workspace of n bytes for one call.  Eager calls of a thread on one stream
+    follow one another there and share one, kept from call to call; a call that is
+    captured has its own."""
+    if torch._C._cuda_isCurrentStreamCapturing():
         return _new((n,), torch.uint8, dev)
     kept = _scratch_of.__dict__
     t = kept.get((dev, raw))
     if t is None or t.numel() < n:
         t = kept[dev, raw] = _new((n,), torch.uint8, dev)
     return t
-
-
-def _keep(stream, *ts):
-    """Tensors allocated here (on the current stream) and used on `stream`: their
-    memory is not handed out again before that stream is done with them."""
-    if not isinstance(stream, torch.cuda.Stream):
-        if int(stream) == 0:
-            stream = torch.cuda.default_stream()
-        else:
-            stream = torch.cuda.ExternalStream(int(stream))
-    for t in ts:
-        if t is not None:
-            t.record_stream(stream)
 
 
 def rope_frequencies(R: int, base: float = 10000.0, factor: float = 1.0,
@@ -517,7 +522,10 @@ def stt_qkv_rope_fwd(qkv: torch.Tensor, H: int, H_kv: int, D: int,
     every query and key head with the weights w_q, w_k bf16 [D] (None: no norm), and
     rotation of each head's first 2 len(freq) elements by positions int32 [B, S]
     (None: 0..S-1) times freq (fp64 radians per position, see rope_frequencies)."""
-    dev, raw = _current(stream)
+    if stream is not None:
+        return _on(stream, stt_qkv_rope_fwd, qkv, H, H_kv, D, positions, freq, w_q, w_k, eps,
+                   interleaved, amplitude, q, k, v)
+    dev, raw = _current()
     if qkv.dim() != 3:
         raise ValueError("qkv must be [B, S, (H + 2 H_kv) D]")
     B, S, _ = qkv.shape
@@ -536,8 +544,6 @@ def stt_qkv_rope_fwd(qkv: torch.Tensor, H: int, H_kv: int, D: int,
         _arg(k, "k", bf16, (B, H_kv, S, D), dev), _arg(v, "v", bf16, (B, H_kv, S, D), dev), raw)
     if st:
         check("stt_qkv_rope_fwd", st)
-    if stream is not None:
-        _keep(stream, q, k, v)
     return q, k, v
 
 
@@ -557,7 +563,10 @@ def stt_qkv_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
     """Gradient of stt_qkv_rope_fwd from dq, dk, dv (all fp32 or all bf16, in the
     layout of q, k, v).  qkv is needed where a weight is given.  Returns (dqkv bf16
     [B, S, (H + 2 H_kv) D], dw_q, dw_k fp32 [D] or None)."""
-    dev, raw = _current(stream)
+    if stream is not None:
+        return _on(stream, stt_qkv_rope_bwd, dq, dk, dv, qkv, positions, freq, w_q, w_k, eps,
+                   interleaved, amplitude, dqkv, dw_q, dw_k, workspace, held=(workspace,))
+    dev, raw = _current()
     if dq.dim() != 4 or dk.dim() != 4:
         raise ValueError("dq must be [B, H, S, D] and dk, dv [B, H_kv, S, D]")
     B, H, S, D = dq.shape
@@ -594,7 +603,7 @@ def stt_qkv_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
     if norm:
         if workspace is None:
             n_ws = lib().stt_qkv_rope_bwd_workspace_size(D)
-            workspace = _scratch(n_ws, dev, raw, stream)
+            workspace = _scratch(n_ws, dev, raw)
             p_ws = workspace.data_ptr()
         else:
             p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
@@ -606,8 +615,6 @@ def stt_qkv_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor,
         p_wk, p_ws, n_ws, raw)
     if st:
         check("stt_qkv_rope_bwd", st)
-    if stream is not None:
-        _keep(stream, dqkv, dw_q, dw_k, workspace)
     return dqkv, dw_q, dw_k
 
 
@@ -651,7 +658,10 @@ def stt_kv_append(qkv: torch.Tensor, H: int, k_cache: torch.Tensor, v_cache: tor
     its transpose).  Norm and rotation as stt_qkv_rope_fwd, at positions int32 [N]
     (None: the key's index).  Returns the queries bf16 [N, H, D]; rows behind the
     last sequence are left as they are."""
-    dev, raw = _current(stream)
+    if stream is not None:
+        return _on(stream, stt_kv_append, qkv, H, k_cache, v_cache, cu_q, seq_lens, page_table,
+                   positions, freq, w_q, w_k, eps, interleaved, amplitude, q)
+    dev, raw = _current()
     pages, H_kv, D, _ = _pages(k_cache, v_cache, cu_q, seq_lens, page_table, dev)
     if qkv.dim() != 2:
         raise ValueError("qkv must be [N, (H + 2 H_kv) D]")
@@ -665,8 +675,6 @@ def stt_kv_append(qkv: torch.Tensor, H: int, k_cache: torch.Tensor, v_cache: tor
         N, H, pages, rope, _arg(q, "q", torch.bfloat16, (N, H, D), dev), raw)
     if st:
         check("stt_kv_append", st)
-    if stream is not None:
-        _keep(stream, q)
     return q
 
 
@@ -687,7 +695,10 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     and new token j iff bit j % 32 of word j / 32 of its row is set.
     Returns (out bf16 [N, H, D], lse fp32 [N, H]); rows behind the last sequence are
     left as they are."""
-    dev, raw = _current(stream)
+    if stream is not None:
+        return _on(stream, stt_paged_attn, q, k_cache, v_cache, cu_q, seq_lens, page_table,
+                   scale, tree_mask, out, lse, workspace, held=(workspace,))
+    dev, raw = _current()
     pages, H_kv, D, B = _pages(k_cache, v_cache, cu_q, seq_lens, page_table, dev)
     if q.dim() != 3 or q.shape[2] != D or q.dtype is not torch.bfloat16 or q.get_device() != dev:
         raise ValueError(f"q must be bfloat16 [N, H, {D}] on cuda:{dev}")
@@ -712,7 +723,7 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     L = lib()
     if workspace is None:
         n_ws = L.stt_paged_attn_workspace_size(N, B, H, H_kv, D)
-        workspace = _scratch(n_ws, dev, raw, stream)
+        workspace = _scratch(n_ws, dev, raw)
         p_ws = workspace.data_ptr()
     else:
         p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
@@ -723,8 +734,6 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         _arg(lse, "lse", torch.float32, (N, H), dev), p_ws, n_ws, raw)
     if st:
         check("stt_paged_attn", st)
-    if stream is not None:
-        _keep(stream, out, lse, workspace)
     return out, lse
 
 
@@ -755,7 +764,10 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
     draft_tokens int32 [B, >= rows - 1].  bias fp32 [V], [1, V] or [B, V]; mask int32
     [N, ceil(V / 32)], bit v % 32 of word v / 32 set where v is allowed.  out may be z
     itself where that is fp32."""
-    dev, on = _current(stream)
+    if stream is not None:
+        return _on(stream, stt_logits_process, z, rows, temperature, repetition, frequency,
+                   presence, tokens, cu_tokens, n_prompt, draft_tokens, bias, mask, raw, out)
+    dev, on = _current()
     if z.dim() != 2:
         raise ValueError("z must be [N, V]")
     N, V = z.shape
@@ -809,8 +821,6 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
         _arg(out, "out", f32, (N, V), dev), on)
     if st:
         check("stt_logits_process", st)
-    if stream is not None:
-        _keep(stream, out)
     return out
 
 

@@ -141,3 +141,57 @@ def test_training_step():
     assert rel <= 7 * BF16, rel
     for a, b in ((dwq, rwq), (dwk, rwk)):
         assert np.linalg.norm(f64(a) - b) <= 7 * BF16 * np.linalg.norm(b)
+
+
+def _busy_block(nbytes):
+    """Address of memory of the current stream that is free again for that stream while
+    its last writer there is still queued."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    t = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    torch.cuda._sleep(200_000_000)       # about a tenth of a second
+    t.fill_(0xFF)
+    return t.data_ptr(), t.untyped_storage().nbytes()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_another_stream_does_not_write_what_this_one_still_uses(captured):
+    """With stream=, results and workspaces are that stream's own memory: not blocks that
+    the caller's stream is yet to finish with."""
+    from _serving import Batch
+    g = gen(21)
+    H, H_kv, D, n = 8, 2, 128, 24
+    bt = Batch([n], [700], 16, H_kv, D, 4)
+    kc, vc = bt.caches()
+    lists = bt.lists()
+    qkv = randn(g, n, (H + 2 * H_kv) * D).to(DEV)
+    rows, freq = qkv.view(1, n, -1), ops.rope_frequencies(D)
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    z = torch.randn(40, 32000, generator=g).to(DEV)
+    dys = [t.float() for t in ops.stt_qkv_rope_fwd(rows, H, H_kv, D, None, freq, w, w)]
+    q0 = ops.stt_kv_append(qkv, H, kc, vc, *lists, None, freq)
+    calls = [lambda **kw: ops.stt_qkv_rope_fwd(rows, H, H_kv, D, None, freq, w, w, **kw),
+             lambda **kw: ops.stt_qkv_rope_bwd(*dys, rows, None, freq, w, w, **kw),
+             lambda **kw: (ops.stt_kv_append(qkv, H, kc, vc, *lists, None, freq, **kw),),
+             lambda **kw: ops.stt_paged_attn(q0, kc, vc, *lists, **kw),
+             lambda **kw: (ops.stt_logits_process(z, **kw),)]
+    want = [c() for c in calls]
+    for call, ref in zip(calls, want):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())   # the inputs
+        if captured:
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                side.wait_stream(torch.cuda.current_stream())
+                got = call(stream=side)
+                torch.cuda.current_stream().wait_stream(side)
+            gr.replay()
+        else:
+            size = sum(t.numel() * t.element_size() for t in ref)
+            low, length = _busy_block(max(size, 1 << 25))
+            got = call(stream=side)
+            for t in got:
+                assert not low <= t.data_ptr() < low + length
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert ops.stt_device_error() == 0
