@@ -57,6 +57,28 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _on(stream, call, *args, held=()):
+    """`call` with `stream` (a torch stream or a handle) current: what it allocates belongs
+    to that stream.  Memory of the caller's stream may still be in use by work that was
+    queued there before; the other stream would write it without waiting for that.  The
+    caller's stream is recorded on the results, which it goes on to use, and `stream` on
+    what the caller gave to be written (the results, `held`)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    if stream == here:
+        return call(*args)
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    for r in (*(result if isinstance(result, tuple) else (result,)), *held):
+        for t in r if isinstance(r, (list, tuple)) else (r,):
+            if t is not None:
+                t.record_stream(stream)
+                t.record_stream(here)
+    return result
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -102,6 +124,8 @@ def stt_attn_fwd(q: torch.Tensor, k_blocks: Sequence[torch.Tensor],
     """Sparse-tree TTT attention forward at step k = len(k_blocks) - 1.
 
     Returns (out bf16 [B,H,Q_LEN,D], lse fp32 [B,H,Q_LEN])."""
+    if stream is not None:
+        return _on(stream, stt_attn_fwd, q, k_blocks, v_blocks, T, scale, out, lse)
     B, H, H_kv, D, Q_LEN, k, T_arr = _attn_dims(q, k_blocks, v_blocks, T)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     if out is None:
@@ -128,6 +152,9 @@ def stt_attn_bwd(q: torch.Tensor, k_blocks: Sequence[torch.Tensor],
                  dv_blocks: Optional[List[torch.Tensor]] = None,
                  workspace: Optional[torch.Tensor] = None, stream=None):
     """Backward of stt_attn_fwd.  Returns (dq, dk_blocks, dv_blocks), all fp32."""
+    if stream is not None:
+        return _on(stream, stt_attn_bwd, q, k_blocks, v_blocks, T, out, dout, lse, scale,
+                   dq, dk_blocks, dv_blocks, workspace, held=(workspace,))
     B, H, H_kv, D, Q_LEN, k, T_arr = _attn_dims(q, k_blocks, v_blocks, T)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _need(out, "out", torch.bfloat16, q.shape)
@@ -174,6 +201,9 @@ def stt_attn_bwd_ex(q: torch.Tensor, k_blocks: Sequence[torch.Tensor],
     bf16 (the dtype of ``dq`` selects STT_BWD_BF16_GRADS).  With ``accumulate``
     the block gradients are added to dk_blocks / dv_blocks (STT_BWD_ACCUMULATE_KV);
     dq is always overwritten."""
+    if stream is not None:
+        return _on(stream, stt_attn_bwd_ex, q, k_blocks, v_blocks, T, out, dout, lse, dq,
+                   dk_blocks, dv_blocks, scale, accumulate, workspace, held=(workspace,))
     B, H, H_kv, D, Q_LEN, k, T_arr = _attn_dims(q, k_blocks, v_blocks, T)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _need(out, "out", torch.bfloat16, q.shape)
@@ -213,6 +243,9 @@ def soft_ce_fwd_bwd_inplace(z: torch.Tensor, p: torch.Tensor, g: torch.Tensor,
                             workspace: Optional[torch.Tensor] = None, want_row_loss: bool = True,
                             stream=None):
     """In-place soft-CE: z is overwritten with dL/dz.  Returns (loss [1], row_loss [N] or None)."""
+    if stream is not None:
+        return _on(stream, soft_ce_fwd_bwd_inplace, z, p, g, row_loss, loss, workspace,
+                   want_row_loss, held=(z, workspace))
     if z.dim() != 2:
         raise ValueError("z must be [N, V]")
     N, V = z.shape
@@ -250,6 +283,9 @@ def soft_ce_fwd_bwd_inplace_ex(z: torch.Tensor, p: torch.Tensor, g: torch.Tensor
     bf16 (STT_CE_BF16), g fp32 of shape [N] (per row) or [N, V] (per element,
     STT_CE_G_PER_ELEMENT).  z is overwritten with dL/dz in its own dtype.
     Returns (loss [1], row_loss [N])."""
+    if stream is not None:
+        return _on(stream, soft_ce_fwd_bwd_inplace_ex, z, p, g, row_loss, loss, workspace,
+                   held=(z, workspace))
     if z.dim() != 2:
         raise ValueError("z must be [N, V]")
     N, V = z.shape
@@ -287,6 +323,9 @@ def soft_ce_fwd_bwd_inplace_noalloc(z: torch.Tensor, p: torch.Tensor, g: torch.T
     """Same as soft_ce_fwd_bwd_inplace but without a workspace: the library's own
     fixed scratch is used (at most 65536 rows), for callers that cannot allocate
     device memory.  Calls must not overlap on the GPU."""
+    if stream is not None:
+        return _on(stream, soft_ce_fwd_bwd_inplace_noalloc, z, p, g, row_loss, loss,
+                   held=(z,))
     if z.dim() != 2:
         raise ValueError("z must be [N, V]")
     N, V = z.shape
@@ -314,6 +353,9 @@ def stt_lm_head_ce(h: torch.Tensor, W: torch.Tensor, p: torch.Tensor, g: torch.T
     """Draft LM head z = h W^T fused with the soft-CE: loss and the fp32 gradients
     of h [N, Hd] and W [V, Hd] (both bf16), z never materialised.
     Returns (loss [1], row_loss [N], dh [N, Hd], dW [V, Hd])."""
+    if stream is not None:
+        return _on(stream, stt_lm_head_ce, h, W, p, g, dh, dW, row_loss, loss, workspace,
+                   held=(workspace,))
     if h.dim() != 2 or W.dim() != 2:
         raise ValueError("h must be [N, Hd] and W [V, Hd]")
     N, Hd = h.shape
@@ -352,6 +394,9 @@ def stt_verify(p_target: torch.Tensor, p_draft: torch.Tensor, draft_tokens: torc
     """Rejection-sampling verification of draft tokens.  p_target, p_draft fp32
     [B, gamma, V]; draft_tokens int32 [B, gamma]; u_accept fp32 [B, gamma];
     u_sample fp32 [B].  Returns (n_accepted int32 [B], out_tokens int32 [B, gamma])."""
+    if stream is not None:
+        return _on(stream, stt_verify, p_target, p_draft, draft_tokens, u_accept, u_sample,
+                   n_accepted, out_tokens)
     if p_target.dim() != 3:
         raise ValueError("p_target must be [B, gamma, V]")
     B, gamma, V = p_target.shape
@@ -386,25 +431,6 @@ def _current():
     """The current device, and its current stream's handle."""
     dev = torch.cuda.current_device()
     return dev, torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _on(stream, call, *args, held=()):
-    """`call` with `stream` (a torch stream or a handle) current: what it allocates belongs
-    to that stream.  Memory of the caller's stream may still be in use by work that was
-    queued there before; the other stream would write it without waiting for that.  The
-    caller's stream is recorded on the results, which it goes on to use, and `stream` on
-    what the caller gave to be written (the results, `held`)."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(stream)
-        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-    here = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
-        result = call(*args)
-    for t in (*(result if isinstance(result, tuple) else (result,)), *held):
-        if t is not None:
-            t.record_stream(stream)
-            t.record_stream(here)
-    return result
 
 
 def _refuse(t, name, dtype, shape, dev):
