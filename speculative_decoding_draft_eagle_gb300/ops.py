@@ -738,8 +738,8 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             ld = s[0]
     words, tree = 0, None
     if tree_mask is not None:
-        if tree_mask.dim() != 2:
-            raise ValueError("tree_mask must be [N, words]")
+        if tree_mask.dim() != 2 or (N > 0 and tree_mask.shape[1] == 0):
+            raise ValueError("tree_mask must be [N, words], at least one word")
         words = tree_mask.shape[1]
         tree = _arg(tree_mask, "tree_mask", torch.int32, (N, words), dev)
     if out is None:

@@ -147,3 +147,25 @@ def test_logits_refusals(L):
     assert call(bias=GOOD) == -1 and call(bias_rows=1) == -1 and call(bias=GOOD, bias_rows=3) == -1
     assert call(temperature=GOOD + 2) == -3 and call(z=GOOD + 2) == -3
     assert L.stt_logits_process(GOOD, 4, 100, 2, None, 0, GOOD, None) == -1
+
+
+def test_a_tree_mask_without_words_is_refused(monkeypatch):
+    """An empty mask has no address, which the library takes for no mask at all: causal
+    attention in place of new tokens that nobody sees."""
+    import torch
+    from speculative_decoding_draft_eagle_gb300 import ops
+
+    class Library:
+        def stt_paged_attn(self, *a):
+            pytest.fail("the call reached the library")
+
+    monkeypatch.setattr(ops, "_current", lambda: (-1, 0))     # CPU tensors pass for the device's
+    monkeypatch.setattr(ops, "lib", Library)
+    bf16, i32 = torch.bfloat16, torch.int32
+    cache = torch.zeros(3, 2, 16, 64, dtype=bf16)
+    q, out, lse = torch.zeros(4, 4, 64, dtype=bf16), torch.zeros(4, 4, 64, dtype=bf16), torch.zeros(4, 4)
+    lists = (torch.tensor([0, 4], dtype=i32), torch.tensor([9], dtype=i32),
+             torch.zeros(1, 2, dtype=i32))
+    with pytest.raises(ValueError, match="tree_mask"):
+        ops.stt_paged_attn(q, cache, cache, *lists, tree_mask=torch.zeros(4, 0, dtype=i32), out=out,
+                           lse=lse, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
