@@ -113,12 +113,15 @@ STT_API int stt_device_error(void* stream, uint32_t* word);
  *                              every copy already issued is waited for before
  *                              the CTA exits, and no tensor-core product is
  *                              issued.
+ *   STT_INJECT_LOGITS_WITHHOLD_PAIRS  the first CTA of a row that several share
+ *                              does not send the others its maximum and sum.
  * 0 switches injection off.  Unknown bits return STT_ERR_INVALID_ARG.  The
  * setting is process-wide; it is meant for tests, never for production runs.
  */
 STT_API int stt_debug_set_wait_budget(uint64_t ns);
 STT_API int stt_debug_inject(uint32_t what);
 #define STT_INJECT_FWD_WITHHOLD_Q 0x1u
+#define STT_INJECT_LOGITS_WITHHOLD_PAIRS 0x2u
 
 /* --------------------------------------------------------------------------
  * Sparse-tree attention, forward.

@@ -53,6 +53,7 @@ struct Params {
   int C, log_c;            // CTAs per row (a power of two)
   int groups, group_rows;  // row groups of a sequence, rows of a group
   int words;               // of the bit map
+  bool withhold;           // test hook: the first CTA of a row sends no pairs
 };
 
 // A logit after the penalties, each step rounded as written.
@@ -478,13 +479,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
     const float4 p = make_float4(s.m, s.l, 0.f, 0.f);
     if (P.C == 1) {
       if (lane == 0) s_pair[warp][0] = p;
-    } else if (lane < P.C) {
+    } else if (lane < P.C && !(P.withhold && rank == 0)) {
       st_async_f4(mapa_shared(smem_u32(&s_pair[warp][rank]), (uint32_t)lane), p,
                   mapa_shared(smem_u32(&bar_pair), (uint32_t)lane));
     }
   }
-  if (P.C > 1) mbar_wait_cluster(&bar_pair, 0, STT_DEVERR_LOGITS_WAIT);
-  else __syncthreads();
+  if (P.C > 1) {
+    cluster_arrive_release();  // this CTA has sent its pairs
+    mbar_wait_cluster(&bar_pair, 0, STT_DEVERR_LOGITS_WAIT);
+  } else {
+    __syncthreads();
+  }
 
   // ----------------------------------------------- second pass: the results --
   for (int q = 0; q < n_rows; ++q) {
@@ -532,6 +537,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
         out[v] = greedy ? (v == best ? 1.f : 0.f) : ex2((out[v] - top) * c) * inv;
       }
     }
+  }
+  // A CTA whose wait gave up may not leave while pairs are on their way to it: everyone
+  // has sent theirs, and they have landed.
+  if (P.C > 1) {
+    cluster_wait_acquire();
+    if (tid == 0) mbar_wait_cluster(&bar_pair, 0, STT_DEVERR_LOGITS_WAIT);
   }
 }
 
@@ -582,6 +593,7 @@ cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s) {
       logits_kernel<__nv_bfloat16, true, false>, logits_kernel<__nv_bfloat16, true, true>};
   const Kernel kern = kernels[which];
   P.words = blocks_of(C) * (kBlock / 32);
+  P.withhold = (debug_inject() & STT_INJECT_LOGITS_WITHHOLD_PAIRS) != 0;
   const int smem = (a.tokens || a.draft) ? P.words * 8 : 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -77,3 +77,28 @@ def test_status_code_of_a_timeout():
     assert st == -5 and (w.value & STT_DEVERR_FWD_WAIT)
     w2 = ctypes.c_uint32(7)
     assert L.stt_device_error(None, ctypes.byref(w2)) == 0 and w2.value == 0
+
+
+STT_INJECT_LOGITS_WITHHOLD_PAIRS = 0x2
+STT_DEVERR_LOGITS_WAIT = 0x80
+
+
+@pytest.mark.parametrize("mask", [False, True])
+def test_logits_wait_runs_out_and_context_survives(mask):
+    """A row's CTAs wait for a pair that is never sent, give up, and leave together."""
+    g = torch.Generator().manual_seed(1)
+    z = torch.randn(6, 40000, generator=g).cuda()
+    kw = dict(mask=torch.full((6, 1250), -1, dtype=torch.int32, device="cuda")) if mask else {}
+    want = ops.stt_logits_process(z, **kw)
+    assert ops.stt_device_error() == 0
+    try:
+        ops.stt_debug_set_wait_budget(1_000_000)      # 1 ms
+        ops.stt_debug_inject(STT_INJECT_LOGITS_WITHHOLD_PAIRS)
+        ops.stt_logits_process(z, **kw)
+        word = ops.stt_device_error()
+    finally:
+        ops.stt_debug_inject(0)
+        ops.stt_debug_set_wait_budget(0)
+    assert word & STT_DEVERR_LOGITS_WAIT, f"error word {word:#x}"
+    assert torch.equal(ops.stt_logits_process(z, **kw), want)
+    assert ops.stt_device_error() == 0
