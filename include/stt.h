@@ -115,6 +115,8 @@ STT_API int stt_device_error(void* stream, uint32_t* word);
  *                              issued.
  *   STT_INJECT_LOGITS_WITHHOLD_PAIRS  the first CTA of a row that several share
  *                              does not send the others its maximum and sum.
+ *   STT_INJECT_PAGED_WITHHOLD_Q  the paged attention's producer never loads
+ *                              queries, as the attention forward's.
  * 0 switches injection off.  Unknown bits return STT_ERR_INVALID_ARG.  The
  * setting is process-wide; it is meant for tests, never for production runs.
  */
@@ -122,6 +124,7 @@ STT_API int stt_debug_set_wait_budget(uint64_t ns);
 STT_API int stt_debug_inject(uint32_t what);
 #define STT_INJECT_FWD_WITHHOLD_Q 0x1u
 #define STT_INJECT_LOGITS_WITHHOLD_PAIRS 0x2u
+#define STT_INJECT_PAGED_WITHHOLD_Q 0x4u
 
 /* --------------------------------------------------------------------------
  * Sparse-tree attention, forward.

@@ -88,6 +88,7 @@ struct Params {
   int key_cap;       // max_pages * page_size
   int d_tok, d_head, d_page;  // place of each among the cache map's outer dimensions
   float scale_log2;
+  uint32_t inject;  // STT_INJECT_* test hooks (0 in normal use)
 };
 
 template <int D>
@@ -544,13 +545,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qs = i & 1;
         if (i >= 2) ok = warp_wait(&bar_q_empty[qs], ((i >> 1) - 1u) & 1u, kSite);
         if (!ok) break;
-        if (lane == 0) {
+        // Test hook: queries are never loaded, the S issuer's wait for them runs out, and
+        // every role gives up in turn.
+        const bool withhold = (P.inject & STT_INJECT_PAGED_WITHHOLD_Q) != 0;
+        if (lane == 0 && !withhold) {
           mbar_arrive_expect_tx(&bar_q_full[qs], (uint32_t)(P.G * P.TT * D * 2));
           for (int cb = 0; cb < D / kColBlock; ++cb)
             tma_load_3d(smem + L::q + qs * L::kQ + cb * kTile * 128, &tmQ, &bar_q_full[qs],
                         cb * kColBlock, s.h * P.G, s.tok0);
         }
-        q_issued = i + 1;
+        if (!withhold) q_issued = i + 1;
       }
       const int32_t* table = P.g.table + (int64_t)s.b * P.g.max_pages;
       // This lane's page of a tile (-1: past the sequence's keys).
@@ -591,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // gave up, too).
     for (uint32_t x = g > (uint32_t)kStages ? g - kStages : 0; x < g; ++x)
       mbar_wait(&full[x & 1], (x >> 1) & 1u, kSite);
-    if (q_issued > 0) mbar_wait(&bar_q_full[(q_issued - 1) & 1], ((q_issued - 1) >> 1) & 1u, kSite);
+    for (uint32_t x = q_issued > 2 ? q_issued - 2 : 0; x < q_issued; ++x)
+      mbar_wait(&bar_q_full[x & 1], (x >> 1) & 1u, kSite);
   } else if (warp == kWarpMma || warp == kWarpPv) {
     // ------------------------------------------------------- MMA issuers --
     if (lane == 0) {
@@ -1105,6 +1110,7 @@ cudaError_t launch(const PagesArgs& pg, const PagedAttnArgs& a, cudaStream_t s) 
   P.slot = slot_floats(P.slot_rows, D);
   P.key_cap = pg.max_pages << pg.page_shift;
   P.scale_log2 = a.scale * kLog2e;
+  P.inject = debug_inject();
   P.join = static_cast<JoinDesc*>(a.workspace);
   P.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + kJoinBytes);
   CUtensorMap tmQ, tmK, tmV;

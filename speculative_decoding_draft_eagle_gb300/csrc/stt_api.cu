@@ -253,7 +253,8 @@ int stt_debug_set_wait_budget(uint64_t ns) {
 }
 
 int stt_debug_inject(uint32_t what) {
-  if (what & ~(uint32_t)(STT_INJECT_FWD_WITHHOLD_Q | STT_INJECT_LOGITS_WITHHOLD_PAIRS))
+  if (what & ~(uint32_t)(STT_INJECT_FWD_WITHHOLD_Q | STT_INJECT_LOGITS_WITHHOLD_PAIRS |
+                         STT_INJECT_PAGED_WITHHOLD_Q))
     return STT_ERR_INVALID_ARG;
   stt::g_inject.store(what, std::memory_order_relaxed);
   return STT_OK;

@@ -102,3 +102,29 @@ def test_logits_wait_runs_out_and_context_survives(mask):
     assert word & STT_DEVERR_LOGITS_WAIT, f"error word {word:#x}"
     assert torch.equal(ops.stt_logits_process(z, **kw), want)
     assert ops.stt_device_error() == 0
+
+
+STT_INJECT_PAGED_WITHHOLD_Q = 0x4
+STT_DEVERR_PAGED_WAIT = 0x40
+
+
+@pytest.mark.parametrize("new,lens", [([1], [40]), ([3, 40, 0, 5], [700, 3000, 5, 90])])
+def test_paged_attn_wait_runs_out_and_context_survives(new, lens):
+    from _serving import Batch, gen, randn
+    bt = Batch(new, lens, 16, 2, 128, 5)
+    q = randn(gen(1), bt.N, 8, 128).cuda()
+    args = (q, *bt.caches(), *bt.lists())
+    want = ops.stt_paged_attn(*args)
+    assert ops.stt_device_error() == 0
+    try:
+        ops.stt_debug_set_wait_budget(1_000_000)      # 1 ms
+        ops.stt_debug_inject(STT_INJECT_PAGED_WITHHOLD_Q)
+        ops.stt_paged_attn(*args)
+        word = ops.stt_device_error()
+    finally:
+        ops.stt_debug_inject(0)
+        ops.stt_debug_set_wait_budget(0)
+    assert word & STT_DEVERR_PAGED_WAIT, f"error word {word:#x}"
+    got = ops.stt_paged_attn(*args)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert ops.stt_device_error() == 0
