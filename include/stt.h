@@ -533,8 +533,8 @@ STT_API int stt_paged_attn(const void* q, int64_t ld_q, int64_t N, int H, const 
  *  N        rows, >= 0, a multiple of `rows` >= 1.   V  >= 1.
  *  temperature, repetition, frequency, presence  fp32 [N / rows] or NULL (1, 1,
  *           0, 0).  temperature = 0 is greedy: the distribution is 1 at the
- *           largest z (the lowest such v) and 0 elsewhere.  temperature >= 0 and
- *           repetition > 0 are the caller's to see to.
+ *           largest z (the lowest such v) and 0 elsewhere.  That all are finite,
+ *           temperature >= 0 and repetition > 0 is the caller's to see to.
  *  tokens, cu_tokens, n_prompt  int32; all NULL without a history (n_prompt
  *           NULL alone: no prompt).  n_tokens: length of tokens, past which
  *           nothing is read.

@@ -28,6 +28,7 @@
 // greedy row's pair is its largest value and the lowest index that has it.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "../../include/stt.h"
@@ -422,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
 
   // ------------------------------------------ first pass: processed logits --
   const bool greedy = temp == 0.f && !A.raw;
-  const float c = temp > 0.f ? __fdiv_rn(kLog2E, temp) : 1.f, t_raw = temp > 0.f ? temp : 1.f;
+  // (Below about 2^-127 the quotient is infinite: the largest number instead, by which
+  // any difference of logits gives a probability of 0 and none stays 0, not NaN.)
+  const float c = temp > 0.f ? fminf(__fdiv_rn(kLog2E, temp), FLT_MAX) : 1.f;
+  const float t_raw = temp > 0.f ? temp : 1.f;
   const Stat none = {-INFINITY, greedy ? __int_as_float(0x7fffffff) : 0.f};
   // Without mask and history the second pass takes the logits again, which are in L2 as
   // well: nothing is written twice (320 bf16 rows of 151936: 80 -> 66 us, with a bias 91 ->

@@ -279,3 +279,17 @@ def test_in_place_on_long_histories(B, rows, V, distinct, kind):
     if kind == "softmax":
         tol = np.maximum((2 * tol + 2.0 ** -20) * np.abs(ref), 1e-36)
     within(want[few], ref, 0.0 if kind == "greedy" else tol, kind)
+
+
+def test_extreme_temperatures():
+    """Down to the smallest numbers, whose reciprocal overflows, and up to the largest."""
+    T = torch.tensor([1e-45, 1e-39, 1e-38, 1e-30, 1e30, 3e38])
+    z = torch.randn(6, 9000, generator=gen(11)) * 4
+    z[:, 77] = z[:, 4321] = 30.0                         # two largest ones
+    mask = np.ones((6, 9000), bool)
+    mask[:, 5] = False
+    for kw in ({}, {"mask": _pack(mask)}):
+        got = ops.stt_logits_process(z.to(DEV), temperature=T.to(DEV), **kw)
+        want, _ = ol.process(f64(z), 1, f64(T), mask=mask if kw else None)
+        # tiny ones: halves, exactly; large ones: equal shares, each exponential within 2^-20
+        within(got, want, np.where(f64(T)[:, None] < 1, 0.0, 2.0 ** -19 * want), "out")
