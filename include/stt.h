@@ -455,10 +455,13 @@ STT_API int stt_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, con
  *  page_size a power of two, 8..1024 (STT_ERR_UNSUPPORTED otherwise).
  *  num_pages >= 1, max_pages >= 1; max_pages * page_size <= 2^30.
  *
- * A page outside [0, num_pages), or a key at or past max_pages * page_size or
- * before 0, is never read or written: it is skipped and reported as
- * STT_DEVERR_PAGE in the device error word, and the attention of that sequence
- * is undefined.
+ * A page outside [0, num_pages), or a key at or past max_pages * page_size, is
+ * never read or written: it is skipped and reported as STT_DEVERR_PAGE in the
+ * device error word, and the attention of that sequence is undefined.  A key
+ * before 0 (a sequence with more new tokens than keys): stt_kv_append skips and
+ * reports it too; stt_paged_attn reports nothing, there is no such key to see, and
+ * a row whose own key lies there sees none (zeros, -inf) unless a tree's bit shows
+ * it a later one.
  * ------------------------------------------------------------------------ */
 typedef struct {
   void* k;
