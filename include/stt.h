@@ -528,7 +528,8 @@ STT_API int stt_paged_attn(const void* q, int64_t ld_q, int64_t N, int H, const 
  *     out = softmax(z / temperature)
  * The history of row (b, i) is tokens[cu_tokens[b]..cu_tokens[b+1]), the first
  * n_prompt[b] of them the prompt and the rest output, and then the draft's
- * tokens 0..i-1, output too.  Tokens outside [0, V) count for nothing.
+ * tokens 0..i-1, output too.  Tokens outside [0, V) count for nothing.  (The draft
+ * is a chain, as in stt_verify; each path of a tree goes as a sequence of its own.)
  *
  *  z        fp32 [N, V], or bf16 with STT_LOGITS_BF16.  A forbidden element may
  *           hold anything; NaN or +inf elsewhere makes its row's probabilities

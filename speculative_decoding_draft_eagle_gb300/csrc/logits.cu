@@ -11,11 +11,15 @@
 // e^(y - m); the pairs of all rows are exchanged with the other CTAs at once; and a
 // second pass turns the output into e^(y - M) / L in place, out of L2, which a CTA's
 // rows do not leave in between: HBM sees 2 or 4 bytes read and 4 written per logit.
-// 320 bf16 rows of 151936 with histories, bias and mask take 124 us (127 among other
-// work), 66 without those, against 44 at HBM's rate: the CTAs of a row wait for one
-// another between the passes, with 32 warps an SM to cover it (the same with twice the
-// loads in flight; five rows together 137; C half as large, 145).  Keeping a row in
-// registers between the passes left fewer warps, 136 to 205 us.
+// 320 bf16 rows of 151936 with histories, bias and mask take 129 us against 44 at HBM's
+// rate.  Without any of them they take 66, with the bias 85, the mask 87, the history 109
+// alone: each CTA of each row (group) scans its sequence's history twice and ranks its
+// bit map, the filter costs instructions and a second write of the output, and between
+// the passes a row's CTAs wait for one another, with 32 warps an SM to cover it (the same
+// with twice the loads in flight; five rows together 137; C half as large, 145).  Keeping
+// a row in registers between the passes left fewer warps, 136 to 205 us.  Histories of
+// 20000 tokens: 341 us.  Rows that are not aligned to four elements go one element at a
+// time: 320 bf16 rows of 50257 take 162 us, of 50256 62.
 //
 // The tokens that occur in the history are few against the vocabulary.  A bit map
 // holds the ones seen; a seen token's rank in it, from the running sum of its words'
@@ -42,9 +46,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxRows = 8;             // rows a cluster takes together
 constexpr int kBlock = 8 * kThreads;    // consecutive logits of a CTA
-constexpr int kBlocksMax = 10;          // blocks of a CTA at most, where C allows
+constexpr int kBlocksMax = 10;          // blocks of a CTA at most, where C allows (*)
 constexpr int kCtasPerSm = 4;           // by registers
-constexpr int kFill = 16;               // CTAs an SM before rows are taken together
+constexpr int kFill = 16;               // CTAs an SM before rows are taken together (*)
+// (*) Chosen on 64 x 5 rows of 151936; other values were not tried on other vocabularies.
 constexpr int kWindow = 2048;           // seen tokens counted at a time
 constexpr uint32_t kPrompt = 0x80000000u;  // the token is in the prompt
 constexpr float kLog2E = 1.4426950408889634f;
@@ -199,9 +204,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
   __syncthreads();
   if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to a neighbour
 
-  // Hands f(v, what) every token of the slice in the history: `what` is kPrompt, 1
-  // for one of the output (draft tokens before this group among it), or 0 for a draft
-  // token of the group, which its later rows count themselves.
   // A token's place among this CTA's logits, or -1.
   auto mine = [&](int token) {
     const uint32_t t = (uint32_t)token, block = t / kBlock;
@@ -209,6 +211,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logits_kernel(const __gr
                ? (int)((block >> P.log_c) * kBlock + t % kBlock)
                : -1;
   };
+  // Hands f(place, what) every token of the slice in the history: `what` is kPrompt, 1
+  // for one of the output (draft tokens before this group among it), or 0 for a draft
+  // token of the group, which its later rows count themselves.
   auto scan_history = [&](auto&& f) {
     if (A.tokens) {
       const int t0 = max(0, min(A.cu_tokens[b], A.n_tokens));

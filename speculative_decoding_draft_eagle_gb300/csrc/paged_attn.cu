@@ -787,6 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    sl2x2, negm2),
                          x0, x1);
             const float p0 = ex2(x0), p1 = ex2(x1);
+            // The sum takes P in fp32, the product with V in bf16, as in the training forward
+            // (the tensor cores have tf32 at half the rate, and fp32 not at all): an output's
+            // error of 2.3e-3, relative and in norm, against 1.7e-3 by its own rounding alone.
             rp[(x >> 1) & 3] = add_f32x2(rp[(x >> 1) & 3], f32x2(p0, p1));
             pk[(c2 * 32 + x) >> 1] = pack_bf16(p0, p1);
           }

@@ -6,13 +6,14 @@
 // heads), fills its table of cosines and sines, and streams the token's heads, 32 / (D
 // / 8) of them a step, four steps' loads in flight.  HBM bounds them where there are
 // many tokens: 8192 tokens of 32 + 16 heads of 128 take 37 us forward (5.5 TB/s, 0.81 of
-// the copy rate; 41 with norms), 2 x 4096 tokens of 64 + 16 heads 110 us backward with
-// norms and fp32 gradients (5.8 TB/s, 0.86).  What moved them there was fewer
-// instructions, not more bytes in flight: 185 a step became about 80 when both elements
-// of a pair came to one lane and arithmetic went in pairs of floats (166 to 113 us
-// backward), while a ring of bulk copies ahead of the warps took 166 to 276 us, and
-// tiles of eight tokens with the warps dividing the heads 147.  Few tokens are bound
-// by the launch and a chain of dependent loads (8 us for 64 sequences of 8 tokens).
+// the copy rate; 38.5 with norms), 2 x 4096 tokens of 64 + 16 heads 110 us backward with
+// norms and fp32 gradients (5.95 TB/s, 0.88), 93 with bf16 gradients (5.2 TB/s, 0.77).
+// What moved them there was fewer instructions, not more bytes in flight: 185 a step
+// became about 80 when both elements of a pair came to one lane and arithmetic went in
+// pairs of floats (166 to 113 us backward), while a ring of bulk copies ahead of the
+// warps took 166 to 276 us, and tiles of eight tokens with the warps dividing the heads
+// 147.  Few tokens are bound by the launch and a chain of dependent loads (8 us for 64
+// sequences of 8 tokens).
 #include <algorithm>
 #include <type_traits>
 

@@ -3,7 +3,8 @@
 Every computation runs in the CUDA library; torch supplies device memory,
 streams and output allocation.  Functions take torch CUDA tensors and enqueue
 on the current torch stream (or ``stream=``, which the caller orders after what
-its inputs come from, and before what reads its results).
+its inputs come from, and before what reads its results).  None of them records
+an autograd graph, whatever its arguments require; ``ttt.ttt_attention`` does.
 """
 
 from __future__ import annotations
@@ -720,7 +721,7 @@ def stt_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     up to its own, or with tree_mask (int32 [N, words]) every key before the new ones
     and new token j iff bit j % 32 of word j / 32 of its row is set.
     Returns (out bf16 [N, H, D], lse fp32 [N, H]); rows behind the last sequence are
-    left as they are."""
+    left as they are.  out may not overlap q."""
     if stream is not None:
         return _on(stream, stt_paged_attn, q, k_cache, v_cache, cu_q, seq_lens, page_table,
                    scale, tree_mask, out, lse, workspace, held=(workspace,))
@@ -787,7 +788,8 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
     temperature, repetition, frequency, presence: fp32 [B].  tokens int32 [total],
     sequence b's being cu_tokens[b]..cu_tokens[b+1]-1 (int32 [B + 1]) with a prompt of
     n_prompt[b] (int32 [B]); position i's history also holds the first i of
-    draft_tokens int32 [B, >= rows - 1].  bias fp32 [V], [1, V] or [B, V]; mask int32
+    draft_tokens int32 [B, >= rows - 1] (a chain: in a tree of drafts a position would
+    need its ancestors, and each path goes as a sequence of its own).  bias fp32 [V], [1, V] or [B, V]; mask int32
     [N, ceil(V / 32)], bit v % 32 of word v / 32 set where v is allowed.  out may be z
     itself where that is fp32."""
     if stream is not None:
