@@ -573,6 +573,96 @@ STT_API int stt_logits_process(const void* z, int64_t N, int64_t V, int rows,
                                void* stream);
 
 /* --------------------------------------------------------------------------
+ * The K largest logits of every row, the largest first and the lower index first
+ * among equals, with the row's log-sum-exp: a teacher's targets as they are stored
+ * for training (soft_ce_topk_fwd_bwd reads them), or the candidates that a draft
+ * tree grows by (values[k] / temperature - lse is a candidate's log-probability).
+ *
+ *  z        fp32 [N, V], or bf16 with STT_LOGITS_BF16; rows ld_z elements apart,
+ *           any alignment of the element.  -inf is never taken (a forbidden
+ *           token); NaN counts as the largest, and makes the row's lse NaN, as
+ *           +inf does.
+ *  N        rows, >= 0.   V  1..STT_ROW_MAX_V.   K  1..min(V, STT_TOP_MAX_K)
+ *           (K > V is STT_ERR_INVALID_ARG).
+ *  temperature  finite and > 0; of lse alone.
+ *  values   fp32 [N, K]: logits as they are, -inf past the row's last.
+ *  indices  int32 [N, K], -1 past the row's last.
+ *  lse      fp32 [N] or NULL: log sum_v exp(z_v / temperature); -inf for a row
+ *           without logits.
+ * ------------------------------------------------------------------------ */
+#define STT_ROW_MAX_V (16 * 45056)
+#define STT_TOP_MAX_K 1024
+STT_API int stt_top_logits(const void* z, int64_t ld_z, int64_t N, int64_t V, int K,
+                           float temperature, uint32_t flags, float* values, int32_t* indices,
+                           float* lse, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Soft-CE against a teacher's top logits, loss and gradient: the target
+ * distribution is K logits a row (SpecForge review, §三 "内存高效梯度计算", with the
+ * targets kept as their top entries in place of [N, V]).  With tau = temperature:
+ *     p_k = exp(t_values[k] / tau - L),  s = sum_k p_k,  pi = softmax(z / tau)
+ *     l_r = s log sum_v exp(z_v / tau) - sum_k p_k z[t_indices[k]] / tau
+ *     L = sum_r g_r l_r,   dz_v = g_r / tau (s pi_v - sum_{k: t_indices[k] = v} p_k)
+ *
+ *  z        fp32 [N, V], or bf16 with STT_CE_BF16; rows ld_z elements apart.
+ *  t_values fp32 [N, K];  t_indices int32 [N, K].  An entry whose index lies
+ *           outside [0, V) is none (so is one of -inf); entries of one token add up.
+ *  t_lse    fp32 [N]: the teacher's log sum_v exp(t_v / tau) over its whole row, as
+ *           stt_top_logits gives it: p are then the teacher's probabilities and s
+ *           their sum.  NULL: over the row's entries alone, s = 1.
+ *  g        fp32 [N], as soft_ce_fwd_bwd_inplace: rows with g_r = 0 are not read,
+ *           their gradient and row_loss are 0.
+ *  N        rows, >= 0.   V  1..STT_ROW_MAX_V.   K  1..STT_TOP_MAX_K.
+ *  temperature  finite and > 0.
+ *  dz       the gradient, of z's type, rows ld_dz apart, OVERWRITTEN, rounded once.
+ *           It may be z (with ld_dz = ld_z); otherwise it may not overlap z.
+ *  row_loss fp32 [N] or NULL;  loss  fp32 scalar (device), summed in a fixed order.
+ *  workspace at least soft_ce_workspace_size(N, V) bytes, as soft_ce_fwd_bwd_inplace.
+ * A logit of -inf has probability 0; its loss is +inf where the teacher's is not 0.
+ * A row of -inf alone is left out (gradient and row_loss 0); NaN or +inf in a row
+ * makes its gradient and loss NaN.
+ * ------------------------------------------------------------------------ */
+STT_API int soft_ce_topk_fwd_bwd(const void* z, int64_t ld_z, const float* t_values,
+                                 const int32_t* t_indices, const float* t_lse, const float* g,
+                                 int64_t N, int64_t V, int K, float temperature, uint32_t flags,
+                                 void* dz, int64_t ld_dz, float* row_loss, float* loss,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Logits to the distribution that temperature, top-k, top-p and min-p leave, and a
+ * token drawn from it with a given random number: the draft's tokens with the
+ * p_draft that stt_verify tests them against, the target's p_target (stt_logits_process
+ * with STT_LOGITS_RAW before it where there are penalties, and no temperature here),
+ * or plain decoding.  Rows come `rows` to a sequence, as there.
+ *
+ * The order of a row's tokens is by logit, the largest first, the lower index first
+ * among equals.  Kept are, of that order, the first top_k; of those the shortest
+ * beginning that holds top_p of their probability, at least one token; of those the
+ * ones at least min_p times as probable as the first.
+ *     probs_v = e^(z_v / temperature) / (its sum over the kept),  0 for the others
+ *     token   = the smallest v with probs_0 + .. + probs_v > u
+ * A token less than 2^-63 times as probable as the first may count as 0.
+ *
+ *  z        fp32 [N, V], or bf16 with STT_LOGITS_BF16; rows ld_z elements apart.
+ *           -inf is a forbidden token.
+ *  N        rows, >= 0, a multiple of `rows` >= 1.   V  1..STT_ROW_MAX_V.
+ *  temperature, top_p, min_p  fp32 [N / rows], top_k  int32 [N / rows]; each may be
+ *           NULL (1, 1, 0, off).  temperature = 0, like top_k = 1, keeps the first
+ *           token alone; top_k <= 0 or >= V, top_p >= 1 and min_p <= 0 cut nothing.
+ *           That none is NaN and temperature >= 0 is the caller's to see to.
+ *  u        fp32 [N] in [0, 1), or NULL: nothing is drawn (tokens and logprobs NULL).
+ *  tokens   int32 [N].   logprobs  fp32 [N] or NULL: log probs[token].
+ *  probs    fp32, rows ld_probs elements apart, or NULL (with u); may be z where that
+ *           is fp32 (with ld_probs = ld_z), otherwise it may not overlap z.
+ * A row with nothing allowed gives token -1, logprob -inf and probabilities 0; one with
+ * NaN or +inf gives -1, NaN and NaN.
+ * ------------------------------------------------------------------------ */
+STT_API int stt_sample(const void* z, int64_t ld_z, int64_t N, int64_t V, int rows,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const float* u, uint32_t flags, int32_t* tokens,
+                       float* logprobs, float* probs, int64_t ld_probs, void* stream);
+
+/* --------------------------------------------------------------------------
  * Per-launch timing (measurement support; no counterpart on the pages).
  * stt_profile_start(capacity) makes every subsequent kernel launch of the
  * library (from any thread) record a CUDA event pair around itself on its
@@ -604,6 +694,9 @@ STT_API const char* stt_kernel_name(int kernel_id);
 #define STT_KERNEL_KV_APPEND 12
 #define STT_KERNEL_PAGED_ATTN 13
 #define STT_KERNEL_LOGITS 14
+#define STT_KERNEL_TOP_LOGITS 15
+#define STT_KERNEL_SOFT_CE_TOPK 16 /* with its loss sum, as STT_KERNEL_SOFT_CE */
+#define STT_KERNEL_SAMPLE 17
 
 /* Device error-word bits: sites of bounded waits that gave up, and blocks
  * whose dynamic shared memory did not have the 1024-byte alignment the
@@ -616,9 +709,10 @@ STT_API const char* stt_kernel_name(int kernel_id);
 #define STT_DEVERR_PAGE 0x20u /* a page or key slot out of range, skipped */
 #define STT_DEVERR_PAGED_WAIT 0x40u
 #define STT_DEVERR_LOGITS_WAIT 0x80u
+#define STT_DEVERR_SAMPLE_WAIT 0x100u
 #define STT_DEVERR_WAIT_MASK                                                           \
   (STT_DEVERR_FWD_WAIT | STT_DEVERR_BWD_WAIT | STT_DEVERR_CE_WAIT | STT_DEVERR_LM_WAIT | \
-   STT_DEVERR_PAGED_WAIT | STT_DEVERR_LOGITS_WAIT)
+   STT_DEVERR_PAGED_WAIT | STT_DEVERR_LOGITS_WAIT | STT_DEVERR_SAMPLE_WAIT)
 
 #ifdef __cplusplus
 }

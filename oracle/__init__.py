@@ -30,6 +30,8 @@ rope       per-head RMS norm and position rotation of queries and keys, and
 paged      attention of new tokens over a paged KV cache.
 logits     penalties, bias, grammar mask, temperature and softmax of the
            target's logits.
+top        the K largest logits of a row, the soft-CE against them, truncated
+           sampling.
 
 Readings of the page where it is silent:
   * kv indexes the concatenation of k+1 blocks, each Q_LEN long; block 0 is
@@ -46,6 +48,7 @@ Readings of the page where it is silent:
 """
 
 from . import mask, attention, soft_ce, lm_head, verify  # noqa: F401
-from . import rope, paged, logits  # noqa: F401
+from . import rope, paged, logits, top  # noqa: F401
 
-__all__ = ["mask", "attention", "soft_ce", "lm_head", "verify", "rope", "paged", "logits"]
+__all__ = ["mask", "attention", "soft_ce", "lm_head", "verify", "rope", "paged", "logits",
+           "top"]

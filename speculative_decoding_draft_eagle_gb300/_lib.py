@@ -50,6 +50,9 @@ EXPORTS = (
     "stt_paged_attn_workspace_size",
     "stt_paged_attn",
     "stt_logits_process",
+    "stt_top_logits",
+    "soft_ce_topk_fwd_bwd",
+    "stt_sample",
     "stt_profile_start",
     "stt_profile_stop",
     "stt_kernel_name",
@@ -148,6 +151,14 @@ def _declare(L):
     L.stt_paged_attn.restype = i32
     L.stt_logits_process.argtypes = [vp, i64, i64, i32, logits, c.c_uint32, vp, vp]
     L.stt_logits_process.restype = i32
+    L.stt_top_logits.argtypes = [vp, i64, i64, i64, i32, f32, c.c_uint32, vp, vp, vp, vp]
+    L.stt_top_logits.restype = i32
+    L.soft_ce_topk_fwd_bwd.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, i32, f32, c.c_uint32, vp,
+                                       i64, vp, vp, vp, sz, vp]
+    L.soft_ce_topk_fwd_bwd.restype = i32
+    L.stt_sample.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, c.c_uint32, vp, vp, vp,
+                             i64, vp]
+    L.stt_sample.restype = i32
     L.stt_profile_start.argtypes = [i32]
     L.stt_profile_start.restype = i32
     L.stt_profile_stop.argtypes = [c.POINTER(i32), c.POINTER(i32), c.POINTER(f32), i32]

@@ -158,10 +158,60 @@ struct LogitsArgs {
 constexpr int64_t kLogitsMaxV = 16 * 24576;
 cudaError_t logits_launch(const LogitsArgs& a, cudaStream_t s);
 
+// --------------------------- top logits, soft-CE against them, sampling --
+constexpr int kRowMaxCtas = 16;                     // CTAs of a cluster that share a row
+constexpr int64_t kRowMaxV = kRowMaxCtas * 45056;  // 16 slices that fit into shared memory
+constexpr int kTopMaxK = 1024;
+struct TopLogitsArgs {
+  const void* z;
+  int64_t ld_z, N;
+  int V, K;
+  bool bf16;
+  float temperature;
+  float* values;
+  int32_t* indices;
+  float* lse;
+};
+cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s);
+
+constexpr int kSoftCeTopkMaxK = 1024;
+struct SoftCeTopkArgs {
+  const void* z;
+  int64_t ld_z;
+  void* dz;
+  int64_t ld_dz, N;
+  int V, K;
+  bool bf16;
+  float temperature;
+  const float* values;
+  const int32_t* indices;
+  const float* lse;
+  const float* g;
+  float *row_loss, *loss, *wl;
+};
+cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s);
+
+struct SampleArgs {
+  const void* z;
+  int64_t ld_z, N;
+  int V, rows;
+  bool bf16;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *u;
+  int32_t* tokens;
+  float* logprobs;
+  float* probs;
+  int64_t ld_p;
+};
+cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s);
+
 // Per-file device error words (read and cleared).
 cudaError_t qkv_rope_error_word(uint32_t* w);
 cudaError_t paged_attn_error_word(uint32_t* w);
 cudaError_t logits_error_word(uint32_t* w);
+cudaError_t soft_ce_topk_error_word(uint32_t* w);
+cudaError_t sample_error_word(uint32_t* w);
 cudaError_t soft_ce_error_word(uint32_t* w);
 cudaError_t attn_fwd_error_word(uint32_t* w);
 cudaError_t attn_bwd_error_word(uint32_t* w);
@@ -171,6 +221,8 @@ cudaError_t attn_fwd_set_wait_budget(uint64_t ns);
 cudaError_t attn_bwd_set_wait_budget(uint64_t ns);
 cudaError_t paged_attn_set_wait_budget(uint64_t ns);
 cudaError_t logits_set_wait_budget(uint64_t ns);
+cudaError_t soft_ce_topk_set_wait_budget(uint64_t ns);
+cudaError_t sample_set_wait_budget(uint64_t ns);
 
 // Streaming multiprocessors of the current device (cached per device; 1 if
 // the query fails, which only shrinks persistent grids).

@@ -107,6 +107,9 @@ const char* stt_kernel_name(int kernel_id) {
     case STT_KERNEL_KV_APPEND: return "kv_append";
     case STT_KERNEL_PAGED_ATTN: return "paged_attn";
     case STT_KERNEL_LOGITS: return "logits";
+    case STT_KERNEL_TOP_LOGITS: return "top_logits";
+    case STT_KERNEL_SOFT_CE_TOPK: return "soft_ce_topk";
+    case STT_KERNEL_SAMPLE: return "sample";
     default: return "unknown";
   }
 }

@@ -1,0 +1,209 @@
+// row_slice.cuh -- a row of logits cut into whole 16-byte pieces of memory, and
+// the order of its elements: shared by the kernels that take, learn from and draw
+// from the top of a distribution.
+//
+// A row of V elements starts anywhere (odd vocabularies, rows of a wider buffer).
+// It is taken in the 16-byte pieces of memory that it touches; of the first and the
+// last piece some elements may lie outside the row, and those are never read: such a
+// piece goes element by element, with -inf for what is not the row's.
+#pragma once
+
+#include <climits>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace stt {
+
+// Pieces of 16 bytes of the longest of C slices of V elements of `size` bytes, wherever
+// the row starts.
+inline int64_t slice_pieces(int64_t V, int size, int C) {
+  const int64_t G = 16 / size;
+  return ((V + 2 * G - 2) / G + C - 1) / C;
+}
+
+__device__ __forceinline__ void unpack_piece(const uint4& r, float (&x)[4]) {
+  x[0] = __uint_as_float(r.x);
+  x[1] = __uint_as_float(r.y);
+  x[2] = __uint_as_float(r.z);
+  x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack_piece(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// The part of a row that CTA `rank` takes, `per` pieces to a CTA.
+template <class T>
+struct RowSlice {
+  static constexpr int G = 16 / (int)sizeof(T);  // elements of a piece
+  const T* row;
+  int V;
+  int first;   // index in the row of the slice's first element; negative before the row
+  int pieces;
+
+  __device__ __forceinline__ RowSlice(const T* row_, int V_, int rank, int per) : row(row_), V(V_) {
+    const int shift = (int)((reinterpret_cast<uintptr_t>(row_) / sizeof(T)) % G);
+    const int all = (V_ + shift + G - 1) / G;
+    const int p0 = min(rank * per, all);
+    pieces = min(per, all - p0);
+    first = p0 * G - shift;
+  }
+  __device__ __forceinline__ int index(int piece) const { return first + piece * G; }
+  __device__ __forceinline__ bool whole(int piece) const {
+    const int v = index(piece);
+    return v >= 0 && v + G <= V;
+  }
+  // A piece's elements, -inf outside the row.
+  __device__ __forceinline__ void edge(int piece, float (&x)[G]) const {
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+      const int v = index(piece) + e;
+      x[e] = v >= 0 && v < V ? (float)row[v] : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ uint4 load(int piece) const {
+    return *reinterpret_cast<const uint4*>(row + index(piece));
+  }
+};
+
+// Brings a slice into shared memory at `dst`: whole pieces by bulk copies, `chunk`
+// pieces on each of `bars` (initialised here), the others by the threads, before the
+// __syncthreads() in here.  Called by all threads, at least 64 of them.
+template <class T>
+__device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64_t* bars, int chunk) {
+  constexpr int G = RowSlice<T>::G;
+  const int tid = threadIdx.x;
+  const int n_chunks = (s.pieces + chunk - 1) / chunk;
+  if (tid == 0) {
+    for (int c = 0; c < n_chunks; ++c) mbar_init(&bars[c], 1);
+    fence_mbar_init();
+    const int a = s.pieces > 0 && !s.whole(0) ? 1 : 0;
+    const int b = s.pieces > 0 && !s.whole(s.pieces - 1) ? s.pieces - 1 : s.pieces;
+    for (int c = 0; c < n_chunks; ++c) {
+      const int lo = max(a, c * chunk), hi = min(b, (c + 1) * chunk);
+      const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
+      mbar_arrive_expect_tx(&bars[c], bytes);
+      if (bytes) bulk_load(dst + lo * G, s.row + s.index(lo), bytes, &bars[c]);
+    }
+  }
+  if (tid >= 32 && tid < 32 + 2 * G) {
+    const int e = (tid - 32) % G, piece = tid - 32 < G ? 0 : s.pieces - 1;
+    if (piece < s.pieces && piece >= 0 && !s.whole(piece)) {
+      const int v = s.index(piece) + e;
+      dst[piece * G + e] = v >= 0 && v < s.V ? s.row[v] : (T)(-INFINITY);
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ order --
+// Larger logits first, the lower index first among equals: one whole number for a
+// logit and its index, larger for what comes earlier.  -0 counts as 0; NaN comes
+// before everything.
+__device__ __forceinline__ uint32_t order_of(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  if (z != z) return 0xffffffffu;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t place_key(float z, int v) {
+  return (uint64_t)order_of(z) << 32 | (0xffffffffu - (uint32_t)v);
+}
+__device__ __forceinline__ int key_index(uint64_t key) {
+  return (int)(0xffffffffu - (uint32_t)key);
+}
+
+// Sorts n keys (a power of two) in shared memory, the largest first: a bitonic network
+// over the block's threads.  Ends with a __syncthreads().
+template <int kThreads>
+__device__ __forceinline__ void sort_keys(uint64_t* a, int n) {
+  for (int size = 2; size <= n; size *= 2) {
+    for (int step = size / 2; step > 0; step /= 2) {
+      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
+        const int i = 2 * t - (t & (step - 1)), j = i + step;
+        const uint64_t x = a[i], y = a[j];
+        const bool down = (i & size) == 0;
+        if ((x < y) == down) {
+          a[i] = y;
+          a[j] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+__device__ __forceinline__ int next_power(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// ------------------------------------------------- neighbours in a cluster --
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+template <class U>
+__device__ __forceinline__ U ld_cluster(const U* p, int rank) {
+  const uint32_t a = mapa_shared(smem_u32(p), (uint32_t)rank);
+  U v;
+  if constexpr (sizeof(U) == 8) {
+    uint64_t w;
+    asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(w) : "r"(a) : "memory");
+    v = *reinterpret_cast<U*>(&w);
+  } else {
+    static_assert(sizeof(U) == 4, "words of 4 or 8 bytes");
+    uint32_t w;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(w) : "r"(a) : "memory");
+    v = *reinterpret_cast<U*>(&w);
+  }
+  return v;
+}
+__device__ __forceinline__ void st_cluster(const uint64_t* p, int rank, uint64_t v) {
+  const uint32_t a = mapa_shared(smem_u32(p), (uint32_t)rank);
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// max(a, b, c) that passes NaN on.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Launches `kern` with C CTAs of a row to a cluster, raising its limits first.
+template <class P>
+inline cudaError_t launch_rows(void (*kern)(const P), const P& p, int64_t rows, int C, int threads,
+                               int smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && C > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  if (rows * C > 0x7fffffffll) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * C), 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace stt

@@ -75,6 +75,9 @@ int from_cuda(cudaError_t e) {
 // context) cannot be cleared and still fails the launches.
 inline void begin_call() { (void)cudaGetLastError(); }
 
+static_assert(STT_ROW_MAX_V == stt::kRowMaxV && STT_TOP_MAX_K == stt::kTopMaxK &&
+                  STT_TOP_MAX_K == stt::kSoftCeTopkMaxK,
+              "limits of the operators on the top of a distribution");
 static_assert(STT_ERR_UNSUPPORTED == -2 && STT_ERR_CUDA == -4, "status_from_cuda codes");
 static_assert(STT_CE_BF16 == stt::kCeBf16 && STT_CE_G_PER_ELEMENT == stt::kCeGPerElement,
               "soft-CE flags");
@@ -119,6 +122,17 @@ int check_attn(const void* q, const void* const* k_blocks, const void* const* v_
 
 inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Validation of N rows of V logits (or of their gradient or probabilities), `ld` elements
+// apart, with STT_LOGITS_BF16 in `flags`.
+int check_logits(const void* z, int64_t ld, int64_t N, int64_t V, uint32_t flags) {
+  if (V > stt::kRowMaxV || N > 0x7fffffffll / stt::kRowMaxCtas) return STT_ERR_UNSUPPORTED;
+  if (N == 0) return STT_OK;
+  if (!z || ld < V) return STT_ERR_INVALID_ARG;
+  if (ld > (1ll << 31)) return STT_ERR_UNSUPPORTED;
+  if (!aligned(z, (flags & STT_LOGITS_BF16) ? 2 : 4)) return STT_ERR_MISALIGNED;
+  return STT_OK;
 }
 
 // Validation of the rotation's arguments; fills `r` on success.
@@ -231,6 +245,10 @@ int stt_device_error(void* stream, uint32_t* word) {
   w |= part;
   if (stt::logits_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
   w |= part;
+  if (stt::soft_ce_topk_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
+  w |= part;
+  if (stt::sample_error_word(&part) != cudaSuccess) return STT_ERR_CUDA;
+  w |= part;
   *word = w;
   return (w & STT_DEVERR_WAIT_MASK) ? STT_ERR_TIMEOUT : STT_OK;
 }
@@ -249,6 +267,8 @@ int stt_debug_set_wait_budget(uint64_t ns) {
   if (e == cudaSuccess) e = stt::lm_head_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::paged_attn_set_wait_budget(ns);
   if (e == cudaSuccess) e = stt::logits_set_wait_budget(ns);
+  if (e == cudaSuccess) e = stt::soft_ce_topk_set_wait_budget(ns);
+  if (e == cudaSuccess) e = stt::sample_set_wait_budget(ns);
   return from_cuda(e);
 }
 
@@ -630,6 +650,118 @@ int stt_logits_process(const void* z, int64_t N, int64_t V, int rows, const stt_
     a.n_tokens = p.n_tokens;
     a.out = out;
     return from_cuda(stt::logits_launch(a, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int stt_top_logits(const void* z, int64_t ld_z, int64_t N, int64_t V, int K, float temperature,
+                   uint32_t flags, float* values, int32_t* indices, float* lse, void* stream) {
+  try {
+    begin_call();
+    if (flags & ~(uint32_t)STT_LOGITS_BF16) return STT_ERR_INVALID_ARG;
+    if (N < 0 || V < 1 || K < 1 || K > V) return STT_ERR_INVALID_ARG;
+    if (!std::isfinite(temperature) || !(temperature > 0.f)) return STT_ERR_INVALID_ARG;
+    if (K > stt::kTopMaxK) return STT_ERR_UNSUPPORTED;
+    const int st = check_logits(z, ld_z, N, V, flags);
+    if (st != STT_OK || N == 0) return st;
+    if (!values || !indices) return STT_ERR_INVALID_ARG;
+    if (!aligned(values, 4) || !aligned(indices, 4) || !aligned(lse, 4)) return STT_ERR_MISALIGNED;
+    stt::TopLogitsArgs a{};
+    a.z = z;
+    a.ld_z = ld_z;
+    a.N = N;
+    a.V = (int)V;
+    a.K = K;
+    a.bf16 = (flags & STT_LOGITS_BF16) != 0;
+    a.temperature = temperature;
+    a.values = values;
+    a.indices = indices;
+    a.lse = lse;
+    return from_cuda(stt::top_logits_launch(a, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int soft_ce_topk_fwd_bwd(const void* z, int64_t ld_z, const float* t_values,
+                         const int32_t* t_indices, const float* t_lse, const float* g, int64_t N,
+                         int64_t V, int K, float temperature, uint32_t flags, void* dz,
+                         int64_t ld_dz, float* row_loss, float* loss, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  try {
+    begin_call();
+    if (flags & ~(uint32_t)STT_CE_BF16) return STT_ERR_INVALID_ARG;
+    if (N < 0 || V < 1 || K < 1) return STT_ERR_INVALID_ARG;
+    if (!std::isfinite(temperature) || !(temperature > 0.f)) return STT_ERR_INVALID_ARG;
+    if (K > stt::kSoftCeTopkMaxK) return STT_ERR_UNSUPPORTED;
+    static_assert(STT_CE_BF16 == STT_LOGITS_BF16, "one check of the logits");
+    int st = check_logits(z, ld_z, N, V, flags);
+    if (st == STT_OK) st = check_logits(dz, ld_dz, N, V, flags);
+    if (st != STT_OK) return st;
+    if (z == dz && ld_z != ld_dz && N > 1) return STT_ERR_INVALID_ARG;
+    if (!loss || (N > 0 && (!t_values || !t_indices || !g))) return STT_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < soft_ce_workspace_size(N, V)) return STT_ERR_WORKSPACE;
+    if (!aligned(t_values, 4) || !aligned(t_indices, 4) || !aligned(t_lse, 4) || !aligned(g, 4) ||
+        !aligned(row_loss, 4) || !aligned(loss, 4) || !aligned(workspace, 4))
+      return STT_ERR_MISALIGNED;
+    stt::SoftCeTopkArgs a{};
+    a.z = z;
+    a.ld_z = ld_z;
+    a.dz = dz;
+    a.ld_dz = ld_dz;
+    a.N = N;
+    a.V = (int)V;
+    a.K = K;
+    a.bf16 = (flags & STT_CE_BF16) != 0;
+    a.temperature = temperature;
+    a.values = t_values;
+    a.indices = t_indices;
+    a.lse = t_lse;
+    a.g = g;
+    a.row_loss = row_loss;
+    a.loss = loss;
+    a.wl = static_cast<float*>(workspace);
+    return from_cuda(stt::soft_ce_topk_launch(a, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return STT_ERR_CUDA;
+  }
+}
+
+int stt_sample(const void* z, int64_t ld_z, int64_t N, int64_t V, int rows,
+               const float* temperature, const int32_t* top_k, const float* top_p,
+               const float* min_p, const float* u, uint32_t flags, int32_t* tokens,
+               float* logprobs, float* probs, int64_t ld_probs, void* stream) {
+  try {
+    begin_call();
+    if (flags & ~(uint32_t)STT_LOGITS_BF16) return STT_ERR_INVALID_ARG;
+    if (N < 0 || V < 1 || rows < 1 || N % rows != 0) return STT_ERR_INVALID_ARG;
+    int st = check_logits(z, ld_z, N, V, flags);
+    if (st == STT_OK && probs) st = check_logits(probs, ld_probs, N, V, 0);
+    if (st != STT_OK || N == 0) return st;
+    if ((!u && (tokens || logprobs)) || (u && !tokens) || (!u && !probs)) return STT_ERR_INVALID_ARG;
+    if (probs == z && ((flags & STT_LOGITS_BF16) || (ld_probs != ld_z && N > 1)))
+      return STT_ERR_INVALID_ARG;
+    if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4))
+      return STT_ERR_MISALIGNED;
+    stt::SampleArgs a{};
+    a.z = z;
+    a.ld_z = ld_z;
+    a.N = N;
+    a.V = (int)V;
+    a.rows = rows;
+    a.bf16 = (flags & STT_LOGITS_BF16) != 0;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    a.probs = probs;
+    a.ld_p = ld_probs;
+    return from_cuda(stt::sample_launch(a, static_cast<cudaStream_t>(stream)));
   } catch (...) {
     return STT_ERR_CUDA;
   }

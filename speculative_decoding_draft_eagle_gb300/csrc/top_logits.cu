@@ -1,0 +1,355 @@
+// top_logits.cu -- the K largest logits of every row, in order, with their indices and
+// the logarithm of the row's sum of exponentials.
+//
+// Bound by HBM: a row is read once.  A CTA (or, with few rows, each CTA of a cluster on
+// its slice) looks at a sample of 4096 elements spread over its slice and takes a lower
+// bound of the K-th largest from it: a sample's r-th largest, with r so far above the
+// K / n share that fewer than K elements of the slice reach it about once in ten
+// thousand rows of independent logits.  Then it reads the slice, sums the exponentials
+// and keeps what reaches the bound, a few times K elements, as 64-bit keys of logit and
+// index, sorts those and has the first K.  Where the bound was too high, or too many
+// reach it (equal logits, orders that the sample does not show), the K-th largest key
+// is found digit by digit over the slice instead, whatever it holds.
+//
+// The K largest of each slice go to the row's first CTA, which sorts them once more.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/stt.h"
+#include "row_slice.cuh"
+
+namespace stt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSample = 16 * kThreads;  // elements looked at first
+constexpr int kMerge = 2048;            // keys that the first CTA of a row sorts, at most
+
+struct Params {
+  TopLogitsArgs a;
+  float c;            // log2(e) / tau
+  float inv_tau;
+  int C, per;         // CTAs of a row, pieces of a CTA
+  int cap;            // keys kept
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_min(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(16) uint64_t keys[];  // [cap], then [C K] of the row's slices
+  __shared__ int s_n, s_count[2];
+  __shared__ float red[2 * kWarps];
+  __shared__ uint32_t hist[256];
+  __shared__ uint64_t s_cut;
+  __shared__ int s_digit, s_need, s_done;
+  __shared__ float s_m, s_l;
+  constexpr int G = RowSlice<T>::G;
+  constexpr int PS = kSample / kThreads / G;  // pieces of the sample, to a thread
+  const TopLogitsArgs& A = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % (unsigned)P.C);
+  const int64_t row = blockIdx.x / (unsigned)P.C;
+  const RowSlice<T> S(static_cast<const T*>(A.z) + row * A.ld_z, A.V, rank, P.per);
+  const int K = A.K, cap = P.cap;
+  if (tid == 0) s_n = 0;
+  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to the first CTA
+
+  // ---- a bound from the sample; -inf where the slice is kept whole
+  float bound = -INFINITY, start = -INFINITY;  // `start`: a first maximum for the sums
+  if (S.pieces * G > cap) {
+    float x[PS * G];
+    // The sample's place whose logit is the bound.
+    const float q = (float)K * ((float)kSample / (float)(S.pieces * G));
+    const int want = (int)ceilf(q + 3.5f * sqrtf(q) + 3.f);
+    // Each warp takes PS runs of 32 pieces, spread evenly over the slice (there are
+    // more than 32, and in short slices the runs overlap).
+#pragma unroll
+    for (int j = 0; j < PS; ++j) {
+      const int run = warp * PS + j;
+      const int q = (int)((int64_t)(S.pieces - 32) * run / (kWarps * PS - 1)) + lane;
+      float y[G];
+      if (S.whole(q)) unpack_piece(S.load(q), y);
+      else S.edge(q, y);
+#pragma unroll
+      for (int e = 0; e < G; ++e) x[j * G + e] = y[e];
+    }
+    float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+    for (int i = 0; i < PS * G; ++i) {
+      hi = fmaxf(hi, x[i]);
+      if (x[i] > -INFINITY) lo = fminf(lo, x[i]);
+    }
+    hi = warp_max(hi);
+    lo = warp_min(lo);
+    if (lane == 0) {
+      red[warp] = hi;
+      red[kWarps + warp] = lo;
+    }
+    if (tid < 2) s_count[tid] = 0;
+    __syncthreads();
+    hi = red[0];
+    lo = red[kWarps];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      hi = fmaxf(hi, red[w]);
+      lo = fminf(lo, red[kWarps + w]);
+    }
+    start = hi;
+    // Halving until a quarter more than wanted reach it at most.  `lo` is reached by
+    // enough, or is the smallest of all.
+    if (hi > lo) {
+      for (int it = 0; it < 18; ++it) {
+        // Halfway between them, or between their places among the floats where they are
+        // far apart (a mask of the type's lowest value).
+        const uint32_t below = order_of(lo);
+        const float mid = hi - lo < 1024.f ? lo + 0.5f * (hi - lo)
+                                           : logit_of(below + (order_of(hi) - below) / 2);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < PS * G; ++i) n += x[i] >= mid ? 1 : 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) atomicAdd(&s_count[it & 1], n);
+        __syncthreads();
+        n = s_count[it & 1];
+        if (tid == 0) s_count[(it & 1) ^ 1] = 0;
+        __syncthreads();
+        if (n >= want) lo = mid;
+        else hi = mid;
+        if (n >= want && n <= want + want / 4) break;
+      }
+    }
+    bound = lo;
+    if (!(bound < INFINITY)) bound = -INFINITY;  // nothing in the sample
+  }
+  __syncthreads();
+
+  auto keep = [&](float z, int v) {
+    const int at = atomicAdd(&s_n, 1);
+    if (at < cap) keys[at] = place_key(z, v);
+  };
+
+  // ---- the slice, once: its sum of exponentials, and what reaches the bound
+  float m = start, l = 0.f;
+  constexpr int U = 4;
+  const bool all = bound == -INFINITY;
+  for (int q0 = tid; q0 < S.pieces; q0 += U * kThreads) {
+    uint4 raw[U];
+    float x[U][G];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = q0 + u * kThreads;
+      if (q < S.pieces && S.whole(q)) raw[u] = S.load(q);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = q0 + u * kThreads;
+      if (q < S.pieces) {
+        if (S.whole(q)) unpack_piece(raw[u], x[u]);
+        else S.edge(q, x[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < G; ++e) x[u][e] = -INFINITY;
+      }
+      float top = x[u][0];
+#pragma unroll
+      for (int e = 1; e < G; ++e) top = max_nan(top, x[u][e]);
+      // (NaN, too, is not below the bound.)
+      if (!(top < bound) && !(top == -INFINITY)) {
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+          if (!(x[u][e] < bound) && !(x[u][e] == -INFINITY)) keep(x[u][e], S.index(q) + e);
+      }
+      if (!(top <= m)) {
+        const float to = fmaxf(m, top);  // passes NaN over; the sum shows it
+        l = m == -INFINITY ? l : l * ex2((m - to) * P.c);
+        m = to;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < G; ++e) l += ex2((x[u][e] - base) * P.c);
+    }
+  }
+  {
+    const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
+    l = warp_sum(l == 0.f ? 0.f : l * ex2((m - base) * P.c));
+    if (lane == 0) {
+      red[warp] = top;
+      red[kWarps + warp] = l;
+    }
+  }
+  __syncthreads();
+  int n = s_n;
+
+  // ---- the K-th largest key digit by digit, where the bound did not do
+  if (n > cap || (!all && n < K)) {
+    auto each = [&](auto&& f) {
+      for (int q = tid; q < (S.pieces + 31) / 32 * 32; q += kThreads) {
+        float x[G];
+        const bool in = q < S.pieces;
+        if (in && S.whole(q)) unpack_piece(S.load(q), x);
+        else if (in) S.edge(q, x);
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const bool take = in && !(x[e] == -INFINITY);
+          f(take, take ? place_key(x[e], S.index(q) + e) : 0ull);
+        }
+      }
+    };
+    uint64_t prefix = 0;
+    int need = K;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+      hist[tid] = 0;
+      static_assert(kThreads == 256, "a thread for each digit");
+      __syncthreads();
+      each([&](bool take, uint64_t key) {
+        const bool in = take && (shift == 56 || key >> ((shift + 8) & 63) == prefix);
+        const uint32_t d = (uint32_t)(key >> shift) & 255u;
+        // A warp of equal digits, as equal logits give, counts at once.
+        int same;
+        __match_all_sync(0xffffffffu, in ? d : 256u, &same);
+        if (same) {
+          if (lane == 0 && in) atomicAdd(&hist[d], 32u);
+        } else if (in) {
+          atomicAdd(&hist[d], 1u);
+        }
+      });
+      __syncthreads();
+      if (tid == 0) {
+        int above = 0, total = 0, digit = 255;
+        if (shift == 56) {
+          for (int d = 0; d < 256; ++d) total += (int)hist[d];
+          need = min(need, total);
+        }
+        s_done = need == 0;
+        if (need > 0) {
+          while (digit > 0 && above + (int)hist[digit] < need) above += (int)hist[digit--];
+          need -= above;
+          s_done = need == (int)hist[digit];
+        }
+        s_digit = digit;
+        s_need = need;
+      }
+      __syncthreads();
+      need = s_need;
+      prefix = prefix << 8 | (uint64_t)s_digit;
+      if (s_done || shift == 0) {
+        if (tid == 0) {
+          s_cut = need == 0 ? ~0ull : prefix << shift;
+          s_n = 0;
+        }
+        break;
+      }
+    }
+    __syncthreads();
+    const uint64_t cut = s_cut;
+    each([&](bool take, uint64_t key) {
+      if (take && key >= cut) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at < cap) keys[at] = key;
+      }
+    });
+    __syncthreads();
+    n = min(s_n, cap);
+  }
+
+  // ---- in order
+  int size = next_power(max(n, 1));
+  for (int i = n + tid; i < size; i += kThreads) keys[i] = 0;
+  __syncthreads();
+  sort_keys<kThreads>(keys, size);
+  n = min(n, K);
+
+  m = red[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, red[w]);
+  l = 0.f;
+  {
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * ex2((red[w] - base) * P.c);
+  }
+  const uint64_t* top = keys;
+  if (P.C > 1) {
+    uint64_t* const all_keys = keys + cap;
+    if (tid == 0) {
+      s_m = m;
+      s_l = l;
+    }
+    cluster_wait_acquire();
+    for (int i = tid; i < K; i += kThreads) st_cluster(all_keys + rank * K + i, 0, i < n ? keys[i] : 0ull);
+    cluster_sync();
+    if (rank == 0) {
+      float om = -INFINITY, ol = 0.f;
+      if (lane < P.C) {
+        om = ld_cluster(&s_m, lane);
+        ol = ld_cluster(&s_l, lane);
+      }
+      m = warp_max(om);
+      const float base = m == -INFINITY ? 0.f : m;
+      l = warp_sum(ol == 0.f ? 0.f : ol * ex2((om - base) * P.c));
+    }
+    cluster_arrive_release();
+    if (rank == 0) {
+      size = next_power(P.C * K);
+      for (int i = P.C * K + tid; i < size; i += kThreads) all_keys[i] = 0;
+      __syncthreads();
+      sort_keys<kThreads>(all_keys, size);
+      top = all_keys;
+    }
+    cluster_wait_acquire();
+    if (rank != 0) return;
+  }
+  for (int i = tid; i < K; i += kThreads) {
+    const uint64_t key = P.C > 1 || i < n ? top[i] : 0ull;
+    A.values[row * K + i] = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
+    A.indices[row * K + i] = key ? key_index(key) : -1;
+  }
+  // (A row without logits: log 0.)
+  if (A.lse && tid == 0) A.lse[row] = l == 0.f ? -INFINITY : fmaf(m, P.inv_tau, logf(l));
+}
+
+}  // namespace
+
+cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
+  const int size = a.bf16 ? 2 : 4;
+  Params P{};
+  P.a = a;
+  P.c = (float)(1.4426950408889634 / (double)a.temperature);
+  P.inv_tau = 1.f / a.temperature;
+  // CTAs of a row: one while the rows fill the GPU, more for few rows, or for rows so
+  // long that the sample says little; as many as the first one can merge.
+  const int most = std::max(1, std::min(kRowMaxCtas, kMerge / a.K));
+  int C = 1;
+  while (2 * C <= most && slice_pieces(a.V, 1, C) * 16 > 262144) C *= 2;
+  while (2 * C <= most && a.N * 2 * C <= 2 * sm_count() && slice_pieces(a.V, size, C) >= 4 * kThreads) C *= 2;
+  P.C = C;
+  P.per = (int)slice_pieces(a.V, size, C);
+  P.cap = a.K <= 512 ? 2048 : 4096;
+  const int smem = P.cap * 8 + (C > 1 ? kMerge * 8 : 0);
+  prof_before(s, STT_KERNEL_TOP_LOGITS);
+  const cudaError_t e =
+      a.bf16 ? launch_rows(top_logits_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
+             : launch_rows(top_logits_kernel<float>, P, a.N, C, kThreads, smem, s);
+  prof_after(s);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace stt

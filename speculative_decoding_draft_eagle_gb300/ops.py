@@ -39,6 +39,9 @@ __all__ = [
     "stt_paged_attn",
     "stt_paged_attn_workspace_size",
     "stt_logits_process",
+    "stt_top_logits",
+    "soft_ce_topk_fwd_bwd",
+    "stt_sample",
     "stt_device_error",
     "stt_debug_set_wait_budget",
     "stt_debug_inject",
@@ -850,6 +853,189 @@ def stt_logits_process(z: torch.Tensor, rows: int = 1,
     if st:
         check("stt_logits_process", st)
     return out
+
+
+def _logits(z, name, dev, dtype=None, shape=None):
+    """Address of rows of logits [N, V] (fp32 or bf16, or `dtype`) that are dense but for
+    the distance between them, and that distance."""
+    if not isinstance(z, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if z.dim() != 2 or (shape is not None and z.shape != shape):
+        raise ValueError(f"{name} must be [N, V]" if shape is None else
+                         f"{name} must have shape {tuple(shape)}, got {tuple(z.shape)}")
+    t = z.dtype
+    if t is not dtype if dtype is not None else (t is not torch.float32 and t is not torch.bfloat16):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t}")
+    if z.get_device() != dev:
+        raise ValueError(f"{name} is on {z.device}, the current device is cuda:{dev}")
+    N, V = z.shape
+    if z.is_contiguous():
+        return z.data_ptr(), V
+    ld, one = z.stride()
+    if (V > 1 and one != 1) or (N > 1 and ld < V):
+        raise ValueError(f"{name} must be dense apart from the distance between its rows")
+    return z.data_ptr(), ld if N > 1 else V
+
+
+def _apart(a, ld_a, b, ld_b, name):
+    """Refuses rows b [N, V] that share memory with the rows a, unless they are a."""
+    N, V = a.shape
+    pa, pb, sa, sb = a.data_ptr(), b.data_ptr(), a.element_size(), b.element_size()
+    if N == 0 or (pa == pb and sa == sb and (ld_a == ld_b or N == 1)):
+        return
+    if pa >= pb + ((N - 1) * ld_b + V) * sb or pb >= pa + ((N - 1) * ld_a + V) * sa:
+        return
+    if ld_a * sa == ld_b * sb:  # columns of one wider buffer
+        off = (pb - pa) % (ld_a * sa)
+        if off >= V * sa and off + V * sb <= ld_a * sa:
+            return
+    raise ValueError(f"{name} overlaps the logits")
+
+
+def stt_top_logits(z: torch.Tensor, K: int, temperature: float = 1.0,
+                   values: Optional[torch.Tensor] = None, indices: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, stream=None
+                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The K largest logits of every row of z [N, V] (fp32 or bf16; rows may be a slice of
+    wider ones), the largest first and the lower index first among equals, -inf never.
+
+    Returns (values fp32 [N, K], -inf past the row's last; indices int32 [N, K], -1 there;
+    lse fp32 [N] = log sum_v exp(z_v / temperature)): what soft_ce_topk_fwd_bwd takes of a
+    teacher, or a draft tree's candidates, whose log-probability is
+    values / temperature - lse."""
+    if stream is not None:
+        return _on(stream, stt_top_logits, z, K, temperature, values, indices, lse)
+    dev, raw = _current()
+    p_z, ld = _logits(z, "z", dev)
+    N, V = z.shape
+    if not 1 <= K <= V:
+        raise ValueError(f"K must be 1..{V}, got {K}")
+    f32, i32 = torch.float32, torch.int32
+    if values is None:
+        values = _new((N, K), f32, dev)
+    if indices is None:
+        indices = _new((N, K), i32, dev)
+    if lse is None:
+        lse = _new((N,), f32, dev)
+    st = lib().stt_top_logits(
+        p_z, ld, N, V, K, temperature, STT_LOGITS_BF16 if z.dtype is torch.bfloat16 else 0,
+        _arg(values, "values", f32, (N, K), dev), _arg(indices, "indices", i32, (N, K), dev),
+        _arg(lse, "lse", f32, (N,), dev), raw)
+    if st:
+        check("stt_top_logits", st)
+    return values, indices, lse
+
+
+def soft_ce_topk_fwd_bwd(z: torch.Tensor, t_values: torch.Tensor, t_indices: torch.Tensor,
+                         g: torch.Tensor, t_lse: Optional[torch.Tensor] = None,
+                         temperature: float = 1.0, dz: Optional[torch.Tensor] = None,
+                         row_loss: Optional[torch.Tensor] = None,
+                         loss: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Soft-CE of logits z [N, V] (fp32 or bf16; rows may be a slice of wider ones) against a
+    teacher's top logits t_values fp32 and t_indices int32 [N, K] (an index outside [0, V),
+    such as -1, is no entry), with the gradient.
+
+    Both sides are divided by `temperature`.  With t_lse fp32 [N], the teacher's
+    log-sum-exp at it (stt_top_logits), the targets are the teacher's probabilities;
+    without, they are renormalised over the entries.  g fp32 [N]: upstream gradient of each
+    row's loss, 0 for a masked row.  The gradient goes over z, or into dz (z's type).
+    Returns (loss [1] = sum g row_loss, row_loss [N], the gradient)."""
+    if stream is not None:
+        return _on(stream, soft_ce_topk_fwd_bwd, z, t_values, t_indices, g, t_lse, temperature,
+                   dz, row_loss, loss, workspace, held=(workspace,))
+    dev, raw = _current()
+    p_z, ld = _logits(z, "z", dev)
+    N, V = z.shape
+    f32 = torch.float32
+    if t_values.dim() != 2 or t_values.shape[1] < 1:
+        raise ValueError("t_values must be [N, K], K at least 1")
+    K = t_values.shape[1]
+    p_v = _arg(t_values, "t_values", f32, (N, K), dev)
+    p_i = _arg(t_indices, "t_indices", torch.int32, (N, K), dev)
+    p_g = _arg(g, "g", f32, (N,), dev)
+    p_l = None if t_lse is None else _arg(t_lse, "t_lse", f32, (N,), dev)
+    if dz is None:
+        dz = z
+    p_d, ld_d = _logits(dz, "dz", dev, z.dtype, z.shape)
+    if dz is not z:
+        _apart(z, ld, dz, ld_d, "dz")
+    if row_loss is None:
+        row_loss = _new((N,), f32, dev)
+    if loss is None:
+        loss = _new((1,), f32, dev)
+    L = lib()
+    if workspace is None:
+        n_ws = L.soft_ce_workspace_size(N, V)
+        workspace = _scratch(n_ws, dev, raw)
+        p_ws = workspace.data_ptr()
+    else:
+        p_ws = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        n_ws = workspace.numel() * workspace.element_size()
+    st = L.soft_ce_topk_fwd_bwd(
+        p_z, ld, p_v, p_i, p_l, p_g, N, V, K, temperature,
+        STT_CE_BF16 if z.dtype is torch.bfloat16 else 0, p_d, ld_d,
+        _arg(row_loss, "row_loss", f32, (N,), dev), _arg(loss, "loss", f32, (1,), dev), p_ws, n_ws,
+        raw)
+    if st:
+        check("soft_ce_topk_fwd_bwd", st)
+    return loss, row_loss, dz
+
+
+def stt_sample(z: torch.Tensor, u: Optional[torch.Tensor] = None, rows: int = 1,
+               temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+               top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+               probs: Optional[torch.Tensor] = None, want_probs: bool = False,
+               tokens: Optional[torch.Tensor] = None, logprobs: Optional[torch.Tensor] = None,
+               stream=None):
+    """Logits z [N, V] (fp32 or bf16; rows may be a slice of wider ones; `rows` consecutive
+    ones for each of the B = N / rows sequences) to the distribution that a sequence's
+    temperature (0: greedy), top_k (int32, <= 0: off), top_p and min_p (fp32), each [B] or
+    None, leave, and with u fp32 [N] in [0, 1) a token drawn from it.
+
+    Kept are the top_k largest logits (the lower index first among equals), of those the
+    fewest that hold top_p of their probability, of those the ones min_p times as probable
+    as the first.  The token is the smallest whose cumulated probability exceeds u.
+    Returns (tokens int32 [N], logprobs fp32 [N], probs fp32 [N, V]); without u the first
+    two are None, and probs is None unless it or want_probs is given, or u is not.  probs
+    may be z itself where that is fp32."""
+    if stream is not None:
+        return _on(stream, stt_sample, z, u, rows, temperature, top_k, top_p, min_p, probs,
+                   want_probs, tokens, logprobs)
+    dev, raw = _current()
+    p_z, ld = _logits(z, "z", dev)
+    N, V = z.shape
+    if rows < 1 or N % rows:
+        raise ValueError("rows must be positive and divide N")
+    f32, i32, of = torch.float32, torch.int32, (N // rows,)
+    p_t = None if temperature is None else _arg(temperature, "temperature", f32, of, dev)
+    p_k = None if top_k is None else _arg(top_k, "top_k", i32, of, dev)
+    p_p = None if top_p is None else _arg(top_p, "top_p", f32, of, dev)
+    p_m = None if min_p is None else _arg(min_p, "min_p", f32, of, dev)
+    p_u = p_tok = p_log = p_pr = None
+    ld_p = V
+    if u is not None:
+        p_u = _arg(u, "u", f32, (N,), dev)
+        if tokens is None:
+            tokens = _new((N,), i32, dev)
+        if logprobs is None:
+            logprobs = _new((N,), f32, dev)
+        p_tok = _arg(tokens, "tokens", i32, (N,), dev)
+        p_log = _arg(logprobs, "logprobs", f32, (N,), dev)
+    elif tokens is not None or logprobs is not None:
+        raise ValueError("tokens and logprobs are given without u")
+    if probs is None and (want_probs or u is None):
+        probs = _new((N, V), f32, dev)
+    if probs is not None:
+        p_pr, ld_p = _logits(probs, "probs", dev, f32, z.shape)
+        if probs is not z:
+            _apart(z, ld, probs, ld_p, "probs")
+    st = lib().stt_sample(p_z, ld, N, V, rows, p_t, p_k, p_p, p_m, p_u,
+                          STT_LOGITS_BF16 if z.dtype is torch.bfloat16 else 0, p_tok, p_log, p_pr,
+                          ld_p, raw)
+    if st:
+        check("stt_sample", st)
+    return tokens, logprobs, probs
 
 
 def stt_device_error(stream=None) -> int:
