@@ -34,13 +34,14 @@
 namespace stt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 8;
 constexpr int kOctaves = 64;
 constexpr uint32_t kBins = 32 * kOctaves;
 constexpr int kList = 2048;                // tokens of a bin that are sorted
-constexpr int kSliceBytes = 40 * 1024;     // preferred bytes of a slice
+constexpr int kSliceBytes = 80 * 1024;     // preferred bytes of a slice
+constexpr int kSegment = 8 * (int)kBins / 2 / kWarps;  // kept tokens that a warp lists, in the bins' memory
 constexpr int64_t kBias = 1ll << 26;       // keeps 2^32 E positive
 constexpr int kUnitShift = 42;             // a weight of 1 in whole numbers is 2^42
 constexpr float kMagic = 393216.f;         // 1.5 2^18: floats there are 1/32 apart
@@ -48,14 +49,14 @@ constexpr float kMagic = 393216.f;         // 1.5 2^18: floats there are 1/32 ap
 struct Params {
   SampleArgs a;
   int C, per, chunk;
-  int units;         // runs of 32 pieces in a slice, at most
-  double octave[32]; // 2^(-j / 32)
+  int runs;            // runs of 32 pieces that a warp takes
+  uint64_t table[32];  // 2^(63 - j / 32)
 };
 
 // A row's grid: bins and weights of its logits.
 struct Grid {
-  float m0, c, c_lo, low;  // subtracted first; log2(e) / T in two parts; smallest product kept
-  int top;                 // bits of the maximum's place on the grid
+  float m0, c, c_lo;  // subtracted first; log2(e) / T in two parts
+  int top;            // bits of the maximum's place on the grid
   // z's product with c, its place on the grid, and its bin.
   struct At {
     float zz, p, ks;
@@ -65,7 +66,9 @@ struct Grid {
     At a;
     a.zz = z - m0;
     a.p = a.zz * c;
-    a.ks = fmaxf(a.p, low) + kMagic;
+    a.ks = a.p + kMagic;
+    // (Products too far below for the grid, down to -inf, give smaller floats, or ones with a
+    // sign: both are far from `top` as whole numbers, too.)
     a.bin = (uint32_t)(top - __float_as_int(a.ks));
     return a;
   }
@@ -113,38 +116,45 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, uint64_t* s) {
   return all;
 }
 
-// The weight of `count` tokens of a bin with the sum of their 2^32 E + 2^26, in units of
-// the bin's own weight.
-__device__ __forceinline__ double weight_of(int64_t count, int64_t sum) {
-  return (double)count + (double)(sum - count * kBias) * (1.0 / 4294967296.0);
-}
-__device__ __forceinline__ double octave_scale(int o) {  // 2^-o
-  return __longlong_as_double((long long)(1023 - o) << 52);
+// The weight of `count` tokens of a bin, `sum` being that of their 2^32 E + 2^26, in units
+// of 2^-42; `table` is that of 2^(63 - j / 32).
+__device__ __forceinline__ uint64_t weight_of(uint32_t bin, int64_t count, int64_t sum,
+                                              const uint64_t* table) {
+  const uint64_t n = (uint64_t)((count << 32) + (sum - count * kBias));  // below 2^53
+  const uint64_t w = __umul64hi(n << 11, table[bin & 31]);               // in 2^-42 of the octave
+  const uint32_t o = bin >> 5;
+  return o == 0 ? w : ((w >> (o - 1)) + 1) >> 1;
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[kMaxChunks];
   __shared__ uint64_t s_red[kWarps];
   __shared__ float s_max[kWarps];
   __shared__ float s_top;
   __shared__ int s_index;
-  __shared__ double s_mass[kOctaves];    // the slice's, then read by the cluster
+  __shared__ uint64_t s_mass[kOctaves];  // the slice's, read by the cluster
   __shared__ int s_count[kOctaves];
-  __shared__ double s_all_mass[kOctaves];
-  __shared__ int s_all_count[kOctaves];
-  __shared__ double s_tab[32];
-  __shared__ uint32_t s_tab32[32];
+  __shared__ uint64_t s_run[kOctaves];   // the row's, with all octaves before
+  __shared__ int s_run_n[kOctaves];
+  __shared__ uint64_t s_tab[32];
+  __shared__ float s_c[2];
+  __shared__ double s_log;               // T log(min_p)
+  __shared__ uint64_t s_target;
   __shared__ int s_n;
   __shared__ uint64_t s_total;
   __shared__ uint64_t s_sum[2][2];  // of the halving steps: counts and sums, in turn
   struct Found {
     uint32_t bin;
     int before, in_bin, offset;  // tokens before it, in it, and of those in slices before
-    double mass;                 // weight before it
+    uint64_t mass;               // weight before it
   };
   __shared__ Found s_found;
+  struct Chosen {
+    uint64_t key, count, sum;
+  };
+  __shared__ Chosen s_cut;
   constexpr int G = RowSlice<T>::G;
   const SampleArgs& A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -157,7 +167,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   uint32_t* const bin_lo = reinterpret_cast<uint32_t*>(smem + (size_t)P.per * 16);  // sums of 2^32 E
   uint32_t* const bin_n = bin_lo + kBins;  // counts, and in the upper half the sums' carries
   uint64_t* const list = reinterpret_cast<uint64_t*>(bin_n + kBins);
-  uint64_t* const unit = list + kList;
+  uint64_t* const run_sum = list + kList;  // [kWarps][P.runs]
+  uint16_t* const kept = reinterpret_cast<uint16_t*>(bin_lo) + warp * kSegment;  // this warp's, places in the slice
 
   const float temp = A.temperature ? A.temperature[b] : 1.f;
   const int top_k = A.top_k ? A.top_k[b] : 0;
@@ -166,10 +177,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const bool greedy = temp == 0.f || top_k == 1;
   const bool want_k = !greedy && top_k > 0 && top_k < A.V;
   const bool want_p = !greedy && top_p < 1.f;
-  if (tid < 32) {
-    s_tab[tid] = P.octave[tid];
-    s_tab32[tid] = (uint32_t)(P.octave[tid] * 2147483648.0 + 0.5);
+  // (In 64-bit floats, of which an SM does two at a time, by one thread.)
+  if (tid == 64) {
+    const double c = 1.4426950408889634074 / (double)(greedy ? 1.f : temp);
+    const float hi = (float)fmin(c, (double)FLT_MAX);
+    s_c[0] = hi;
+    s_c[1] = c < (double)FLT_MAX ? (float)(c - (double)hi) : 0.f;
+    if (min_p > 0.f) s_log = (double)temp * log((double)fminf(min_p, 1.f));
   }
+  if (tid < 32) s_tab[tid] = P.table[tid];
   if (want_k || want_p)
     for (int i = tid; i < 2 * (int)kBins; i += kThreads) bin_lo[i] = 0;
   if (tid == 0) s_index = INT_MAX;
@@ -241,22 +257,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return;
   }
 
+  const bool truncated = greedy || want_k || want_p || min_p > 0.f;
+  if (probs && truncated) {
+    // Most of the row; what is kept is written over it.
+    const float zero[G] = {};
+    for (int q = tid; q < S.pieces; q += kThreads) put(S.index(q), zero);
+  }
+
   // ---- the grid
   Grid grid;
   {
-    const double c = 1.4426950408889634074 / (double)(greedy ? 1.f : temp);
-    grid.c = (float)fmin(c, (double)FLT_MAX);
-    grid.c_lo = c < (double)FLT_MAX ? (float)(c - (double)grid.c) : 0.f;
+    grid.c = s_c[0];
+    grid.c_lo = s_c[1];
     // Where the products would leave the grid's range the maximum is taken off first: the
     // logits that matter are then within a 2^10th of it and the difference is exact.
     grid.m0 = fabsf(m) * grid.c < 65536.f ? 0.f : m;
-    grid.low = -FLT_MAX;
-    const float p = (m - grid.m0) * grid.c;
-    grid.top = __float_as_int(p + kMagic);
-    grid.low = p - (kOctaves + 1.f);
+    grid.top = __float_as_int((m - grid.m0) * grid.c + kMagic);
   }
 
-  Cut cut{-INFINITY, -1};
+  Cut cut{-INFINITY, INT_MAX};  // (the weight of -inf is 0)
   auto cut_at = [&](float z, int v) {  // the stricter of the two
     if (z > cut.z || (z == cut.z && v < cut.v)) cut = Cut{z, v};
   };
@@ -278,8 +297,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < G; ++e) {
         const auto a = grid.at(x[e]);
+        const uint32_t v = (uint32_t)(grid.e32(a) + (int)kBias);
         if (a.bin < kBins) {
-          const uint32_t v = (uint32_t)(grid.e32(a) + (int)kBias);
           const uint32_t old = atomicAdd(&bin_lo[a.bin], v);
           atomicAdd(&bin_n[a.bin], 1u + (old + v < old ? 1u << 16 : 0u));
         }
@@ -291,48 +310,51 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     // Octaves: a warp's lanes take an octave's bins.
     for (int o = warp; o < kOctaves; o += kWarps) {
       const uint32_t lo = bin_lo[o * 32 + lane], n = bin_n[o * 32 + lane];
-      double w = weight_of(bin_count(n), bin_sum(lo, n)) * s_tab[lane];
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+      const uint64_t w = warp_sum64(weight_of(o * 32 + lane, bin_count(n), bin_sum(lo, n), s_tab));
       const int k = __reduce_add_sync(0xffffffffu, bin_count(n));
       if (lane == 0) {
-        s_mass[o] = w * octave_scale(o);
+        s_mass[o] = w;
         s_count[o] = k;
       }
     }
     cluster_sync();
     if (tid < kOctaves) {
-      double w = 0.0;
+      uint64_t w = 0;
       int k = 0;
       for (int r = 0; r < C; ++r) {
         w += ld_cluster(&s_mass[tid], r);
         k += ld_cluster(&s_count[tid], r);
       }
-      s_all_mass[tid] = w;
-      s_all_count[tid] = k;
+      s_run[tid] = w;
+      s_run_n[tid] = k;
     }
     __syncthreads();
-    double whole = 0.0;  // the row's weight, every thread's in the same order
-    int many = 0;
-    for (int o = 0; o < kOctaves; ++o) {
-      whole += s_all_mass[o];
-      many += s_all_count[o];
+    if (warp == 0) {
+      uint64_t w[2] = {s_run[2 * lane], s_run[2 * lane + 1]};
+      uint32_t n[2] = {(uint32_t)s_run_n[2 * lane], (uint32_t)s_run_n[2 * lane + 1]};
+      const uint64_t run = warp_scan64(w[0] + w[1]), run_n = warp_scan64((uint64_t)(n[0] + n[1]));
+      s_run[2 * lane] = run - w[1];
+      s_run[2 * lane + 1] = run;
+      s_run_n[2 * lane] = (int)run_n - (int)n[1];
+      s_run_n[2 * lane + 1] = (int)run_n;
     }
+    __syncthreads();
+    uint64_t whole = s_run[kOctaves - 1];  // the row's weight
+    const int many = s_run_n[kOctaves - 1];
 
     // Finds the bin where the running count reaches `k`, or (k < 0) the running weight
-    // reaches `target`: into s_found, by warp 0.  False: no bin does.
-    auto find_bin = [&](int k, double target) {
-      double before = 0.0;
-      int count = 0, o = 0;
-      for (; o < kOctaves; ++o) {
-        const double w = before + s_all_mass[o];
-        const int n = count + s_all_count[o];
-        if (k >= 0 ? n >= k : w >= target) break;
-        before = w;
-        count = n;
-      }
-      if (o == kOctaves) return false;
+    // reaches `target`: into s_found, by warp 0.  One does.
+    auto find_bin = [&](int k, uint64_t target) {
       if (warp == 0) {
+        int o = 0;
+        for (int half = 0; half < 2; ++half) {
+          const int i = half * 32 + lane;
+          const bool reached = k >= 0 ? s_run_n[i] >= k : s_run[i] >= target;
+          o += __popc(~__ballot_sync(0xffffffffu, reached));
+        }
+        o = min(o, kOctaves - 1);
+        const uint64_t before = o ? s_run[o - 1] : 0;
+        const int before_n = o ? s_run_n[o - 1] : 0;
         // The octave's bins over the cluster, a lane to each.
         int n = 0, offset = 0;
         int64_t sum = 0;
@@ -342,37 +364,23 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
           n += bin_count(c);
           sum += bin_sum(lo, c);
         }
-        const double w = weight_of(n, sum) * s_tab[lane] * octave_scale(o);
-        // (One after another, as the octaves: what a bin holds before it is the same sum
-        // for everyone.)
-        double run = before, mine = before;
-        int at = count, mine_n = count, hit = 32;
-        int last = -1;
-        for (int j = 0; j < 32; ++j) {
-          const double wj = __shfl_sync(0xffffffffu, w, j);
-          const int nj = __shfl_sync(0xffffffffu, n, j);
-          if (lane == j) {
-            mine = run;
-            mine_n = at;
-          }
-          run += wj;
-          at += nj;
-          if (nj > 0) last = j;
-          if (hit == 32 && nj > 0 && (k >= 0 ? at >= k : run >= target)) hit = j;
-        }
-        // (The octave's weight was summed in another order: its last bin with tokens.)
-        if (hit == 32) hit = last < 0 ? 0 : last;
-        if (lane == hit) s_found = Found{(uint32_t)(o * 32 + lane), mine_n, n, offset, mine};
+        const uint64_t w = weight_of(o * 32 + lane, n, sum, s_tab);
+        const uint64_t run = before + warp_scan64(w);
+        const int run_n = before_n + (int)warp_scan64((uint64_t)n);
+        const uint32_t reached =
+            __ballot_sync(0xffffffffu, n > 0 && (k >= 0 ? run_n >= k : run >= target));
+        const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
+        // (The octave's own weight is a sum of rounded ones: its last bin with tokens.)
+        const int hit = reached ? __ffs((int)reached) - 1 : any ? 31 - __clz((int)any) : 0;
+        if (lane == hit) s_found = Found{(uint32_t)(o * 32 + lane), run_n - n, n, offset, run - w};
       }
       __syncthreads();
-      return true;
     };
     // Halves the found bin by key: kept are the tokens down to the one at which the
     // running count in the bin reaches `need`, or (need < 0) the row's weight `target`.
     // Returns their count and sum of 2^32 E + 2^26, and cuts there.
     int turn = 0;
-    auto halve = [&](const Found& f, int need, double target, int64_t& count, int64_t& sum) {
-      const double scale = s_tab[f.bin & 31] * octave_scale((int)(f.bin >> 5));
+    auto halve = [&](const Found& f, int need, uint64_t target, int64_t& count, int64_t& sum) {
       auto reaches = [&](uint64_t key, int64_t& n, int64_t& s) {
         uint64_t my_n = 0, my_s = 0;
         each_piece([&](const float (&x)[G], int v) {
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         turn ^= 1;
         n = (int64_t)warp_sum64(on);
         s = (int64_t)warp_sum64(os);
-        return need >= 0 ? n >= need : n > 0 && f.mass + scale * weight_of(n, s) >= target;
+        return need >= 0 ? n >= need : n > 0 && f.mass + weight_of(f.bin, n, s, s_tab) >= target;
       };
       // The logit first, then the index.
       uint64_t lo = 0, hi = (uint64_t)order_of(m) + 1;  // `lo` reaches, `hi` does not
@@ -419,168 +427,232 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       reaches(z | lo, count, sum);
       cut_at(logit_of((uint32_t)(z >> 32)), key_index(z | lo));
     };
-    // Gathers the found bin's tokens, sorts them and cuts as halve() does.
-    auto select = [&](const Found& f, int need, double target, int64_t& count, int64_t& sum) {
-      const double scale = s_tab[f.bin & 31] * octave_scale((int)(f.bin >> 5));
+    // Gathers the found bin's tokens in the row's first CTA, which sorts them and cuts as
+    // halve() does.
+    auto select = [&](const Found& f, int need, uint64_t target, int64_t& count, int64_t& sum) {
       const int n = f.in_bin;
       if (tid == 0) s_n = 0;
-      cluster_sync();  // and everyone is done with its list
+      cluster_sync();  // and the first CTA is done with its list
       each_piece([&](const float (&x)[G], int v) {
 #pragma unroll
         for (int e = 0; e < G; ++e) {
           if (grid.at(x[e]).bin == f.bin) {
             const int at = f.offset + atomicAdd(&s_n, 1);
-            const uint64_t key = place_key(x[e], v + e);
-            if (at < kList)
-              for (int r = 0; r < C; ++r) st_cluster(&list[at], r, key);
+            if (at < kList) st_cluster(&list[at], 0, place_key(x[e], v + e));
           }
         }
       });
-      const int size = next_power(n);
-      for (int i = n + tid; i < size; i += kThreads) list[i] = 0;
       cluster_sync();
-      sort_keys<kThreads>(list, size);
-      // Running sums over the sorted tokens, a run of them to a thread.
-      const int each = (size + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
-      uint64_t mine = 0;
-      auto e_of = [&](uint64_t key) {
-        return (uint64_t)(grid.e32(grid.at(logit_of((uint32_t)(key >> 32)))) + (int)kBias);
-      };
-      for (int i = i0; i < i1; ++i) mine += e_of(list[i]);
-      const uint64_t incl = warp_scan64(mine);
-      if (lane == 31) s_red[warp] = incl;
-      __syncthreads();
-      uint64_t run = incl - mine;
-      for (int w = 0; w < warp; ++w) run += s_red[w];
-      __syncthreads();
-      int kept = 0;
-      uint64_t kept_sum = 0;
-      for (int i = i0; i < i1; ++i) {
-        const bool keep = need >= 0 ? i < need
-                                    : i == 0 || f.mass + scale * weight_of(i, (int64_t)run) < target;
-        if (!keep) break;
-        const uint64_t v = e_of(list[i]);
-        run += v;
-        ++kept;
-        kept_sum += v;
+      if (rank == 0) {
+        const int size = next_power(n);
+        for (int i = n + tid; i < size; i += kThreads) list[i] = 0;
+        __syncthreads();
+        sort_keys<kThreads>(list, size);
+        // Running sums over the sorted tokens, a run of them to a thread.
+        const int each = (size + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
+        uint64_t mine = 0;
+        auto e_of = [&](uint64_t key) {
+          return (uint64_t)(grid.e32(grid.at(logit_of((uint32_t)(key >> 32)))) + (int)kBias);
+        };
+        for (int i = i0; i < i1; ++i) mine += e_of(list[i]);
+        const uint64_t incl = warp_scan64(mine);
+        if (lane == 31) s_red[warp] = incl;
+        if (tid == 0) s_cut = Chosen{};
+        __syncthreads();
+        uint64_t run = incl - mine;
+        for (int w = 0; w < warp; ++w) run += s_red[w];
+        // The last token that is kept, whose next one is not.
+        for (int i = i0; i < i1; ++i) {
+          const uint64_t next = run + e_of(list[i]);
+          const bool keep = need >= 0 ? i < need
+                                      : i == 0 || f.mass + weight_of(f.bin, i, (int64_t)run, s_tab) < target;
+          const bool more = need >= 0 ? i + 1 < need
+                                      : f.mass + weight_of(f.bin, i + 1, (int64_t)next, s_tab) < target;
+          if (keep && (i + 1 == n || !more)) s_cut = Chosen{list[i], (uint64_t)(i + 1), next};
+          run = next;
+        }
       }
-      count = (int64_t)block_sum64((uint64_t)kept, s_red);
-      sum = (int64_t)block_sum64(kept_sum, s_red);
-      const uint64_t last = list[count - 1];
+      cluster_sync();
+      const uint64_t last = ld_cluster(&s_cut.key, 0);
+      count = (int64_t)ld_cluster(&s_cut.count, 0);
+      sum = (int64_t)ld_cluster(&s_cut.sum, 0);
       cut_at(logit_of((uint32_t)(last >> 32)), key_index(last));
     };
-    auto cut_bin = [&](int need, double target, int64_t& count, int64_t& sum) {
+    auto cut_bin = [&](int need, uint64_t target) {
       const Found f = s_found;
+      int64_t count, sum;
       if (f.in_bin <= kList) select(f, need < 0 ? -1 : need - f.before, target, count, sum);
       else halve(f, need < 0 ? -1 : need - f.before, target, count, sum);
-      return f.mass + s_tab[f.bin & 31] * octave_scale((int)(f.bin >> 5)) * weight_of(count, sum);
+      return f.mass + weight_of(f.bin, count, sum, s_tab);
     };
-    int64_t count, sum;
-    if (want_k && many > top_k && find_bin(top_k, 0.0)) whole = cut_bin(top_k, 0.0, count, sum);
-    __syncthreads();
-    if (want_p && find_bin(-1, fmin((double)top_p, 1.0) * whole))
-      cut_bin(-1, fmin((double)top_p, 1.0) * whole, count, sum);
+    if (want_k && many > top_k) {
+      find_bin(top_k, 0);
+      whole = cut_bin(top_k, 0);
+    }
+    if (want_p) {
+      // A beginning is short of p times the whole if, as a whole number, it is below this.
+      if (tid == 0) s_target = (uint64_t)ceil(fmax(0.0, (double)top_p) * (double)whole);
+      __syncthreads();
+      const uint64_t target = s_target;
+      find_bin(-1, target);
+      cut_bin(-1, target);
+    }
   }
   if (!greedy && min_p > 0.f) {
     // w >= min_p: z >= max + T log(min_p), as the smallest float that satisfies it.
-    const double z = (double)m + (double)temp * log((double)fminf(min_p, 1.f));
-    cut_at(__double2float_ru(z), INT_MAX);
+    cut_at(__double2float_ru((double)m + s_log), INT_MAX);
   }
 
-  // ---- the kept weights in whole numbers, by runs of 32 pieces in the order of indices
+  // ---- the kept weights in whole numbers
   auto weight = [&](float x) -> uint64_t {
     const auto a = grid.at(x);
     if (a.bin >= kBins) return 0;
-    const uint32_t t = s_tab32[a.bin & 31];
+    const uint32_t t = (uint32_t)(s_tab[a.bin & 31] >> 32);
     const uint32_t w = t + (uint32_t)((int64_t)((uint64_t)t) * grid.e32(a) >> 32);
     // w / 2^31 2^-octave, in units of 2^-42, rounded.
     const uint64_t u = (uint64_t)w << (kUnitShift - 31 + 1) >> (a.bin >> 5);
     return (u + 1) >> 1;
   };
-  uint64_t mine = 0;
-  for (int q0 = warp * 32; q0 < S.pieces; q0 += kThreads) {
-    const int q = q0 + lane;
+  // A warp takes its slice's pieces in order, as runs of 32, and lists what is kept of
+  // them; where that is too much for its list, `dense`, it adds up run by run.
+  const int q_begin = min(S.pieces, warp * P.runs * 32), q_end = min(S.pieces, q_begin + P.runs * 32);
+  int n_kept = 0;
+  bool dense = !truncated;
+  // (The bins' memory: no neighbour reads bins after the barriers of the cut.)
+  for (int q0 = q_begin; q0 < q_end && !dense; q0 += 32) {
+    const int q = q0 + lane, v = S.index(q);
     float x[G];
-    bool any = false;
-    const int v = S.index(q);
-    if (q < S.pieces) {
+    uint32_t keep = 0;
+    if (q < q_end) {
       unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
 #pragma unroll
-      for (int e = 0; e < G; ++e) any |= x[e] >= cut.z && x[e] > -INFINITY;
-    }
-    uint64_t w = 0;
-    if (__any_sync(0xffffffffu, any)) {
-      if (any) {
+      for (int e = 0; e < G; ++e) keep |= x[e] >= cut.z ? 1u << e : 0u;
+      if (keep) {
 #pragma unroll
         for (int e = 0; e < G; ++e)
-          if (cut.keeps(x[e], v + e)) w += weight(x[e]);
+          if (x[e] == -INFINITY || !cut.keeps(x[e], v + e)) keep &= ~(1u << e);
+      }
+    }
+    if (__any_sync(0xffffffffu, keep != 0)) {
+      const int n = __popc(keep);
+      int at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += t;
+      }
+      const int all = __shfl_sync(0xffffffffu, at, 31);
+      if (n_kept + all > kSegment) {
+        dense = true;
+      } else {
+        at += n_kept - n;
+        for (uint32_t k = keep; k; k &= k - 1) kept[at++] = (uint16_t)(q * G + __ffs((int)k) - 1);
+        n_kept += all;
+      }
+    }
+  }
+  __syncwarp();
+  uint64_t mine = 0;
+  if (!dense) {
+    for (int i = lane; i < n_kept; i += 32) mine += weight((float)zs[kept[i]]);
+    mine = warp_sum64(mine);
+  } else {
+    for (int q0 = q_begin; q0 < q_end; q0 += 32) {
+      const int q = q0 + lane, v = S.index(q);
+      uint64_t w = 0;
+      if (q < q_end) {
+        float x[G];
+        unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const uint64_t t = weight(x[e]);  // (0 for -inf)
+          if (cut.keeps(x[e], v + e)) w += t;
+        }
       }
       w = warp_sum64(w);
+      if (lane == 0) run_sum[warp * P.runs + (q0 - q_begin) / 32] = w;
+      mine += w;
     }
-    if (lane == 0) unit[q0 / 32] = w;
-    mine += w;  // the same in every lane
   }
   if (lane == 0) s_red[warp] = mine;
   __syncthreads();
-  mine = 0;
+  uint64_t slice = 0, slice_before = 0;  // the slice's, and what its warps before this one have
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mine += s_red[w];
-  if (tid == 0) s_total = mine;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) slice_before += s_red[w];
+    slice += s_red[w];
+  }
+  if (tid == 0) s_total = slice;
   cluster_sync();
   uint64_t total, before;
   {
     const uint64_t o = lane < C ? ld_cluster(&s_total, lane) : 0;
     const uint64_t run = warp_scan64(o);
     total = __shfl_sync(0xffffffffu, run, 31);
-    before = __shfl_sync(0xffffffffu, run - o, rank);
+    before = __shfl_sync(0xffffffffu, run - o, rank) + slice_before;
   }
   cluster_arrive_release();  // done with the neighbours' shared memory; waited for at the end
 
-  // ---- the token
-  if (A.u && warp == 0) {
+  // ---- the token: its warp finds it
+  if (A.u && before < total) {
     uint64_t at = (uint64_t)fmax(0.0, (double)A.u[row] * (double)total);
     at = min(at, total - 1);
+    auto drawn = [&](int v, uint64_t w) {
+      if (A.tokens) A.tokens[row] = v;
+      if (A.logprobs) A.logprobs[row] = logf((float)w / (float)total);
+    };
     if (before <= at && at < before + mine) {
       at -= before;
-      // The run of pieces, then the lane's piece, then the element.
-      const int n = (S.pieces + 31) / 32;
-      int q0 = 0;
-      for (int u0 = 0; u0 < n; u0 += 32) {
-        const uint64_t w = u0 + lane < n ? unit[u0 + lane] : 0;
-        const uint64_t run = warp_scan64(w);
-        const uint32_t over = __ballot_sync(0xffffffffu, run > at);
-        if (over) {
-          const int j = __ffs((int)over) - 1;
-          at -= __shfl_sync(0xffffffffu, run - w, j);
-          q0 = (u0 + j) * 32;
-          break;
+      if (!dense) {
+        for (int i0 = 0; i0 < n_kept; i0 += 32) {
+          const int place = i0 + lane < n_kept ? kept[i0 + lane] : 0;
+          const uint64_t w = i0 + lane < n_kept ? weight((float)zs[place]) : 0;
+          const uint64_t run = warp_scan64(w);
+          if (run > at && run - w <= at) drawn(S.first + place, w);
+          const uint64_t all = __shfl_sync(0xffffffffu, run, 31);
+          if (all > at) break;
+          at -= all;
         }
-        at -= __shfl_sync(0xffffffffu, run, 31);
-      }
-      const int q = q0 + lane, v = S.index(q);
-      float x[G];
-      uint64_t w[G], sum = 0;
-#pragma unroll
-      for (int e = 0; e < G; ++e) w[e] = 0;
-      if (q < S.pieces) {
-        unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
-#pragma unroll
-        for (int e = 0; e < G; ++e) {
-          if (x[e] > -INFINITY && cut.keeps(x[e], v + e)) w[e] = weight(x[e]);
-          sum += w[e];
+      } else {
+        // The run of pieces, then the lane's piece, then the element.
+        const int n = (q_end - q_begin + 31) / 32;
+        int q0 = q_begin;
+        for (int u0 = 0; u0 < n; u0 += 32) {
+          const uint64_t w = u0 + lane < n ? run_sum[warp * P.runs + u0 + lane] : 0;
+          const uint64_t run = warp_scan64(w);
+          const uint32_t over = __ballot_sync(0xffffffffu, run > at);
+          if (over) {
+            const int j = __ffs((int)over) - 1;
+            at -= __shfl_sync(0xffffffffu, run - w, j);
+            q0 = q_begin + (u0 + j) * 32;
+            break;
+          }
+          at -= __shfl_sync(0xffffffffu, run, 31);
         }
-      }
-      const uint64_t run = warp_scan64(sum);
-      if (run - sum <= at && at < run) {
-        uint64_t acc = run - sum;
-        bool done = false;
+        const int q = q0 + lane, v = S.index(q);
+        float x[G];
+        uint64_t w[G], sum = 0;
 #pragma unroll
-        for (int e = 0; e < G; ++e) {
-          acc += w[e];
-          if (!done && acc > at) {
-            done = true;
-            if (A.tokens) A.tokens[row] = v + e;
-            if (A.logprobs) A.logprobs[row] = logf((float)w[e] / (float)total);
+        for (int e = 0; e < G; ++e) w[e] = 0;
+        if (q < q_end) {
+          unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
+#pragma unroll
+          for (int e = 0; e < G; ++e) {
+            if (cut.keeps(x[e], v + e)) w[e] = weight(x[e]);
+            sum += w[e];
+          }
+        }
+        const uint64_t run = warp_scan64(sum);
+        if (run - sum <= at && at < run) {
+          uint64_t acc = run - sum;
+          bool done = false;
+#pragma unroll
+          for (int e = 0; e < G; ++e) {
+            acc += w[e];
+            if (!done && acc > at) {
+              done = true;
+              drawn(v + e, w[e]);
+            }
           }
         }
       }
@@ -590,20 +662,30 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   // ---- the probabilities
   if (probs) {
     // 1 / total, for weights in units of the maximum's bin.
-    const float inv = (float)((double)(1ull << kUnitShift) / (double)total);
-    each_piece([&](const float (&x)[G], int v) {
-      float y[G];
-#pragma unroll
-      for (int e = 0; e < G; ++e) {
-        y[e] = 0.f;
-        if (x[e] >= cut.z && x[e] > -INFINITY && cut.keeps(x[e], v + e)) {
-          const auto a = grid.at(x[e]);
-          if (a.bin < kBins)
-            y[e] = ex2((float)a.bin * (-1.f / 32.f)) * fmaf((float)grid.e32(a), 0x1p-32f, 1.f) * inv;
-        }
+    const float inv = 1.f / ((float)total * 0x1p-42f);
+    auto probability = [&](float x) {
+      const auto a = grid.at(x);
+      const float p = ex2((float)a.bin * (-1.f / 32.f)) * fmaf((float)grid.e32(a), 0x1p-32f, 1.f) * inv;
+      return a.bin < kBins ? p : 0.f;
+    };
+    if (!dense) {
+      for (int i = lane; i < n_kept; i += 32) {
+        const int place = kept[i];
+        probs[S.first + place] = probability((float)zs[place]);
       }
-      put(v, y);
-    });
+    } else {
+      for (int q = q_begin + lane; q < q_end; q += 32) {
+        const int v = S.index(q);
+        float x[G], y[G];
+        unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const float p = probability(x[e]);
+          y[e] = cut.keeps(x[e], v + e) ? p : 0.f;
+        }
+        put(v, y);
+      }
+    }
   }
   __syncwarp();
   cluster_wait_acquire();
@@ -615,7 +697,8 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   const int size = a.bf16 ? 2 : 4;
   Params P{};
   P.a = a;
-  for (int j = 0; j < 32; ++j) P.octave[j] = std::exp2(-j / 32.0);
+  for (int j = 0; j < 32; ++j)  // (exact in a double, but for its last bits)
+    P.table[j] = j == 0 ? 1ull << 63 : (uint64_t)std::ldexp(std::exp2(-j / 32.0), 63);
   int C = (int)((a.V * (int64_t)size + kSliceBytes - 1) / kSliceBytes);
   C = std::max(1, std::min(C, kRowMaxCtas));
   while (C < kRowMaxCtas && a.N * 2 * C <= sm_count() && slice_pieces(a.V, size, C) >= 2 * kThreads) C *= 2;
@@ -624,8 +707,8 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   P.per = (int)slice_pieces(a.V, size, C);
   const int round = 512;
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
-  P.units = (P.per + 31) / 32;
-  const int smem = P.per * 16 + kBins * 8 + kList * 8 + P.units * 8;
+  P.runs = ((P.per + 31) / 32 + kWarps - 1) / kWarps;
+  const int smem = P.per * 16 + kBins * 8 + kList * 8 + kWarps * P.runs * 8;
   prof_before(s, STT_KERNEL_SAMPLE);
   const cudaError_t e = a.bf16 ? launch_rows(sample_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
                                : launch_rows(sample_kernel<float>, P, a.N, C, kThreads, smem, s);
