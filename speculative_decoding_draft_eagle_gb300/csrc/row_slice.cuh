@@ -122,10 +122,67 @@ __device__ __forceinline__ int key_index(uint64_t key) {
   return (int)(0xffffffffu - (uint32_t)key);
 }
 
-// Sorts n keys (a power of two) in shared memory, the largest first: a bitonic network
-// over the block's threads.  Ends with a __syncthreads().
+// Sorts n keys (a power of two) in shared memory, the largest first: a bitonic network.
+// Thread t holds keys t, t + kThreads, .. (E of them): steps between those stay in its
+// registers, steps within a warp go by shuffles, and only those between warps through
+// shared memory (9 of 45 for 512 keys and 256 threads).
+template <int kThreads, int E>
+__device__ __forceinline__ void sort_held(uint64_t* a, int n) {
+  const int tid = threadIdx.x;
+  uint64_t key[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) key[e] = tid + e * kThreads < n ? a[tid + e * kThreads] : 0;
+  for (int size = 2; size <= n; size *= 2) {
+    for (int step = size / 2; step > 0; step /= 2) {
+      if (step >= kThreads) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+#pragma unroll
+          for (int d = 1; d < E; d *= 2) {
+            if (step == d * kThreads && (e & d) == 0) {
+              const bool down = ((e * kThreads + tid) & size) == 0;
+              const uint64_t x = key[e], y = key[e | d];
+              if ((x < y) == down) {
+                key[e] = y;
+                key[e | d] = x;
+              }
+            }
+          }
+        }
+        continue;
+      }
+      uint64_t other[E];
+      if (step >= 32) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (tid + e * kThreads < n) a[tid + e * kThreads] = key[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) other[e] = tid + e * kThreads < n ? a[(tid + e * kThreads) ^ step] : 0;
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) other[e] = __shfl_xor_sync(0xffffffffu, key[e], step);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = tid + e * kThreads;
+        const bool larger = ((i & step) == 0) == ((i & size) == 0);
+        key[e] = (key[e] < other[e]) == larger ? other[e] : key[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (tid + e * kThreads < n) a[tid + e * kThreads] = key[e];
+  __syncthreads();
+}
+// Ends with a __syncthreads().
 template <int kThreads>
 __device__ __forceinline__ void sort_keys(uint64_t* a, int n) {
+  if (n <= kThreads) return sort_held<kThreads, 1>(a, n);
+  if (n <= 2 * kThreads) return sort_held<kThreads, 2>(a, n);
+  if (n <= 4 * kThreads) return sort_held<kThreads, 4>(a, n);
   for (int size = 2; size <= n; size *= 2) {
     for (int step = size / 2; step > 0; step /= 2) {
       for (int t = threadIdx.x; t < n / 2; t += kThreads) {

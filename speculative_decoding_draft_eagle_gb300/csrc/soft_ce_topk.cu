@@ -9,15 +9,17 @@
 //
 // Bound by HBM: a logit is read once and its gradient written once.  A cluster of C
 // CTAs takes a row, each its slice in shared memory (bulk copies); the maximum and sum
-// of every slice, and its part of sum p z, are exchanged through distributed shared
-// memory, and the gradient is written out of shared memory.  The teacher's entries are
-// held by the threads: an entry's CTA writes its element again after the dense pass.
-// Entries of the same token are found with a bit map over the slice; only then are
-// they added up, in their order.
+// of every slice, and its part of sum p z, go to the others by st.async, which signals an
+// mbarrier there (a cluster barrier would wait for stores to drain), and the gradient is
+// written out of shared memory.  One warp looks through the teacher's entries meanwhile
+// and lists the slice's own; their elements are written again after the dense pass.
+// Entries of the same token are found with a bit map over the slice; only then are they
+// added up, in their order.
 #include <algorithm>
 #include <cmath>
 
 #include "../../include/stt.h"
+#include "attn_common.cuh"
 #include "row_slice.cuh"
 
 namespace stt {
@@ -26,9 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 8;
-constexpr int kEntries = kSoftCeTopkMaxK / kThreads;  // of the teacher's, to a thread
 constexpr int kSliceBytes = 40 * 1024;  // preferred bytes of a slice
-constexpr float kLog2E = 1.4426950408889634f;
 
 struct Params {
   SoftCeTopkArgs a;
@@ -47,28 +47,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The block's sum, in a fixed order; ends with a __syncthreads().
-__device__ __forceinline__ float block_sum(float v, float* s) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float all = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += s[w];
-  __syncthreads();
-  return all;
-}
-__device__ __forceinline__ float block_max(float v, float* s) {
-  v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float all = s[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) all = fmaxf(all, s[w]);
-  __syncthreads();
-  return all;
-}
-
 template <class T>
 __device__ __forceinline__ void store_piece(T* dst, const float (&y)[16 / sizeof(T)]) {
   if constexpr (sizeof(T) == 4) {
@@ -84,11 +62,12 @@ __device__ __forceinline__ void store_piece(T* dst, const float (&y)[16 / sizeof
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(128) unsigned char smem[];  // the slice, its bit map, the entries
-  __shared__ uint64_t bars[kMaxChunks];
-  __shared__ float red[2 * kWarps];
-  __shared__ __align__(16) float4 s_part;
-  __shared__ int s_twice;
+  extern __shared__ __align__(128) unsigned char smem[];  // the slice, its bit map, its entries
+  __shared__ uint64_t bars[kMaxChunks], bar_part;
+  __shared__ float red[3][kWarps];
+  __shared__ __align__(16) float4 s_part[kRowMaxCtas];
+  __shared__ int s_entries, s_twice;
+  __shared__ float s_sum;
   constexpr int G = RowSlice<T>::G;
   const SoftCeTopkArgs& A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -126,57 +105,71 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   T* const zs = reinterpret_cast<T*>(smem);
   const int words = (P.per * G + 31) / 32;
   uint32_t* const bits = reinterpret_cast<uint32_t*>(smem + (size_t)P.per * 16);
-  int* const ent_v = reinterpret_cast<int*>(bits + words);
+  int* const ent_v = reinterpret_cast<int*>(bits + words);  // place in the slice
   float* const ent_p = reinterpret_cast<float*>(ent_v + A.K);
   for (int w = tid; w < words; w += kThreads) bits[w] = 0;
-  if (tid == 0) s_twice = 0;
+  if (tid == 0) {
+    mbar_init(&bar_part, 1);
+    fence_mbar_init();
+    if (P.C > 1) mbar_arrive_expect_tx(&bar_part, (uint32_t)P.C * 16u);
+  }
   fetch_slice(S, zs, bars, P.chunk);
+  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to a neighbour
 
-  // ---- the teacher's entries, k = tid, tid + kThreads, ..
-  float p[kEntries];
-  int at[kEntries];  // place in the slice, -1: not here
-  float s = 0.f;
-  {
+  // ---- the teacher's entries, by the last warp: p of all, and the list of the slice's own in
+  // their order
+  if (warp == kWarps - 1) {
+    const int32_t* const idx = A.indices + row * A.K;
+    const float* const val = A.values + row * A.K;
+    auto entry = [&](int k, int& v) {  // t / tau, -inf where there is none
+      v = k < A.K ? __ldg(idx + k) : -1;
+      const bool there = v >= 0 && v < A.V;
+      if (!there) v = -1;
+      return there ? __ldg(val + k) * P.inv_tau : -INFINITY;
+    };
     float L;
-    int v[kEntries];
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j) {
-      const int k = tid + j * kThreads;
-      v[j] = -1;
-      p[j] = -INFINITY;
-      if (k < A.K) {
-        v[j] = __ldg(A.indices + row * A.K + k);
-        if (v[j] >= 0 && v[j] < A.V) p[j] = __ldg(A.values + row * A.K + k) * P.inv_tau;
-        else v[j] = -1;
-      }
-    }
+    int v;
     if (A.lse) {
       L = __ldg(A.lse + row);
     } else {
-      float m = p[0], e = 0.f;
-#pragma unroll
-      for (int j = 1; j < kEntries; ++j) m = fmaxf(m, p[j]);
-      m = block_max(m, red);
-      if (m == -INFINITY) m = 0.f;
-#pragma unroll
-      for (int j = 0; j < kEntries; ++j) e += ex2((p[j] - m) * kLog2E);
-      e = block_sum(e, red);
-      L = e == 0.f ? 0.f : m + logf(e);
+      float top = -INFINITY, e = 0.f;
+      for (int k = lane; k < A.K; k += 32) top = fmaxf(top, entry(k, v));
+      top = warp_max(top);
+      if (top == -INFINITY) top = 0.f;
+      for (int k = lane; k < A.K; k += 32) e += ex2((entry(k, v) - top) * kLog2e);
+      e = warp_sum(e);
+      L = e == 0.f ? 0.f : top + logf(e);
     }
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j) {
-      p[j] = v[j] < 0 ? 0.f : ex2((p[j] - L) * kLog2E);
-      s += p[j];
-      const int x = v[j] - S.first;
-      at[j] = v[j] >= 0 && x >= 0 && x < S.pieces * G ? x : -1;
-      if (at[j] >= 0 && atomicOr(&bits[at[j] >> 5], 1u << (at[j] & 31)) >> (at[j] & 31) & 1u)
-        s_twice = 1;
+    float s = 0.f;
+    int n = 0;
+    bool twice = false;
+    for (int k0 = 0; k0 < A.K; k0 += 32) {
+      const float t = entry(k0 + lane, v);
+      const float p = v < 0 ? 0.f : ex2((t - L) * kLog2e);
+      s += p;
+      const int at = v - S.first;
+      const bool here = v >= 0 && at >= 0 && at < S.pieces * G;
+      if (here) twice |= atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u;
+      const uint32_t mask = __ballot_sync(0xffffffffu, here);
+      if (here) {
+        const int i = n + __popc(mask & ((1u << lane) - 1u));
+        ent_v[i] = at;
+        ent_p[i] = p;
+      }
+      n += __popc(mask);
     }
-    s = block_sum(s, red);
+    s = warp_sum(s);
+    twice = __any_sync(0xffffffffu, twice);
+    if (lane == 0) {
+      s_sum = s;
+      s_entries = n;
+      s_twice = twice;
+    }
   }
 
   // ---- the slice's maximum and sum of exponentials, as it arrives
   constexpr int U = 16 / G;  // pieces taken together
+  const uint64_t cc = f32x2(P.c, P.c);
   float m = -INFINITY, l = 0.f;
   const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   for (int c = 0; c < n_chunks; ++c) {
@@ -197,91 +190,102 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < G; ++e) top = fmaxf(top, x[u][e]);
+        for (int e = 0; e < G; e += 2) top = fmax3(top, x[u][e], x[u][e + 1]);
       const float base = top == -INFINITY ? 0.f : top;
-      l *= ex2((m - base) * P.c);
+      const uint64_t low = f32x2(-base, -base);
+      uint64_t sum = f32x2(l * ex2((m - base) * P.c), 0.f);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < G; ++e) l += ex2((x[u][e] - base) * P.c);
+        for (int e = 0; e < G; e += 2) {
+          float y0, y1;
+          unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[u][e], x[u][e + 1]), low), cc), y0, y1);
+          sum = add_f32x2(sum, f32x2(ex2(y0), ex2(y1)));
+        }
+      float y0, y1;
+      unpack_f32x2(sum, y0, y1);
+      l = y0 + y1;
       m = top;
     }
   }
-  // What the entries here contribute to sum p z; p = 0 counts for nothing whatever z is.
-  float d = 0.f;
-#pragma unroll
-  for (int j = 0; j < kEntries; ++j)
-    if (at[j] >= 0 && p[j] != 0.f) d = fmaf(p[j], (float)zs[at[j]] * P.inv_tau, d);
 
-  // ---- the row's, through distributed shared memory
+  // ---- the slice's, then the row's: a warp's lanes send the slice's part to the neighbours
   {
     const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
     l = warp_sum(l == 0.f ? 0.f : l * ex2((m - base) * P.c));
     if (lane == 0) {
-      red[warp] = top;
-      red[kWarps + warp] = l;
+      red[0][warp] = top;
+      red[1][warp] = l;
     }
+    __syncthreads();  // and the entries are listed
+    // What the entries here contribute to sum p z; p = 0 counts for nothing whatever z is.
+    float d = 0.f;
+    const int n = s_entries;
+    for (int i = tid; i < n; i += kThreads)
+      if (ent_p[i] != 0.f) d = fmaf(ent_p[i], (float)zs[ent_v[i]] * P.inv_tau, d);
+    if (warp * 32 < n) d = warp_sum(d);
+    if (lane == 0) red[2][warp] = d;
     __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, red[w]);
-    l = 0.f;
-    const float b = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * ex2((red[w] - b) * P.c);
-    __syncthreads();
-    d = block_sum(d, red);
   }
-  if (P.C > 1) {
-    if (tid == 0) s_part = make_float4(m, l, d, 0.f);
-    cluster_sync();
-    float4 o = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    if (lane < P.C) o = ld_shared_cluster_f4(mapa_shared(smem_u32(&s_part), (uint32_t)lane));
-    cluster_arrive_release();  // done with the neighbours' shared memory; waited for at the end
-    m = warp_max(o.x);
-    const float b = m == -INFINITY ? 0.f : m;
-    l = warp_sum(o.y == 0.f ? 0.f : o.y * ex2((o.x - b) * P.c));
-    d = warp_sum(o.z);
+  float d;
+  {
+    auto rows = [&](float a, float b, float c) {  // lanes' parts to the sum of all
+      m = warp_max(a);
+      const float base = m == -INFINITY ? 0.f : m;
+      l = warp_sum(b == 0.f ? 0.f : b * ex2((a - base) * P.c));
+      d = warp_sum(c);
+    };
+    const bool has = lane < kWarps;
+    if (P.C == 1) {
+      rows(has ? red[0][lane] : -INFINITY, has ? red[1][lane] : 0.f, has ? red[2][lane] : 0.f);
+    } else {
+      cluster_wait_acquire();
+      if (warp == 0) {
+        rows(has ? red[0][lane] : -INFINITY, has ? red[1][lane] : 0.f, has ? red[2][lane] : 0.f);
+        if (lane < P.C)
+          st_async_f4(mapa_shared(smem_u32(&s_part[rank]), (uint32_t)lane), make_float4(m, l, d, 0.f),
+                      mapa_shared(smem_u32(&bar_part), (uint32_t)lane));
+        __syncwarp();
+      }
+      cluster_arrive_release();  // this CTA has sent its part; waited for at the end
+      mbar_wait_cluster(&bar_part, 0, STT_DEVERR_CE_WAIT);
+      const float4 o = lane < P.C ? s_part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      rows(o.x, o.y, o.z);
+    }
   }
 
   if (m == -INFINITY && l == 0.f) {
     masked();  // no logit at all: nothing to learn
   } else {
-    const float scale = g * P.inv_tau, a = scale * s / l;
+    const float scale = g * P.inv_tau, s = s_sum, a = scale * s / l;
+    const uint64_t low = f32x2(-m, -m), aa = f32x2(a, a);
     for (int q = tid; q < S.pieces; q += kThreads) {
       float x[G];
       unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
 #pragma unroll
-      for (int e = 0; e < G; ++e) x[e] = ex2((x[e] - m) * P.c) * a;
+      for (int e = 0; e < G; e += 2) {
+        float y0, y1;
+        unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[e], x[e + 1]), low), cc), y0, y1);
+        unpack_f32x2(mul_f32x2(f32x2(ex2(y0), ex2(y1)), aa), x[e], x[e + 1]);
+      }
       put(q, x);
     }
-    const bool twice = s_twice != 0;  // set before the last barriers
-    if (twice) {
-#pragma unroll
-      for (int j = 0; j < kEntries; ++j) {
-        const int k = tid + j * kThreads;
-        if (k < A.K) {
-          ent_v[k] = at[j];
-          ent_p[k] = p[j];
-        }
-      }
-    }
     __syncthreads();  // the dense gradient is written
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j) {
-      if (at[j] < 0) continue;
-      float t = p[j];
+    const int n = s_entries;
+    const bool twice = s_twice != 0;
+    for (int i = tid; i < n; i += kThreads) {
+      const int at = ent_v[i];
+      float t = ent_p[i];
       bool mine = true;
       if (twice) {
         t = 0.f;
-        for (int k = 0; k < A.K; ++k) {
-          if (ent_v[k] != at[j]) continue;
-          if (k < tid + j * kThreads) mine = false;  // the first of a token's entries writes
+        for (int k = 0; k < n; ++k) {
+          if (ent_v[k] != at) continue;
+          if (k < i) mine = false;  // the first of a token's entries writes
           t += ent_p[k];
         }
       }
-      if (mine)
-        out[S.first + at[j]] = (T)fmaf(ex2(((float)zs[at[j]] - m) * P.c), a, -t * scale);
+      if (mine) out[S.first + at] = (T)fmaf(ex2(((float)zs[at] - m) * P.c), a, -t * scale);
     }
     if (rank == 0 && tid == 0) {
       const float loss = fmaf(s, m * P.inv_tau + logf(l), -d);
@@ -289,8 +293,13 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
       A.wl[row] = g * loss;
     }
   }
+  // A CTA whose wait gave up may not leave while parts are on their way to it: everyone has
+  // sent theirs, and they have landed.
   __syncwarp();
-  if (P.C > 1) cluster_wait_acquire();
+  if (P.C > 1) {
+    cluster_wait_acquire();
+    if (tid == 0) mbar_wait_cluster(&bar_part, 0, STT_DEVERR_CE_WAIT);
+  }
 }
 
 }  // namespace

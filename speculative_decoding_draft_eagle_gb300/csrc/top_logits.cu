@@ -13,9 +13,11 @@
 //
 // The K largest of each slice go to the row's first CTA, which sorts them once more.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/stt.h"
+#include "attn_common.cuh"
 #include "row_slice.cuh"
 
 namespace stt {
@@ -29,9 +31,9 @@ constexpr int kMerge = 2048;            // keys that the first CTA of a row sort
 struct Params {
   TopLogitsArgs a;
   float c;            // log2(e) / tau
-  float inv_tau;
+  float inv_tau, far; // 1 / tau; the difference of logits whose ratio is 2^64
   int C, per;         // CTAs of a row, pieces of a CTA
-  int cap;            // keys kept
+  int cap;            // keys kept, and pieces listed
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -52,8 +54,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) uint64_t keys[];  // [cap], then [C K] of the row's slices
-  __shared__ int s_n, s_count[2];
+  extern __shared__ __align__(16) uint64_t keys[];  // [cap], [C K] of the row's slices, pieces [cap]
+  __shared__ int s_n, s_pieces, s_count[2];
   __shared__ float red[2 * kWarps];
   __shared__ uint32_t hist[256];
   __shared__ uint64_t s_cut;
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   const int64_t row = blockIdx.x / (unsigned)P.C;
   const RowSlice<T> S(static_cast<const T*>(A.z) + row * A.ld_z, A.V, rank, P.per);
   const int K = A.K, cap = P.cap;
-  if (tid == 0) s_n = 0;
+  if (tid == 0) s_n = s_pieces = 0;
   if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to the first CTA
 
   // ---- a bound from the sample; -inf where the slice is kept whole
@@ -139,51 +141,75 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   }
   __syncthreads();
 
-  auto keep = [&](float z, int v) {
-    const int at = atomicAdd(&s_n, 1);
-    if (at < cap) keys[at] = place_key(z, v);
-  };
-
-  // ---- the slice, once: its sum of exponentials, and what reaches the bound
-  float m = start, l = 0.f;
-  constexpr int U = 4;
+  // ---- the slice, once: its sum of exponentials, and the pieces in which something
+  // reaches the bound.  (Few do, and the elements of those are looked at afterwards: the
+  // loop is a subtraction, a product, an exponential and a sum to an element, and half a
+  // maximum.)
+  uint32_t* const listed = reinterpret_cast<uint32_t*>(keys + cap + (P.C > 1 ? kMerge : 0));
+  float m = start, limit = start + P.far, l = 0.f;
+  uint64_t sum = 0;  // two sums side by side
   const bool all = bound == -INFINITY;
-  for (int q0 = tid; q0 < S.pieces; q0 += U * kThreads) {
-    uint4 raw[U];
-    float x[U][G];
+  const float least = all ? -FLT_MAX : bound;  // (-inf is never taken)
+  auto take = [&](int q, const float (&x)[G]) {
+    float top = max3_nan(x[0], x[1], x[2]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = q0 + u * kThreads;
-      if (q < S.pieces && S.whole(q)) raw[u] = S.load(q);
+    for (int e = 3; e < G; e += 2) top = e + 1 < G ? max3_nan(top, x[e], x[e + 1]) : max_nan(top, x[e]);
+    // (NaN, too, is not below the bound.)
+    if (!(top < least)) {
+      const int at = atomicAdd(&s_pieces, 1);
+      if (at < cap) listed[at] = (uint32_t)q;
+      if (top > limit || m == -INFINITY) {  // the sum's reference is too low, or none yet
+        float s0, s1;
+        unpack_f32x2(sum, s0, s1);
+        const float f = m == -INFINITY ? 0.f : ex2((m - top) * P.c);
+        sum = f32x2(m == -INFINITY ? 0.f : s0 * f, m == -INFINITY ? 0.f : s1 * f);
+        if (top > -INFINITY) m = top;
+        limit = m + P.far;
+      }
     }
+    const float base = m == -INFINITY ? 0.f : m;
+    const uint64_t low = f32x2(-base, -base), cc = f32x2(P.c, P.c);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = q0 + u * kThreads;
-      if (q < S.pieces) {
-        if (S.whole(q)) unpack_piece(raw[u], x[u]);
-        else S.edge(q, x[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < G; ++e) x[u][e] = -INFINITY;
-      }
-      float top = x[u][0];
-#pragma unroll
-      for (int e = 1; e < G; ++e) top = max_nan(top, x[u][e]);
-      // (NaN, too, is not below the bound.)
-      if (!(top < bound) && !(top == -INFINITY)) {
-#pragma unroll
-        for (int e = 0; e < G; ++e)
-          if (!(x[u][e] < bound) && !(x[u][e] == -INFINITY)) keep(x[u][e], S.index(q) + e);
-      }
-      if (!(top <= m)) {
-        const float to = fmaxf(m, top);  // passes NaN over; the sum shows it
-        l = m == -INFINITY ? l : l * ex2((m - to) * P.c);
-        m = to;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int e = 0; e < G; ++e) l += ex2((x[u][e] - base) * P.c);
+    for (int e = 0; e < G; e += 2) {
+      float y0, y1;
+      unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[e], x[e + 1]), low), cc), y0, y1);
+      sum = add_f32x2(sum, f32x2(ex2(y0), ex2(y1)));
     }
+  };
+  {
+    constexpr int U = 4;
+    // Whole pieces, and the one or two others.
+    const int first = S.pieces > 0 && !S.whole(0) ? 1 : 0;
+    const int last = S.pieces > 0 && !S.whole(S.pieces - 1) ? S.pieces - 1 : S.pieces;
+    const uint4* const src = reinterpret_cast<const uint4*>(S.row + S.index(0));
+    int q = first + tid;
+    for (; q + (U - 1) * kThreads < last; q += U * kThreads) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = __ldg(src + q + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[G];
+        unpack_piece(raw[u], x);
+        take(q + u * kThreads, x);
+      }
+    }
+    for (; q < last; q += kThreads) {
+      float x[G];
+      unpack_piece(__ldg(src + q), x);
+      take(q, x);
+    }
+    if (tid < 2 && S.pieces > 0) {
+      const int edge = tid == 0 ? 0 : S.pieces - 1;
+      if (!S.whole(edge) && (tid == 0 || S.pieces > 1)) {
+        float x[G];
+        S.edge(edge, x);
+        take(edge, x);
+      }
+    }
+    float s0, s1;
+    unpack_f32x2(sum, s0, s1);
+    l = s0 + s1;
   }
   {
     const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
@@ -194,7 +220,25 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     }
   }
   __syncthreads();
-  int n = s_n;
+  // ---- the elements of the listed pieces
+  const int n_pieces = s_pieces;
+  if (n_pieces <= cap) {
+    for (int i = tid; i < n_pieces; i += kThreads) {
+      const int q = (int)listed[i];
+      float x[G];
+      if (S.whole(q)) unpack_piece(S.load(q), x);
+      else S.edge(q, x);
+#pragma unroll
+      for (int e = 0; e < G; ++e) {
+        if (!(x[e] < least)) {
+          const int at = atomicAdd(&s_n, 1);
+          if (at < cap) keys[at] = place_key(x[e], S.index(q) + e);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  int n = n_pieces > cap ? cap + 1 : s_n;
 
   // ---- the K-th largest key digit by digit, where the bound did not do
   if (n > cap || (!all && n < K)) {
@@ -333,6 +377,7 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   P.a = a;
   P.c = (float)(1.4426950408889634 / (double)a.temperature);
   P.inv_tau = 1.f / a.temperature;
+  P.far = 64.f / P.c;
   // CTAs of a row: one while the rows fill the GPU, more for few rows, or for rows so
   // long that the sample says little; as many as the first one can merge.
   const int most = std::max(1, std::min(kRowMaxCtas, kMerge / a.K));
@@ -342,7 +387,7 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   P.C = C;
   P.per = (int)slice_pieces(a.V, size, C);
   P.cap = a.K <= 512 ? 2048 : 4096;
-  const int smem = P.cap * 8 + (C > 1 ? kMerge * 8 : 0);
+  const int smem = P.cap * 12 + (C > 1 ? kMerge * 8 : 0);
   prof_before(s, STT_KERNEL_TOP_LOGITS);
   const cudaError_t e =
       a.bf16 ? launch_rows(top_logits_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
