@@ -107,58 +107,91 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   uint32_t* const bits = reinterpret_cast<uint32_t*>(smem + (size_t)P.per * 16);
   int* const ent_v = reinterpret_cast<int*>(bits + words);  // place in the slice
   float* const ent_p = reinterpret_cast<float*>(ent_v + A.K);
-  for (int w = tid; w < words; w += kThreads) bits[w] = 0;
   if (tid == 0) {
     mbar_init(&bar_part, 1);
     fence_mbar_init();
     if (P.C > 1) mbar_arrive_expect_tx(&bar_part, (uint32_t)P.C * 16u);
   }
   fetch_slice(S, zs, bars, P.chunk);
-  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to a neighbour
+  if (P.C > 1) cluster_arrive_relaxed();  // everyone runs before anyone writes to a neighbour
 
   // ---- the teacher's entries, by the last warp: p of all, and the list of the slice's own in
   // their order
   if (warp == kWarps - 1) {
+    constexpr int kAhead = 4;  // groups of 32 entries whose loads are in flight
     const int32_t* const idx = A.indices + row * A.K;
     const float* const val = A.values + row * A.K;
-    auto entry = [&](int k, int& v) {  // t / tau, -inf where there is none
-      v = k < A.K ? __ldg(idx + k) : -1;
-      const bool there = v >= 0 && v < A.V;
-      if (!there) v = -1;
-      return there ? __ldg(val + k) * P.inv_tau : -INFINITY;
+    // f(group's tokens or -1, their t / tau or -inf), kAhead groups at a time
+    auto each = [&](auto&& f) {
+      for (int k0 = 0; k0 < A.K; k0 += 32 * kAhead) {
+        int v[kAhead];
+        float t[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int k = k0 + u * 32 + lane;
+          v[u] = k < A.K ? __ldg(idx + k) : -1;
+          t[u] = k < A.K ? __ldg(val + k) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const bool there = v[u] >= 0 && v[u] < A.V;
+          v[u] = there ? v[u] : -1;
+          t[u] = there ? t[u] * P.inv_tau : -INFINITY;
+        }
+        f(v, t);
+      }
     };
     float L;
-    int v;
     if (A.lse) {
       L = __ldg(A.lse + row);
     } else {
       float top = -INFINITY, e = 0.f;
-      for (int k = lane; k < A.K; k += 32) top = fmaxf(top, entry(k, v));
+      each([&](const int (&)[kAhead], const float (&t)[kAhead]) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) top = fmaxf(top, t[u]);
+      });
       top = warp_max(top);
       if (top == -INFINITY) top = 0.f;
-      for (int k = lane; k < A.K; k += 32) e += ex2((entry(k, v) - top) * kLog2e);
+      each([&](const int (&)[kAhead], const float (&t)[kAhead]) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) e += ex2((t[u] - top) * kLog2e);
+      });
       e = warp_sum(e);
       L = e == 0.f ? 0.f : top + logf(e);
     }
     float s = 0.f;
     int n = 0;
-    bool twice = false;
-    for (int k0 = 0; k0 < A.K; k0 += 32) {
-      const float t = entry(k0 + lane, v);
-      const float p = v < 0 ? 0.f : ex2((t - L) * kLog2e);
-      s += p;
-      const int at = v - S.first;
-      const bool here = v >= 0 && at >= 0 && at < S.pieces * G;
-      if (here) twice |= atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u;
-      const uint32_t mask = __ballot_sync(0xffffffffu, here);
-      if (here) {
-        const int i = n + __popc(mask & ((1u << lane) - 1u));
-        ent_v[i] = at;
-        ent_p[i] = p;
+    each([&](const int (&v)[kAhead], const float (&t)[kAhead]) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float p = v[u] < 0 ? 0.f : ex2((t[u] - L) * kLog2e);
+        s += p;
+        const int at = v[u] - S.first;
+        const bool here = v[u] >= 0 && at >= 0 && at < S.pieces * G;
+        const uint32_t mask = __ballot_sync(0xffffffffu, here);
+        if (here) {
+          const int i = n + __popc(mask & ((1u << lane) - 1u));
+          ent_v[i] = at;
+          ent_p[i] = p;
+        }
+        n += __popc(mask);
       }
-      n += __popc(mask);
-    }
+    });
     s = warp_sum(s);
+    __syncwarp();
+    // A token twice: up to 32 entries by comparison, more with the bit map.
+    bool twice = false;
+    if (n <= 32) {
+      const int at = lane < n ? ent_v[lane] : -1 - lane;
+      twice = __popc(__match_any_sync(0xffffffffu, at)) > 1;
+    } else {
+      for (int w = lane; w < words; w += 32) bits[w] = 0;
+      __syncwarp();
+      for (int i = lane; i < n; i += 32) {
+        const int at = ent_v[i];
+        twice |= atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u;
+      }
+    }
     twice = __any_sync(0xffffffffu, twice);
     if (lane == 0) {
       s_sum = s;
@@ -247,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
                       mapa_shared(smem_u32(&bar_part), (uint32_t)lane));
         __syncwarp();
       }
-      cluster_arrive_release();  // this CTA has sent its part; waited for at the end
+      cluster_arrive_relaxed();  // this CTA has sent its part; waited for at the end
       mbar_wait_cluster(&bar_part, 0, STT_DEVERR_CE_WAIT);
       const float4 o = lane < P.C ? s_part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
       rows(o.x, o.y, o.z);
@@ -259,8 +292,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   } else {
     const float scale = g * P.inv_tau, s = s_sum, a = scale * s / l;
     const uint64_t low = f32x2(-m, -m), aa = f32x2(a, a);
-    for (int q = tid; q < S.pieces; q += kThreads) {
-      float x[G];
+    auto gradient = [&](int q, float (&x)[G]) {
       unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
 #pragma unroll
       for (int e = 0; e < G; e += 2) {
@@ -268,7 +300,32 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
         unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[e], x[e + 1]), low), cc), y0, y1);
         unpack_f32x2(mul_f32x2(f32x2(ex2(y0), ex2(y1)), aa), x[e], x[e + 1]);
       }
-      put(q, x);
+    };
+    if (vec) {
+      // Whole pieces; the one or two others apart.
+      const int lo = S.pieces > 0 && !S.whole(0) ? 1 : 0;
+      const int hi = S.pieces > 0 && !S.whole(S.pieces - 1) ? S.pieces - 1 : S.pieces;
+      T* const at = out + S.index(0);
+#pragma unroll 4
+      for (int q = lo + tid; q < hi; q += kThreads) {
+        float x[G];
+        gradient(q, x);
+        store_piece<T>(at + q * G, x);
+      }
+      if (tid < 2 && S.pieces > 0) {
+        const int q = tid == 0 ? 0 : S.pieces - 1;
+        if (!S.whole(q) && (tid == 0 || S.pieces > 1)) {
+          float x[G];
+          gradient(q, x);
+          put(q, x);
+        }
+      }
+    } else {
+      for (int q = tid; q < S.pieces; q += kThreads) {
+        float x[G];
+        gradient(q, x);
+        put(q, x);
+      }
     }
     __syncthreads();  // the dense gradient is written
     const int n = s_entries;
@@ -316,7 +373,7 @@ cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s) {
   C = std::min(C, kRowMaxCtas);
   P.C = C;
   P.per = (int)slice_pieces(a.V, size, C);
-  const int round = 512;
+  const int round = 1024;  // four pieces of fp32 to a thread, or eight of bf16
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
   const int smem = P.per * 16 + (P.per * (16 / size) + 31) / 32 * 4 + a.K * 8;
   prof_before(s, STT_KERNEL_SOFT_CE_TOPK);
