@@ -198,7 +198,82 @@ __device__ __forceinline__ void sort_keys(uint64_t* a, int n) {
     }
   }
 }
+// How many of a descending run's n keys are above `key`; n is below 2^steps.
+template <int steps>
+__device__ __forceinline__ int above(const uint64_t* run, int n, uint64_t key) {
+  int at = 0;
+#pragma unroll
+  for (int s = 1 << (steps - 1); s > 0; s /= 2)
+    if (at + s <= n && run[at + s - 1] > key) at += s;
+  return at;
+}
+
+// Sorts n <= E kThreads different keys in shared memory, the largest first, as far as the
+// first K: each warp sorts 32 E by shuffles alone, and a key's place is the sum of its
+// places among the warps' runs.  Ends with a __syncthreads().
+template <int kThreads, int E>
+__device__ __forceinline__ void sort_runs(uint64_t* a, int n, int K) {
+  constexpr int kRun = 32 * E;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp * kRun;
+  uint64_t key[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) key[e] = first + e * 32 + lane < n ? a[first + e * 32 + lane] : 0;
+  if (first < n) {
+    // Key e of a lane is number lane + 32 e of the run.
+#pragma unroll
+    for (int size = 2; size <= kRun; size *= 2) {
+#pragma unroll
+      for (int step = size / 2; step > 0; step /= 2) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool down = ((lane + 32 * e) & size) == 0;
+          if (step >= 32) {
+            const int f = e | (step / 32);
+            if (f != e && (key[e] < key[f]) == down) {
+              const uint64_t x = key[e];
+              key[e] = key[f];
+              key[f] = x;
+            }
+          } else {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, key[e], step);
+            const bool larger = ((lane & step) == 0) == down;
+            key[e] = (key[e] < other) == larger ? other : key[e];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (first + e * 32 + lane < n) a[first + e * 32 + lane] = key[e];
+  }
+  __syncthreads();
+  int place[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) place[e] = lane + 32 * e;
+  for (int r = 0; r * kRun < n; ++r) {
+    if (r == warp) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      place[e] += above<E == 2 ? 7 : 8>(a + r * kRun, min(kRun, n - r * kRun), key[e]);
+  }
+  static_assert(E == 2 || E == 4, "runs of 64 or 128");
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (first + e * 32 + lane < n && place[e] < K) a[place[e]] = key[e];
+  __syncthreads();
+}
 __device__ __forceinline__ int next_power(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+// Sorts n different keys as far as the first K; there is room for the next power of two.
+template <int kThreads>
+__device__ __forceinline__ void sort_top(uint64_t* a, int n, int K) {
+  if (n <= 2 * kThreads) return sort_runs<kThreads, 2>(a, n, K);
+  if (n <= 4 * kThreads) return sort_runs<kThreads, 4>(a, n, K);
+  const int size = next_power(n);
+  for (int i = n + (int)threadIdx.x; i < size; i += kThreads) a[i] = 0;
+  __syncthreads();
+  sort_keys<kThreads>(a, size);
+}
 
 // ------------------------------------------------- neighbours in a cluster --
 __device__ __forceinline__ void cluster_sync() {

@@ -4,8 +4,8 @@
 // Bound by HBM: a row is read once.  A CTA (or, with few rows, each CTA of a cluster on
 // its slice) looks at a sample of 4096 elements spread over its slice and takes a lower
 // bound of the K-th largest from it: a sample's r-th largest, with r so far above the
-// K / n share that fewer than K elements of the slice reach it about once in ten
-// thousand rows of independent logits.  Then it reads the slice, sums the exponentials
+// K / n share that fewer than K elements of the slice reach it about once in a
+// million rows of independent logits.  Then it reads the slice, sums the exponentials
 // and keeps what reaches the bound, a few times K elements, as 64-bit keys of logit and
 // index, sorts those and has the first K.  Where the bound was too high, or too many
 // reach it (equal logits, orders that the sample does not show), the K-th largest key
@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSample = 16 * kThreads;  // elements looked at first
+constexpr int kHeld = 1024;             // listed pieces that are kept with their places
 constexpr int kMerge = 2048;            // keys that the first CTA of a row sorts, at most
 
 struct Params {
@@ -54,8 +55,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) uint64_t keys[];  // [cap], [C K] of the row's slices, pieces [cap]
-  __shared__ int s_n, s_pieces, s_count[2];
+  extern __shared__ __align__(16) uint64_t keys[];  // [cap], [C K] of the row's slices, kHeld pieces, the places of [cap]
+  __shared__ int s_n, s_pieces, s_count[3];
   __shared__ float red[2 * kWarps];
   __shared__ uint32_t hist[256];
   __shared__ uint64_t s_cut;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   const RowSlice<T> S(static_cast<const T*>(A.z) + row * A.ld_z, A.V, rank, P.per);
   const int K = A.K, cap = P.cap;
   if (tid == 0) s_n = s_pieces = 0;
-  if (P.C > 1) cluster_arrive_release();  // everyone runs before anyone writes to the first CTA
+  if (P.C > 1) cluster_arrive_relaxed();  // everyone runs before anyone writes to the first CTA
 
   // ---- a bound from the sample; -inf where the slice is kept whole
   float bound = -INFINITY, start = -INFINITY;  // `start`: a first maximum for the sums
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     float x[PS * G];
     // The sample's place whose logit is the bound.
     const float q = (float)K * ((float)kSample / (float)(S.pieces * G));
-    const int want = (int)ceilf(q + 3.5f * sqrtf(q) + 3.f);
+    const int want = (int)ceilf(q + 4.5f * sqrtf(q) + 4.f);
     // Each warp takes PS runs of 32 pieces, spread evenly over the slice (there are
     // more than 32, and in short slices the runs overlap).
 #pragma unroll
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       red[warp] = hi;
       red[kWarps + warp] = lo;
     }
-    if (tid < 2) s_count[tid] = 0;
+    if (tid < 3) s_count[tid] = 0;
     __syncthreads();
     hi = red[0];
     lo = red[kWarps];
@@ -126,14 +127,13 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < PS * G; ++i) n += x[i] >= mid ? 1 : 0;
         n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) atomicAdd(&s_count[it & 1], n);
+        if (lane == 0) atomicAdd(&s_count[it % 3], n);
         __syncthreads();
-        n = s_count[it & 1];
-        if (tid == 0) s_count[(it & 1) ^ 1] = 0;
-        __syncthreads();
+        n = s_count[it % 3];
+        if (tid == 0) s_count[(it + 2) % 3] = 0;  // read before this barrier, used after the next
         if (n >= want) lo = mid;
         else hi = mid;
-        if (n >= want && n <= want + want / 4) break;
+        if (n >= want && n <= want + want / 3) break;
       }
     }
     bound = lo;
@@ -145,19 +145,21 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   // reaches the bound.  (Few do, and the elements of those are looked at afterwards: the
   // loop is a subtraction, a product, an exponential and a sum to an element, and half a
   // maximum.)
-  uint32_t* const listed = reinterpret_cast<uint32_t*>(keys + cap + (P.C > 1 ? kMerge : 0));
+  uint4* const listed = reinterpret_cast<uint4*>(keys + cap + (P.C > 1 ? kMerge : 0));
+  uint32_t* const listed_at = reinterpret_cast<uint32_t*>(listed + kHeld);
   float m = start, limit = start + P.far, l = 0.f;
   uint64_t sum = 0;  // two sums side by side
   const bool all = bound == -INFINITY;
   const float least = all ? -FLT_MAX : bound;  // (-inf is never taken)
-  auto take = [&](int q, const float (&x)[G]) {
+  auto take = [&](int q, const float (&x)[G], const uint4& raw) {
     float top = max3_nan(x[0], x[1], x[2]);
 #pragma unroll
     for (int e = 3; e < G; e += 2) top = e + 1 < G ? max3_nan(top, x[e], x[e + 1]) : max_nan(top, x[e]);
     // (NaN, too, is not below the bound.)
     if (!(top < least)) {
       const int at = atomicAdd(&s_pieces, 1);
-      if (at < cap) listed[at] = (uint32_t)q;
+      if (at < cap) listed_at[at] = (uint32_t)q;
+      if (at < kHeld) listed[at] = raw;
       if (top > limit || m == -INFINITY) {  // the sum's reference is too low, or none yet
         float s0, s1;
         unpack_f32x2(sum, s0, s1);
@@ -183,28 +185,48 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     const int last = S.pieces > 0 && !S.whole(S.pieces - 1) ? S.pieces - 1 : S.pieces;
     const uint4* const src = reinterpret_cast<const uint4*>(S.row + S.index(0));
     int q = first + tid;
-    for (; q + (U - 1) * kThreads < last; q += U * kThreads) {
-      uint4 raw[U];
+    if (q + (U - 1) * kThreads < last) {
+      uint4 raw[U], then[U];  // the next pieces are on their way
 #pragma unroll
       for (int u = 0; u < U; ++u) raw[u] = __ldg(src + q + u * kThreads);
+      while (true) {
+        const bool more = q + (2 * U - 1) * kThreads < last;
+        if (more) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[G];
-        unpack_piece(raw[u], x);
-        take(q + u * kThreads, x);
+          for (int u = 0; u < U; ++u) then[u] = __ldg(src + q + (U + u) * kThreads);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[G];
+          unpack_piece(raw[u], x);
+          take(q + u * kThreads, x, raw[u]);
+        }
+        q += U * kThreads;
+        if (!more) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = then[u];
       }
     }
     for (; q < last; q += kThreads) {
       float x[G];
-      unpack_piece(__ldg(src + q), x);
-      take(q, x);
+      const uint4 raw = __ldg(src + q);
+      unpack_piece(raw, x);
+      take(q, x, raw);
     }
     if (tid < 2 && S.pieces > 0) {
       const int edge = tid == 0 ? 0 : S.pieces - 1;
       if (!S.whole(edge) && (tid == 0 || S.pieces > 1)) {
+        // (As the type's own bits again, which -inf outside the row has too.)
         float x[G];
         S.edge(edge, x);
-        take(edge, x);
+        uint4 raw;
+        if constexpr (G == 4)
+          raw = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                           __float_as_uint(x[3]));
+        else
+          raw = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                           pack_bf16(x[6], x[7]));
+        take(edge, x, raw);
       }
     }
     float s0, s1;
@@ -224,9 +246,10 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   const int n_pieces = s_pieces;
   if (n_pieces <= cap) {
     for (int i = tid; i < n_pieces; i += kThreads) {
-      const int q = (int)listed[i];
+      const int q = (int)listed_at[i];
       float x[G];
-      if (S.whole(q)) unpack_piece(S.load(q), x);
+      if (i < kHeld) unpack_piece(listed[i], x);
+      else if (S.whole(q)) unpack_piece(S.load(q), x);
       else S.edge(q, x);
 #pragma unroll
       for (int e = 0; e < G; ++e) {
@@ -312,11 +335,56 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     n = min(s_n, cap);
   }
 
+  // ---- fewer of them, by halving their range of logits: a quarter more than K are enough
+  constexpr int kEach = 8;
+  if (n > 128 && n > K + K / 2 && n <= kEach * kThreads) {
+    uint64_t key[kEach];
+    uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      key[j] = tid + j * kThreads < n ? keys[tid + j * kThreads] : 0;
+      if (key[j]) lo = min(lo, (uint32_t)(key[j] >> 32));
+      hi = max(hi, (uint32_t)(key[j] >> 32));
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      hist[warp] = lo;
+      hist[kWarps + warp] = hi;
+    }
+    if (tid < 3) s_count[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      lo = min(lo, hist[w]);
+      hi = max(hi, hist[kWarps + w]);
+    }
+    for (int it = 0; it < 12 && hi - lo > 1; ++it) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      int above_mid = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) above_mid += (uint32_t)(key[j] >> 32) >= mid ? 1 : 0;
+      above_mid = __reduce_add_sync(0xffffffffu, above_mid);
+      if (lane == 0) atomicAdd(&s_count[it % 3], above_mid);
+      __syncthreads();
+      above_mid = s_count[it % 3];
+      if (tid == 0) s_count[(it + 2) % 3] = 0;
+      if (above_mid >= K) lo = mid;
+      else hi = mid;
+      if (above_mid >= K && above_mid <= K + K / 4) break;
+    }
+    __syncthreads();
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if ((uint32_t)(key[j] >> 32) >= lo && key[j]) keys[atomicAdd(&s_n, 1)] = key[j];
+    __syncthreads();
+    n = s_n;
+  }
+
   // ---- in order
-  int size = next_power(max(n, 1));
-  for (int i = n + tid; i < size; i += kThreads) keys[i] = 0;
-  __syncthreads();
-  sort_keys<kThreads>(keys, size);
+  sort_top<kThreads>(keys, n, K);
   n = min(n, K);
 
   m = red[0];
@@ -329,8 +397,15 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     for (int w = 0; w < kWarps; ++w)
       l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * ex2((red[w] - base) * P.c);
   }
-  const uint64_t* top = keys;
-  if (P.C > 1) {
+  auto give = [&](int place, uint64_t key) {
+    A.values[row * K + place] = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
+    A.indices[row * K + place] = key ? key_index(key) : -1;
+  };
+  if (P.C == 1) {
+    for (int i = tid; i < K; i += kThreads) give(i, i < n ? keys[i] : 0ull);
+  } else {
+    // Every slice's first K to the row's first CTA, where a key's place is the sum of its
+    // places among the slices.
     uint64_t* const all_keys = keys + cap;
     if (tid == 0) {
       s_m = m;
@@ -338,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     }
     cluster_wait_acquire();
     for (int i = tid; i < K; i += kThreads) st_cluster(all_keys + rank * K + i, 0, i < n ? keys[i] : 0ull);
+    if (rank == 0)
+      for (int i = tid; i < K; i += kThreads) give(i, 0ull);  // where the row has fewer
     cluster_sync();
     if (rank == 0) {
       float om = -INFINITY, ol = 0.f;
@@ -349,21 +426,22 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       const float base = m == -INFINITY ? 0.f : m;
       l = warp_sum(ol == 0.f ? 0.f : ol * ex2((om - base) * P.c));
     }
-    cluster_arrive_release();
+    __syncwarp();
+    cluster_arrive_relaxed();
     if (rank == 0) {
-      size = next_power(P.C * K);
-      for (int i = P.C * K + tid; i < size; i += kThreads) all_keys[i] = 0;
-      __syncthreads();
-      sort_keys<kThreads>(all_keys, size);
-      top = all_keys;
+      for (int i = tid; i < P.C * K; i += kThreads) {
+        const uint64_t key = all_keys[i];
+        if (!key) continue;
+        const int own = i / K;
+        int place = i - own * K;
+        for (int c = 0; c < P.C && place < K; ++c)
+          if (c != own) place += above<11>(all_keys + c * K, K, key);
+        if (place < K) give(place, key);
+      }
     }
-    cluster_wait_acquire();
+    __syncwarp();
+    cluster_wait_acquire();  // nobody leaves while its sum is read
     if (rank != 0) return;
-  }
-  for (int i = tid; i < K; i += kThreads) {
-    const uint64_t key = P.C > 1 || i < n ? top[i] : 0ull;
-    A.values[row * K + i] = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
-    A.indices[row * K + i] = key ? key_index(key) : -1;
   }
   // (A row without logits: log 0.)
   if (A.lse && tid == 0) A.lse[row] = l == 0.f ? -INFINITY : fmaf(m, P.inv_tau, logf(l));
@@ -387,7 +465,7 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   P.C = C;
   P.per = (int)slice_pieces(a.V, size, C);
   P.cap = a.K <= 512 ? 2048 : 4096;
-  const int smem = P.cap * 12 + (C > 1 ? kMerge * 8 : 0);
+  const int smem = P.cap * 12 + kHeld * 16 + (C > 1 ? kMerge * 8 : 0);
   prof_before(s, STT_KERNEL_TOP_LOGITS);
   const cudaError_t e =
       a.bf16 ? launch_rows(top_logits_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
