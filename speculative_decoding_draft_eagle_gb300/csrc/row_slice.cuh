@@ -250,7 +250,7 @@ __device__ __forceinline__ void sort_runs(uint64_t* a, int n, int K) {
   int place[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) place[e] = lane + 32 * e;
-  for (int r = 0; r * kRun < n; ++r) {
+  for (int r = 0; r * kRun < n && first < n; ++r) {
     if (r == warp) continue;
 #pragma unroll
     for (int e = 0; e < E; ++e)

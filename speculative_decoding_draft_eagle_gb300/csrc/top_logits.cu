@@ -32,7 +32,7 @@ constexpr int kMerge = 2048;            // keys that the first CTA of a row sort
 struct Params {
   TopLogitsArgs a;
   float c;            // log2(e) / tau
-  float inv_tau, far; // 1 / tau; the difference of logits whose ratio is 2^64
+  float far;          // the difference of logits whose ratio is 2^64
   int C, per;         // CTAs of a row, pieces of a CTA
   int cap;            // keys kept, and pieces listed
 };
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       hi = fmaxf(hi, x[i]);
       if (x[i] > -INFINITY) lo = fminf(lo, x[i]);
     }
+    const float mine = hi;
     hi = warp_max(hi);
     lo = warp_min(lo);
     if (lane == 0) {
@@ -114,8 +115,10 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       lo = fminf(lo, red[kWarps + w]);
     }
     start = hi;
-    // Halving until a quarter more than wanted reach it at most.  `lo` is reached by
-    // enough, or is the smallest of all.
+    // Halving until a third more than wanted reach it at most.  `lo` is reached by enough, or
+    // is the smallest of all.  (Few wanted ones are hardly ever in one thread's 16: then its
+    // largest stands for them, and a step is a barrier that counts.)
+    const bool few = want <= kThreads / 4;
     if (hi > lo) {
       for (int it = 0; it < 18; ++it) {
         // Halfway between them, or between their places among the floats where they are
@@ -124,13 +127,17 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
         const float mid = hi - lo < 1024.f ? lo + 0.5f * (hi - lo)
                                            : logit_of(below + (order_of(hi) - below) / 2);
         int n = 0;
+        if (few) {
+          n = __syncthreads_count(mine >= mid);
+        } else {
 #pragma unroll
-        for (int i = 0; i < PS * G; ++i) n += x[i] >= mid ? 1 : 0;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) atomicAdd(&s_count[it % 3], n);
-        __syncthreads();
-        n = s_count[it % 3];
-        if (tid == 0) s_count[(it + 2) % 3] = 0;  // read before this barrier, used after the next
+          for (int i = 0; i < PS * G; ++i) n += x[i] >= mid ? 1 : 0;
+          n = __reduce_add_sync(0xffffffffu, n);
+          if (lane == 0) atomicAdd(&s_count[it % 3], n);
+          __syncthreads();
+          n = s_count[it % 3];
+          if (tid == 0) s_count[(it + 2) % 3] = 0;  // read before this barrier, used after the next
+        }
         if (n >= want) lo = mid;
         else hi = mid;
         if (n >= want && n <= want + want / 3) break;
@@ -147,8 +154,17 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   // maximum.)
   uint4* const listed = reinterpret_cast<uint4*>(keys + cap + (P.C > 1 ? kMerge : 0));
   uint32_t* const listed_at = reinterpret_cast<uint32_t*>(listed + kHeld);
-  float m = start, limit = start + P.far, l = 0.f;
+  // The reference of the sums, as an exponent of 2: 2^(z c - m) takes one product-and-sum.
+  // (Within a range that leaves room to the float's; see the end for logits beyond.)
+  auto exponent = [&](float z) { return fminf(fmaxf(z * P.c, -1e38f), 1e38f); };
+  float m = -INFINITY, limit = -INFINITY, l = 0.f;  // none yet
+  if (fabsf(start) < INFINITY) {
+    m = exponent(start);
+    limit = start + P.far;
+  }
+  uint64_t low = f32x2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
   uint64_t sum = 0;  // two sums side by side
+  const uint64_t cc = f32x2(P.c, P.c);
   const bool all = bound == -INFINITY;
   const float least = all ? -FLT_MAX : bound;  // (-inf is never taken)
   auto take = [&](int q, const float (&x)[G], const uint4& raw) {
@@ -160,21 +176,21 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       const int at = atomicAdd(&s_pieces, 1);
       if (at < cap) listed_at[at] = (uint32_t)q;
       if (at < kHeld) listed[at] = raw;
-      if (top > limit || m == -INFINITY) {  // the sum's reference is too low, or none yet
+      if (top > limit) {  // the reference is too low, or there is none yet
+        const float to = exponent(top);
         float s0, s1;
         unpack_f32x2(sum, s0, s1);
-        const float f = m == -INFINITY ? 0.f : ex2((m - top) * P.c);
-        sum = f32x2(m == -INFINITY ? 0.f : s0 * f, m == -INFINITY ? 0.f : s1 * f);
-        if (top > -INFINITY) m = top;
-        limit = m + P.far;
+        const float f = m == -INFINITY ? 0.f : ex2(m - to);
+        sum = f32x2(s0 == 0.f ? 0.f : s0 * f, s1 == 0.f ? 0.f : s1 * f);
+        m = to;
+        low = f32x2(-m, -m);
+        limit = top + P.far;
       }
     }
-    const float base = m == -INFINITY ? 0.f : m;
-    const uint64_t low = f32x2(-base, -base), cc = f32x2(P.c, P.c);
 #pragma unroll
     for (int e = 0; e < G; e += 2) {
       float y0, y1;
-      unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[e], x[e + 1]), low), cc), y0, y1);
+      unpack_f32x2(fma_f32x2(f32x2(x[e], x[e + 1]), cc, low), y0, y1);
       sum = add_f32x2(sum, f32x2(ex2(y0), ex2(y1)));
     }
   };
@@ -189,22 +205,29 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       uint4 raw[U], then[U];  // the next pieces are on their way
 #pragma unroll
       for (int u = 0; u < U; ++u) raw[u] = __ldg(src + q + u * kThreads);
-      while (true) {
-        const bool more = q + (2 * U - 1) * kThreads < last;
-        if (more) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) then[u] = __ldg(src + q + (U + u) * kThreads);
-        }
+      auto use = [&](const uint4 (&r)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float x[G];
-          unpack_piece(raw[u], x);
-          take(q + u * kThreads, x, raw[u]);
+          unpack_piece(r[u], x);
+          take(q + u * kThreads, x, r[u]);
         }
         q += U * kThreads;
-        if (!more) break;
+      };
+      // True if there was another group, which is then in r once its loads are done.
+      auto fetch = [&](uint4 (&r)[U]) {
+        if (q + (2 * U - 1) * kThreads >= last) return false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = then[u];
+        for (int u = 0; u < U; ++u) r[u] = __ldg(src + q + (U + u) * kThreads);
+        return true;
+      };
+      while (true) {
+        bool more = fetch(then);
+        use(raw);
+        if (!more) break;
+        more = fetch(raw);
+        use(then);
+        if (!more) break;
       }
     }
     for (; q < last; q += kThreads) {
@@ -234,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     l = s0 + s1;
   }
   {
-    const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
-    l = warp_sum(l == 0.f ? 0.f : l * ex2((m - base) * P.c));
+    const float top = warp_max(m);
+    l = warp_sum(l == 0.f ? 0.f : l * (m == top ? 1.f : ex2(m - top)));
     if (lane == 0) {
       red[warp] = top;
       red[kWarps + warp] = l;
@@ -245,18 +268,38 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   // ---- the elements of the listed pieces
   const int n_pieces = s_pieces;
   if (n_pieces <= cap) {
-    for (int i = tid; i < n_pieces; i += kThreads) {
-      const int q = (int)listed_at[i];
+    for (int i0 = warp * 32; i0 < n_pieces; i0 += kThreads) {
+      const int i = i0 + lane;
       float x[G];
-      if (i < kHeld) unpack_piece(listed[i], x);
-      else if (S.whole(q)) unpack_piece(S.load(q), x);
-      else S.edge(q, x);
+      int q = 0;
+      uint32_t in = 0;
+      if (i < n_pieces) {
+        q = (int)listed_at[i];
+        if (i < kHeld) unpack_piece(listed[i], x);
+        else if (S.whole(q)) unpack_piece(S.load(q), x);
+        else S.edge(q, x);
 #pragma unroll
-      for (int e = 0; e < G; ++e) {
-        if (!(x[e] < least)) {
-          const int at = atomicAdd(&s_n, 1);
-          if (at < cap) keys[at] = place_key(x[e], S.index(q) + e);
-        }
+        for (int e = 0; e < G; ++e) in |= x[e] < least ? 0u : 1u << e;
+      }
+      // A warp's keys side by side.
+      int at = __popc(in);
+      const int mine = at;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += t;
+      }
+      int base = 0;
+      if (lane == 31) base = atomicAdd(&s_n, at);
+      at += __shfl_sync(0xffffffffu, base, 31) - mine;
+      while (in) {
+        const int e = __ffs((int)in) - 1;
+        in &= in - 1;
+        float y = x[0];
+#pragma unroll
+        for (int i = 1; i < G; ++i) y = e == i ? x[i] : y;
+        if (at < cap) keys[at] = place_key(y, S.index(q) + e);
+        ++at;
       }
     }
   }
@@ -392,10 +435,9 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   for (int w = 1; w < kWarps; ++w) m = fmaxf(m, red[w]);
   l = 0.f;
   {
-    const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * ex2((red[w] - base) * P.c);
+      l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * (red[w] == m ? 1.f : ex2(red[w] - m));
   }
   auto give = [&](int place, uint64_t key) {
     A.values[row * K + place] = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
@@ -423,8 +465,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
         ol = ld_cluster(&s_l, lane);
       }
       m = warp_max(om);
-      const float base = m == -INFINITY ? 0.f : m;
-      l = warp_sum(ol == 0.f ? 0.f : ol * ex2((om - base) * P.c));
+      l = warp_sum(ol == 0.f ? 0.f : ol * (om == m ? 1.f : ex2(om - m)));
     }
     __syncwarp();
     cluster_arrive_relaxed();
@@ -443,8 +484,17 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     cluster_wait_acquire();  // nobody leaves while its sum is read
     if (rank != 0) return;
   }
-  // (A row without logits: log 0.)
-  if (A.lse && tid == 0) A.lse[row] = l == 0.f ? -INFINITY : fmaf(m, P.inv_tau, logf(l));
+  if (A.lse && tid == 0) {
+    float lse = fmaf(m, kLn2, logf(l));
+    if (l == 0.f || l == INFINITY) {
+      // No logit; or the largest is so far from 0 that it alone is left after rounding.
+      uint64_t key = P.C == 1 ? (n > 0 ? keys[0] : 0) : 0;
+      for (int c = 0; c < P.C && P.C > 1; ++c) key = max(key, keys[cap + c * K]);
+      const float z = logit_of((uint32_t)(key >> 32));
+      lse = !key ? -INFINITY : z < INFINITY ? __fdiv_rn(z, A.temperature) : NAN;
+    }
+    A.lse[row] = lse;
+  }
 }
 
 }  // namespace
@@ -454,7 +504,6 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   Params P{};
   P.a = a;
   P.c = (float)(1.4426950408889634 / (double)a.temperature);
-  P.inv_tau = 1.f / a.temperature;
   P.far = 64.f / P.c;
   // CTAs of a row: one while the rows fill the GPU, more for few rows, or for rows so
   // long that the sample says little; as many as the first one can merge.

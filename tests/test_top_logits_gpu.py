@@ -147,3 +147,18 @@ def test_far_rows():
     v, i, _ = ops.stt_top_logits(rows, 20)
     V_, I_, _ = ot.top(f64(z), 20)
     assert np.array_equal(i.cpu().numpy(), I_) and np.array_equal(f64(v), V_)
+
+
+@pytest.mark.parametrize("V", [50, 20011])
+def test_lse_of_logits_far_from_zero(V):
+    """A row of the type's lowest value alone, or of values that near its limits: the sum of
+    such a row is its largest logit to within rounding (one division and half a step)."""
+    low = torch.finfo(torch.float32).min
+    z = torch.full((4, V), low)
+    z[1, V // 2] = -1e38
+    z[2, 3] = 3e38
+    z[3, V - 1] = 2.5e38
+    for tau in (1.0, 1.6):
+        _, _, lse = ops.stt_top_logits(z.to(DEV), 5, tau)
+        want = f64(z).max(1) / tau
+        assert np.abs(f64(lse) / want - 1).max() <= 2.0 ** -22
