@@ -8,6 +8,7 @@
 // piece goes element by element, with -inf for what is not the row's.
 #pragma once
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -314,14 +315,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Launches `kern` with C CTAs of a row to a cluster, raising its limits first.
+// Devices (the first 64) on which a kernel's limits have been raised, one for each kernel.
+using Raised = std::atomic<uint64_t>;
+
+// Launches `kern` with C CTAs of a row to a cluster; raises its limits first, to all that a
+// device has, once on each.
 template <class P>
 inline cudaError_t launch_rows(void (*kern)(const P), const P& p, int64_t rows, int C, int threads,
-                               int smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && C > 8)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                               int smem, Raised& raised, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    cudaFuncAttributes fa;
+    int most = 0;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               most - (int)fa.sharedSizeBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (rows * C > 0x7fffffffll) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C), 1, 1);

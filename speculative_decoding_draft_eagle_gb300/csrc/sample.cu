@@ -699,10 +699,10 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   P.a = a;
   for (int j = 0; j < 32; ++j)  // (exact in a double, but for its last bits)
     P.table[j] = j == 0 ? 1ull << 63 : (uint64_t)std::ldexp(std::exp2(-j / 32.0), 63);
+  // CTAs of a row: as few as leave room for two on an SM; more while all rows run at once.
   int C = (int)((a.V * (int64_t)size + kSliceBytes - 1) / kSliceBytes);
   C = std::max(1, std::min(C, kRowMaxCtas));
-  while (C < kRowMaxCtas && a.N * 2 * C <= sm_count() && slice_pieces(a.V, size, C) >= 2 * kThreads) C *= 2;
-  C = std::min(C, kRowMaxCtas);
+  while (C < kRowMaxCtas && a.N * (C + 1) <= 2 * sm_count() && slice_pieces(a.V, size, C + 1) >= 2 * kThreads) ++C;
   P.C = C;
   P.per = (int)slice_pieces(a.V, size, C);
   const int round = 512;
@@ -710,8 +710,10 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   P.runs = ((P.per + 31) / 32 + kWarps - 1) / kWarps;
   const int smem = P.per * 16 + kBins * 8 + kList * 8 + kWarps * P.runs * 8;
   prof_before(s, STT_KERNEL_SAMPLE);
-  const cudaError_t e = a.bf16 ? launch_rows(sample_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
-                               : launch_rows(sample_kernel<float>, P, a.N, C, kThreads, smem, s);
+  static Raised raised[2];
+  const cudaError_t e =
+      a.bf16 ? launch_rows(sample_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, raised[1], s)
+             : launch_rows(sample_kernel<float>, P, a.N, C, kThreads, smem, raised[0], s);
   prof_after(s);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -377,9 +377,10 @@ cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s) {
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
   const int smem = P.per * 16 + (P.per * (16 / size) + 31) / 32 * 4 + a.K * 8;
   prof_before(s, STT_KERNEL_SOFT_CE_TOPK);
+  static Raised raised[2];
   cudaError_t e = a.N == 0 ? cudaSuccess
-                  : a.bf16 ? launch_rows(soft_ce_topk_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
-                           : launch_rows(soft_ce_topk_kernel<float>, P, a.N, C, kThreads, smem, s);
+                  : a.bf16 ? launch_rows(soft_ce_topk_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, raised[1], s)
+                           : launch_rows(soft_ce_topk_kernel<float>, P, a.N, C, kThreads, smem, raised[0], s);
   if (e == cudaSuccess) e = soft_ce_loss_sum_launch(a.wl, a.N, a.loss, s);
   prof_after(s);
   if (e != cudaSuccess) return e;

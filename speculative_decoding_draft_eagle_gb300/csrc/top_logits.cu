@@ -516,9 +516,10 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   P.cap = a.K <= 512 ? 2048 : 4096;
   const int smem = P.cap * 12 + kHeld * 16 + (C > 1 ? kMerge * 8 : 0);
   prof_before(s, STT_KERNEL_TOP_LOGITS);
+  static Raised raised[2];
   const cudaError_t e =
-      a.bf16 ? launch_rows(top_logits_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, s)
-             : launch_rows(top_logits_kernel<float>, P, a.N, C, kThreads, smem, s);
+      a.bf16 ? launch_rows(top_logits_kernel<__nv_bfloat16>, P, a.N, C, kThreads, smem, raised[1], s)
+             : launch_rows(top_logits_kernel<float>, P, a.N, C, kThreads, smem, raised[0], s);
   prof_after(s);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
