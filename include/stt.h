@@ -117,6 +117,9 @@ STT_API int stt_device_error(void* stream, uint32_t* word);
  *                              does not send the others its maximum and sum.
  *   STT_INJECT_PAGED_WITHHOLD_Q  the paged attention's producer never loads
  *                              queries, as the attention forward's.
+ *   STT_INJECT_CE_TOPK_WITHHOLD_PARTS  the first CTA of a row that several share
+ *                              does not send the others its part of the soft-CE against
+ *                              top logits.
  * 0 switches injection off.  Unknown bits return STT_ERR_INVALID_ARG.  The
  * setting is process-wide; it is meant for tests, never for production runs.
  */
@@ -125,6 +128,7 @@ STT_API int stt_debug_inject(uint32_t what);
 #define STT_INJECT_FWD_WITHHOLD_Q 0x1u
 #define STT_INJECT_LOGITS_WITHHOLD_PAIRS 0x2u
 #define STT_INJECT_PAGED_WITHHOLD_Q 0x4u
+#define STT_INJECT_CE_TOPK_WITHHOLD_PARTS 0x8u
 
 /* --------------------------------------------------------------------------
  * Sparse-tree attention, forward.

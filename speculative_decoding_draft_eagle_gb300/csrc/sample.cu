@@ -258,11 +258,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   const bool truncated = greedy || want_k || want_p || min_p > 0.f;
-  if (probs && truncated) {
-    // Most of the row; what is kept is written over it.
-    const float zero[G] = {};
-    for (int q = tid; q < S.pieces; q += kThreads) put(S.index(q), zero);
-  }
 
   // ---- the grid
   Grid grid;
@@ -444,12 +439,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       });
       cluster_sync();
       if (rank == 0) {
-        const int size = next_power(n);
-        for (int i = n + tid; i < size; i += kThreads) list[i] = 0;
-        __syncthreads();
-        sort_keys<kThreads>(list, size);
+        sort_top<kThreads>(list, n, n);
         // Running sums over the sorted tokens, a run of them to a thread.
-        const int each = (size + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
+        const int each = (n + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
         uint64_t mine = 0;
         auto e_of = [&](uint64_t key) {
           return (uint64_t)(grid.e32(grid.at(logit_of((uint32_t)(key >> 32)))) + (int)kBias);
@@ -668,6 +660,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const float p = ex2((float)a.bin * (-1.f / 32.f)) * fmaf((float)grid.e32(a), 0x1p-32f, 1.f) * inv;
       return a.bin < kBins ? p : 0.f;
     };
+    if (truncated) {  // most of the row; what is kept is written over it
+      const float zero[G] = {};
+      for (int q = tid; q < S.pieces; q += kThreads) put(S.index(q), zero);
+      __syncthreads();
+    }
     if (!dense) {
       for (int i = lane; i < n_kept; i += 32) {
         const int place = kept[i];

@@ -34,6 +34,7 @@ struct Params {
   SoftCeTopkArgs a;
   float inv_tau, c;   // 1 / tau, log2(e) / tau
   int C, per, chunk;  // CTAs of a row, pieces of a CTA, pieces of a copy
+  bool withhold;      // test hook: the first CTA of a row sends no part
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
       cluster_wait_acquire();
       if (warp == 0) {
         rows(has ? red[0][lane] : -INFINITY, has ? red[1][lane] : 0.f, has ? red[2][lane] : 0.f);
-        if (lane < P.C)
+        if (lane < P.C && !(P.withhold && rank == 0))
           st_async_f4(mapa_shared(smem_u32(&s_part[rank]), (uint32_t)lane), make_float4(m, l, d, 0.f),
                       mapa_shared(smem_u32(&bar_part), (uint32_t)lane));
         __syncwarp();
@@ -376,6 +377,7 @@ cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s) {
   const int round = 1024;  // four pieces of fp32 to a thread, or eight of bf16
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
   const int smem = P.per * 16 + (P.per * (16 / size) + 31) / 32 * 4 + a.K * 8;
+  P.withhold = (debug_inject() & STT_INJECT_CE_TOPK_WITHHOLD_PARTS) != 0;
   prof_before(s, STT_KERNEL_SOFT_CE_TOPK);
   static Raised raised[2];
   cudaError_t e = a.N == 0 ? cudaSuccess
