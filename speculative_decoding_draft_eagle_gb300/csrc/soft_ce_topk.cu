@@ -28,7 +28,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 8;
-constexpr int kSliceBytes = 40 * 1024;  // preferred bytes of a slice
+// Preferred bytes of a slice: three CTAs on an SM.  (8192 fp32 rows of 151936 / 4096 bf16 rows of
+// 128256: 24 KB 1470 / 463 us, 40 KB 1447 / 397, 56 KB 1507 / 372, 62 KB 1383 / 373, 72 KB
+// 1376 / 396, 76 KB, which is two on an SM, 1582 / 396.)
+constexpr int kSliceBytes = 62 * 1024;
 
 struct Params {
   SoftCeTopkArgs a;

@@ -470,9 +470,15 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
     __syncwarp();
     cluster_arrive_relaxed();
     if (rank == 0) {
+      // Of every slice's first K / C the last, the least of which has K keys at or above it:
+      // what is below is not among the row's (8 bf16 rows of 151936, K 128, 16 CTAs: 61 us
+      // without this).
+      const int share = (K + P.C - 1) / P.C;
+      uint64_t floor_key = ~0ull;
+      for (int c = 0; c < P.C; ++c) floor_key = min(floor_key, all_keys[c * K + share - 1]);
       for (int i = tid; i < P.C * K; i += kThreads) {
         const uint64_t key = all_keys[i];
-        if (!key) continue;
+        if (!key || key < floor_key) continue;
         const int own = i / K;
         int place = i - own * K;
         for (int c = 0; c < P.C && place < K; ++c)
@@ -505,12 +511,15 @@ cudaError_t top_logits_launch(const TopLogitsArgs& a, cudaStream_t s) {
   P.a = a;
   P.c = (float)(1.4426950408889634 / (double)a.temperature);
   P.far = 64.f / P.c;
-  // CTAs of a row: one while the rows fill the GPU, more for few rows, or for rows so
-  // long that the sample says little; as many as the first one can merge.
+  // CTAs of a row: one while the rows fill the GPU; more for few rows of more than 128 KB,
+  // or for rows so long that the sample says little; as many as the first one can merge.
+  // (Splitting from 16 KB on: 64 fp32 rows of 32000, K 8: 10.3 us, unsplit 10.1; one bf16 row
+  // of 151936: 13.1, unsplit 14.6, from 128 KB on 11.1; 8 of them, K 128: from 128 KB on
+  // 14.7, unsplit 19.8; 40 fp32 rows of 151936: 18.2, unsplit 27.2.)
   const int most = std::max(1, std::min(kRowMaxCtas, kMerge / a.K));
   int C = 1;
   while (2 * C <= most && slice_pieces(a.V, 1, C) * 16 > 262144) C *= 2;
-  while (2 * C <= most && a.N * 2 * C <= 2 * sm_count() && slice_pieces(a.V, size, C) >= 4 * kThreads) C *= 2;
+  while (2 * C <= most && a.N * 2 * C <= 2 * sm_count() && slice_pieces(a.V, size, C) >= 32 * kThreads) C *= 2;
   P.C = C;
   P.per = (int)slice_pieces(a.V, size, C);
   P.cap = a.K <= 512 ? 2048 : 4096;
