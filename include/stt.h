@@ -588,7 +588,7 @@ STT_API int stt_logits_process(const void* z, int64_t N, int64_t V, int rows,
  *           +inf does.
  *  N        rows, >= 0.   V  1..STT_ROW_MAX_V.   K  1..min(V, STT_TOP_MAX_K)
  *           (K > V is STT_ERR_INVALID_ARG).
- *  temperature  finite and > 0; of lse alone.
+ *  temperature  finite and at least 2^-126; of lse alone.
  *  values   fp32 [N, K]: logits as they are, -inf past the row's last.
  *  indices  int32 [N, K], -1 past the row's last.
  *  lse      fp32 [N] or NULL: log sum_v exp(z_v / temperature); -inf for a row
@@ -617,7 +617,7 @@ STT_API int stt_top_logits(const void* z, int64_t ld_z, int64_t N, int64_t V, in
  *  g        fp32 [N], as soft_ce_fwd_bwd_inplace: rows with g_r = 0 are not read,
  *           their gradient and row_loss are 0.
  *  N        rows, >= 0.   V  1..STT_ROW_MAX_V.   K  1..STT_TOP_MAX_K.
- *  temperature  finite and > 0.
+ *  temperature  finite and at least 2^-126.
  *  dz       the gradient, of z's type, rows ld_dz apart, OVERWRITTEN, rounded once.
  *           It may be z (with ld_dz = ld_z); otherwise it may not overlap z.
  *  row_loss fp32 [N] or NULL;  loss  fp32 scalar (device), summed in a fixed order.

@@ -3,6 +3,7 @@
 // allocates device memory or synchronises (except stt_device_error, which is
 // documented to synchronise its stream).
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -661,7 +662,8 @@ int stt_top_logits(const void* z, int64_t ld_z, int64_t N, int64_t V, int K, flo
     begin_call();
     if (flags & ~(uint32_t)STT_LOGITS_BF16) return STT_ERR_INVALID_ARG;
     if (N < 0 || V < 1 || K < 1 || K > V) return STT_ERR_INVALID_ARG;
-    if (!std::isfinite(temperature) || !(temperature > 0.f)) return STT_ERR_INVALID_ARG;
+    // (The factor 1 / temperature has to be finite, too.)
+    if (!std::isfinite(temperature) || !(temperature >= FLT_MIN)) return STT_ERR_INVALID_ARG;
     if (K > stt::kTopMaxK) return STT_ERR_UNSUPPORTED;
     const int st = check_logits(z, ld_z, N, V, flags);
     if (st != STT_OK || N == 0) return st;
@@ -693,7 +695,8 @@ int soft_ce_topk_fwd_bwd(const void* z, int64_t ld_z, const float* t_values,
     begin_call();
     if (flags & ~(uint32_t)STT_CE_BF16) return STT_ERR_INVALID_ARG;
     if (N < 0 || V < 1 || K < 1) return STT_ERR_INVALID_ARG;
-    if (!std::isfinite(temperature) || !(temperature > 0.f)) return STT_ERR_INVALID_ARG;
+    // (The factor 1 / temperature has to be finite, too.)
+    if (!std::isfinite(temperature) || !(temperature >= FLT_MIN)) return STT_ERR_INVALID_ARG;
     if (K > stt::kSoftCeTopkMaxK) return STT_ERR_UNSUPPORTED;
     static_assert(STT_CE_BF16 == STT_LOGITS_BF16, "one check of the logits");
     int st = check_logits(z, ld_z, N, V, flags);

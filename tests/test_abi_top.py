@@ -111,3 +111,11 @@ def test_columns_of_one_buffer_are_apart(cpu_ops):
     cpu_ops._apart(flat[:, 100:200], 250, flat[:, :100], 250, "dz")
     cpu_ops._apart(flat[:2, :100], 250, flat[2:, :100], 250, "dz")
     cpu_ops._apart(flat[:, :100], 250, flat[:, :100], 250, "dz")
+
+
+@pytest.mark.parametrize("t", [1e-40, 2.0 ** -127, 1e-50])
+def test_a_temperature_without_a_finite_factor(L, t):
+    """1 / temperature would be infinite, or times a logit of 0 not a number."""
+    assert L.stt_top_logits(GOOD, 100, 4, 100, 8, t, 0, GOOD, GOOD, GOOD, None) == -1
+    assert L.soft_ce_topk_fwd_bwd(GOOD, 100, GOOD, GOOD, GOOD, GOOD, 4, 100, 8, t, 0, 2 * GOOD, 100,
+                                  GOOD, GOOD, GOOD, 1 << 20, None) == -1

@@ -140,3 +140,42 @@ def test_a_thread_that_has_made_no_call_before():
     t.join()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got[0], want))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rows_further_apart_than_32_bits(bf16):
+    """The second row starts 2^31 elements after the first, of the logits, the gradient and
+    the probabilities: the bits are those of dense rows."""
+    N, V, K, ld = 2, 5003, 9, 1 << 31
+
+    def far(dtype):
+        return torch.empty(ld + V, dtype=dtype, device=DEV).as_strided((N, V), (ld, 1))
+    dense = logits(N, V, bf16).to(DEV)
+    z = far(dense.dtype)
+    z.copy_(dense)
+    top = ops.stt_top_logits(z, K)
+    assert all(torch.equal(a, b) for a, b in zip(top, ops.stt_top_logits(dense, K)))
+    g = torch.tensor([1.0, -0.5], device=DEV)
+    want = ops.soft_ce_topk_fwd_bwd(dense, *top[:2], g, top[2], dz=torch.empty_like(dense))
+    got = ops.soft_ce_topk_fwd_bwd(z, *top[:2], g, top[2], dz=far(dense.dtype))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    u, p = torch.tensor([0.3, 0.8], device=DEV), torch.full((N,), 0.9, device=DEV)
+    want = ops.stt_sample(dense, u, top_p=p, want_probs=True)
+    got = ops.stt_sample(z, u, top_p=p, probs=far(torch.float32))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("tau", [2.0 ** -126, 2.0 ** 120])
+def test_the_smallest_and_a_huge_temperature(tau):
+    """All of a row's weight on its first (or spread evenly), nothing infinite or undefined."""
+    N, V, K = 3, 3001, 5
+    z = (logits(N, V) / 16).to(DEV)  # below 1: a logit times 2^126 is finite
+    g = torch.zeros(N, device=DEV) + 2.0 ** -126
+    values, indices, lse = ops.stt_top_logits(z, K, tau)
+    top = z.max(1)
+    assert torch.equal(values[:, 0], top.values) and torch.equal(indices[:, 0], top.indices.int())
+    x = f64(z).max(1) / tau if tau < 1 else np.full(N, np.log(V))
+    # (An element's exponent, the quotient and the sum: 2^-22 of it in all, see lse_bound.)
+    assert (np.abs(f64(lse) - x) <= 2.0 ** -20 * np.abs(x)).all()
+    _, row_loss, dz = ops.soft_ce_topk_fwd_bwd(z, values, indices, g, None, tau, torch.empty_like(z))
+    assert bool(torch.isfinite(row_loss).all()) and bool(torch.isfinite(dz).all())
