@@ -103,6 +103,11 @@ __device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64
   }
   __syncthreads();
 }
+// Waits once more for a slice's copies, by a thread whose wait for one gave up, before its CTA
+// leaves: they may still be on their way.  (By one thread always: 2 % of a gradient's time.)
+__device__ __forceinline__ void settle_slice(uint64_t* bars, int n_chunks, uint32_t site) {
+  for (int c = 0; c < n_chunks; ++c) mbar_wait(&bars[c], 0, site);
+}
 
 // ------------------------------------------------------------------ order --
 // Larger logits first, the lower index first among equals: one whole number for a
@@ -124,66 +129,9 @@ __device__ __forceinline__ int key_index(uint64_t key) {
 }
 
 // Sorts n keys (a power of two) in shared memory, the largest first: a bitonic network.
-// Thread t holds keys t, t + kThreads, .. (E of them): steps between those stay in its
-// registers, steps within a warp go by shuffles, and only those between warps through
-// shared memory (9 of 45 for 512 keys and 256 threads).
-template <int kThreads, int E>
-__device__ __forceinline__ void sort_held(uint64_t* a, int n) {
-  const int tid = threadIdx.x;
-  uint64_t key[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) key[e] = tid + e * kThreads < n ? a[tid + e * kThreads] : 0;
-  for (int size = 2; size <= n; size *= 2) {
-    for (int step = size / 2; step > 0; step /= 2) {
-      if (step >= kThreads) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-#pragma unroll
-          for (int d = 1; d < E; d *= 2) {
-            if (step == d * kThreads && (e & d) == 0) {
-              const bool down = ((e * kThreads + tid) & size) == 0;
-              const uint64_t x = key[e], y = key[e | d];
-              if ((x < y) == down) {
-                key[e] = y;
-                key[e | d] = x;
-              }
-            }
-          }
-        }
-        continue;
-      }
-      uint64_t other[E];
-      if (step >= 32) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (tid + e * kThreads < n) a[tid + e * kThreads] = key[e];
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e) other[e] = tid + e * kThreads < n ? a[(tid + e * kThreads) ^ step] : 0;
-        __syncthreads();
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) other[e] = __shfl_xor_sync(0xffffffffu, key[e], step);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = tid + e * kThreads;
-        const bool larger = ((i & step) == 0) == ((i & size) == 0);
-        key[e] = (key[e] < other[e]) == larger ? other[e] : key[e];
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (tid + e * kThreads < n) a[tid + e * kThreads] = key[e];
-  __syncthreads();
-}
 // Ends with a __syncthreads().
 template <int kThreads>
 __device__ __forceinline__ void sort_keys(uint64_t* a, int n) {
-  if (n <= kThreads) return sort_held<kThreads, 1>(a, n);
-  if (n <= 2 * kThreads) return sort_held<kThreads, 2>(a, n);
-  if (n <= 4 * kThreads) return sort_held<kThreads, 4>(a, n);
   for (int size = 2; size <= n; size *= 2) {
     for (int step = size / 2; step > 0; step /= 2) {
       for (int t = threadIdx.x; t < n / 2; t += kThreads) {
@@ -265,18 +213,25 @@ __device__ __forceinline__ void sort_runs(uint64_t* a, int n, int K) {
   __syncthreads();
 }
 __device__ __forceinline__ int next_power(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
-// Sorts n different keys as far as the first K; there is room for the next power of two.
-template <int kThreads>
+// Sorts n <= kMost different keys as far as the first K; where kMost is above 4 kThreads there
+// is room for the next power of two.
+template <int kThreads, int kMost>
 __device__ __forceinline__ void sort_top(uint64_t* a, int n, int K) {
   if (n <= 2 * kThreads) return sort_runs<kThreads, 2>(a, n, K);
-  if (n <= 4 * kThreads) return sort_runs<kThreads, 4>(a, n, K);
-  const int size = next_power(n);
-  for (int i = n + (int)threadIdx.x; i < size; i += kThreads) a[i] = 0;
-  __syncthreads();
-  sort_keys<kThreads>(a, size);
+  if (kMost <= 4 * kThreads || n <= 4 * kThreads) return sort_runs<kThreads, 4>(a, n, K);
+  if constexpr (kMost > 4 * kThreads) {
+    const int size = next_power(n);
+    for (int i = n + (int)threadIdx.x; i < size; i += kThreads) a[i] = 0;
+    __syncthreads();
+    sort_keys<kThreads>(a, size);
+  }
 }
 
 // ------------------------------------------------- neighbours in a cluster --
+// Arrives without ordering any memory access: it does not wait for stores on their way.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
   cluster_arrive_release();

@@ -15,7 +15,7 @@
 // the logits and one write of the probabilities.  The cut is found in two steps.  A
 // histogram of the slice over 2048 bins of 1/32 octave of weight gives, summed over the
 // cluster, the bin where the cut lies; the bin's tokens, a few hundred in practice, are
-// then gathered from the cluster and sorted by every CTA.  (A bin that holds more, as
+// then gathered in the row's first CTA and sorted there.  (A bin that holds more, as
 // equal logits make it, is halved by key and counted over the slices instead.)
 //
 // Neighbours at the border of the kept weight differ by little, and so do a draw's, so
@@ -24,6 +24,14 @@
 // polynomial of degree 4 and is summed as a whole number of 2^-32.  A histogram's bin
 // holds the count and the sum of E in 64 bits, split over two words of shared memory.
 // A weight more than 2048 bins, about 2^-64, below the largest is taken as 0.
+//
+// 320 fp32 rows of 151936 by top-p, with probabilities: 286 us, against 58 at HBM's rate; 64
+// bf16 rows of 128256 with all cuts, tokens alone: 41 (2.4); 99 bf16 rows of 50257: 39 (4.4);
+// one fp32 row of 32000: 18 to 22, most of it the call's host path.  HBM is at 11 % of its
+// rate: bound by instructions (112 of a warp for 32 logits, half of the issue slots) and by
+// the row's CTAs waiting at barriers (a quarter of the stalls).  Left out after measuring: a
+// row to one CTA that reads its logits again from L2 (266 to 290 us for the first, but 50,
+// 60 and 23 on the others); threads' own lists of the kept (295).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -34,13 +42,13 @@
 namespace stt {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;  // (320 rows of 151936: 256 threads 335 us, 384 301, 512 294, 640 301)
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 8;
 constexpr int kOctaves = 64;
 constexpr uint32_t kBins = 32 * kOctaves;
 constexpr int kList = 2048;                // tokens of a bin that are sorted
-constexpr int kSliceBytes = 80 * 1024;     // preferred bytes of a slice
+constexpr int kSliceBytes = 80 * 1024;     // preferred bytes of a slice: two CTAs on an SM
 constexpr int kSegment = 8 * (int)kBins / 2 / kWarps;  // kept tokens that a warp lists, in the bins' memory
 constexpr int64_t kBias = 1ll << 26;       // keeps 2^32 E positive
 constexpr int kUnitShift = 42;             // a weight of 1 in whole numbers is 2^42
@@ -201,10 +209,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // ---- the row's largest logit
   float m = -INFINITY;
+  bool there = true;  // the slice's copies, or a wait gave up
+  const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   {
-    const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
     for (int c = 0; c < n_chunks; ++c) {
-      mbar_wait(&bars[c], 0, STT_DEVERR_SAMPLE_WAIT);
+      there &= mbar_wait(&bars[c], 0, STT_DEVERR_SAMPLE_WAIT);
       const int end = min(S.pieces, (c + 1) * P.chunk);
       for (int q = c * P.chunk + tid; q < end; q += kThreads) {
         float x[G];
@@ -253,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (A.tokens) A.tokens[row] = -1;
       if (A.logprobs) A.logprobs[row] = m == -INFINITY ? -INFINITY : NAN;
     }
+    if (!there) settle_slice(bars, n_chunks, STT_DEVERR_SAMPLE_WAIT);
     cluster_sync();  // nobody leaves while its maximum is read
     return;
   }
@@ -439,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       });
       cluster_sync();
       if (rank == 0) {
-        sort_top<kThreads>(list, n, n);
+        sort_top<kThreads, kList>(list, n, n);
         // Running sums over the sorted tokens, a run of them to a thread.
         const int each = (n + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
         uint64_t mine = 0;
@@ -684,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   }
+  if (!there) settle_slice(bars, n_chunks, STT_DEVERR_SAMPLE_WAIT);
   __syncwarp();
   cluster_wait_acquire();
 }
@@ -696,7 +707,9 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   P.a = a;
   for (int j = 0; j < 32; ++j)  // (exact in a double, but for its last bits)
     P.table[j] = j == 0 ? 1ull << 63 : (uint64_t)std::ldexp(std::exp2(-j / 32.0), 63);
-  // CTAs of a row: as few as leave room for two on an SM; more while all rows run at once.
+  // CTAs of a row: as few as leave room for two on an SM; more while all rows run at once,
+  // but none below 16 KB (99 bf16 rows of 50257 in two CTAs 42 us, in three 39; one row of
+  // 32000 in 15 CTAs 23 us, in seven 18).
   int C = (int)((a.V * (int64_t)size + kSliceBytes - 1) / kSliceBytes);
   C = std::max(1, std::min(C, kRowMaxCtas));
   while (C < kRowMaxCtas && a.N * (C + 1) <= 2 * sm_count() && slice_pieces(a.V, size, C + 1) >= 2 * kThreads) ++C;
