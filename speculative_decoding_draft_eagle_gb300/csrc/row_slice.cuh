@@ -103,10 +103,12 @@ __device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64
   }
   __syncthreads();
 }
-// Waits once more for a slice's copies, by a thread whose wait for one gave up, before its CTA
-// leaves: they may still be on their way.  (By one thread always: 2 % of a gradient's time.)
-__device__ __forceinline__ void settle_slice(uint64_t* bars, int n_chunks, uint32_t site) {
-  for (int c = 0; c < n_chunks; ++c) mbar_wait(&bars[c], 0, site);
+// Waits for a slice's c-th copies; where that gives up, once more for all of them, so that a
+// CTA does not leave while they are on their way.  (Here and not at its end, where it took 2 %
+// of a gradient's time.)
+__device__ __forceinline__ void wait_slice(uint64_t* bars, int c, int n_chunks, uint32_t site) {
+  if (!mbar_wait(&bars[c], 0, site))
+    for (int i = 0; i < n_chunks; ++i) mbar_wait(&bars[i], 0, site);
 }
 
 // ------------------------------------------------------------------ order --

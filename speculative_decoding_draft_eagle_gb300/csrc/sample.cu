@@ -26,7 +26,7 @@
 // A weight more than 2048 bins, about 2^-64, below the largest is taken as 0.
 //
 // 320 fp32 rows of 151936 by top-p, with probabilities: 286 us, against 58 at HBM's rate; 64
-// bf16 rows of 128256 with all cuts, tokens alone: 41 (2.4); 99 bf16 rows of 50257: 39 (4.4);
+// bf16 rows of 128256 with all cuts, tokens alone: 41 (2.4); 99 bf16 rows of 50257: 40 (4.4);
 // one fp32 row of 32000: 18 to 22, most of it the call's host path.  HBM is at 11 % of its
 // rate: bound by instructions (112 of a warp for 32 logits, half of the issue slots) and by
 // the row's CTAs waiting at barriers (a quarter of the stalls).  Left out after measuring: a
@@ -209,11 +209,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // ---- the row's largest logit
   float m = -INFINITY;
-  bool there = true;  // the slice's copies, or a wait gave up
   const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   {
     for (int c = 0; c < n_chunks; ++c) {
-      there &= mbar_wait(&bars[c], 0, STT_DEVERR_SAMPLE_WAIT);
+      wait_slice(bars, c, n_chunks, STT_DEVERR_SAMPLE_WAIT);
       const int end = min(S.pieces, (c + 1) * P.chunk);
       for (int q = c * P.chunk + tid; q < end; q += kThreads) {
         float x[G];
@@ -262,7 +261,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (A.tokens) A.tokens[row] = -1;
       if (A.logprobs) A.logprobs[row] = m == -INFINITY ? -INFINITY : NAN;
     }
-    if (!there) settle_slice(bars, n_chunks, STT_DEVERR_SAMPLE_WAIT);
     cluster_sync();  // nobody leaves while its maximum is read
     return;
   }
@@ -694,7 +692,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   }
-  if (!there) settle_slice(bars, n_chunks, STT_DEVERR_SAMPLE_WAIT);
   __syncwarp();
   cluster_wait_acquire();
 }
@@ -708,8 +705,8 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   for (int j = 0; j < 32; ++j)  // (exact in a double, but for its last bits)
     P.table[j] = j == 0 ? 1ull << 63 : (uint64_t)std::ldexp(std::exp2(-j / 32.0), 63);
   // CTAs of a row: as few as leave room for two on an SM; more while all rows run at once,
-  // but none below 16 KB (99 bf16 rows of 50257 in two CTAs 42 us, in three 39; one row of
-  // 32000 in 15 CTAs 23 us, in seven 18).
+  // but none below 16 KB (99 bf16 rows of 50257 in two CTAs 42.9 us, in three 41.5; one row of
+  // 32000 in 15 CTAs 23.0, in seven 18.6, all at the time).
   int C = (int)((a.V * (int64_t)size + kSliceBytes - 1) / kSliceBytes);
   C = std::max(1, std::min(C, kRowMaxCtas));
   while (C < kRowMaxCtas && a.N * (C + 1) <= 2 * sm_count() && slice_pieces(a.V, size, C + 1) >= 2 * kThreads) ++C;

@@ -214,10 +214,9 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   constexpr int U = 16 / G;  // pieces taken together
   const uint64_t cc = f32x2(P.c, P.c);
   float m = -INFINITY, l = 0.f;
-  bool there = true;  // the slice's copies, or a wait gave up
   const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   for (int c = 0; c < n_chunks; ++c) {
-    there &= mbar_wait(&bars[c], 0, STT_DEVERR_CE_WAIT);
+    wait_slice(bars, c, n_chunks, STT_DEVERR_CE_WAIT);
     const int end = min(S.pieces, (c + 1) * P.chunk);
     for (int q = c * P.chunk + tid; q < end; q += U * kThreads) {
       float x[U][G];
@@ -363,8 +362,6 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   }
   // A CTA whose wait gave up may not leave while parts are on their way to it: everyone has
   // sent theirs, and they have landed.
-  __syncwarp();
-  if (!there) settle_slice(bars, n_chunks, STT_DEVERR_CE_WAIT);
   __syncwarp();
   if (P.C > 1) {
     cluster_wait_acquire();
