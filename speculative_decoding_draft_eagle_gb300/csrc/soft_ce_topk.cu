@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const bool there = v[u] >= 0 && v[u] < A.V;
+          // (A logit of -inf is no entry, whatever L is: with an L of -inf, a teacher row without
+          // any, its exponent would be -inf + inf.)
+          const bool there = v[u] >= 0 && v[u] < A.V && t[u] != -INFINITY;
           v[u] = there ? v[u] : -1;
           t[u] = there ? t[u] * P.inv_tau : -INFINITY;
         }
