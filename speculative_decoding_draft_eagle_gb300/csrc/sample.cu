@@ -72,9 +72,11 @@ struct Grid {
   };
   __device__ __forceinline__ At at(float z) const {
     At a;
-    a.zz = z - m0;
-    a.p = a.zz * c;
-    a.ks = a.p + kMagic;
+    // (Each rounded by itself, never as one product-and-sum: all uses of a logit, and `top`,
+    // have to put it at the same place.)
+    a.zz = __fsub_rn(z, m0);
+    a.p = __fmul_rn(a.zz, c);
+    a.ks = __fadd_rn(a.p, kMagic);
     // (Products too far below for the grid, down to -inf, give smaller floats, or ones with a
     // sign: both are far from `top` as whole numbers, too.)
     a.bin = (uint32_t)(top - __float_as_int(a.ks));
@@ -82,7 +84,7 @@ struct Grid {
   }
   // 2^32 E of an element whose bin is below kBins.
   __device__ __forceinline__ int e32(const At& a) const {
-    const float r = (a.p - (a.ks - kMagic)) + fmaf(a.zz, c_lo, fmaf(a.zz, c, -a.p));
+    const float r = __fsub_rn(a.p, __fsub_rn(a.ks, kMagic)) + fmaf(a.zz, c_lo, fmaf(a.zz, c, -a.p));
     // 2^r - 1, times 2^32: (r ln 2)^n / n!, |r| <= 2^-6 and the product's low part.
     constexpr double s = 4294967296.0, l = 0.693147180559945309;
     constexpr float a1 = (float)(s * l), a2 = (float)(s * l * l / 2), a3 = (float)(s * l * l * l / 6),
@@ -270,12 +272,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the grid
   Grid grid;
   {
+    grid.top = 0;
     grid.c = s_c[0];
     grid.c_lo = s_c[1];
     // Where the products would leave the grid's range the maximum is taken off first: the
     // logits that matter are then within a 2^10th of it and the difference is exact.
     grid.m0 = fabsf(m) * grid.c < 65536.f ? 0.f : m;
-    grid.top = __float_as_int((m - grid.m0) * grid.c + kMagic);
+    grid.top = __float_as_int(grid.at(m).ks);
   }
 
   Cut cut{-INFINITY, INT_MAX};  // (the weight of -inf is 0)

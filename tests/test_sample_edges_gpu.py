@@ -1,0 +1,73 @@
+"""Truncated sampling where its arithmetic could go astray, against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from _serving import gen
+from _top import logits
+from speculative_decoding_draft_eagle_gb300 import ops
+from test_sample_gpu import _check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decoding_draft_eagle_gb300 import build
+    build.build()
+    yield
+    assert ops.stt_device_error() == 0
+
+
+def _on_a_border(T, lo, hi):
+    """Logits whose product with log2(e) / T, rounded, lies halfway between two places of the
+    grid of 1/32, while the exact product is on the other side than the one the tie goes to:
+    rounding once and rounding twice give different bins."""
+    c = np.float32(np.log2(np.e) / T)
+    x = np.arange(np.float32(lo).view(np.int32), np.float32(hi).view(np.int32), dtype=np.int32).view(np.float32)
+    exact = x.astype(np.float64) * np.float64(c)      # 48 bits
+    magic = np.float32(1.5 * 2 ** 18)
+    twice = exact.astype(np.float32) + magic
+    once = (exact + np.float64(magic)).astype(np.float32)
+    assert twice.dtype == np.float32
+    return x[twice < once], x[twice > once]
+
+
+@pytest.mark.parametrize("T", [1.0, 0.75])
+@pytest.mark.parametrize("kind", ["", "k", "p", "m"])
+def test_the_largest_logit_on_a_border(T, kind):
+    """The most likely token of each row is such a logit: it keeps its weight."""
+    for x in _on_a_border(T, 12.5, 12.9):
+        assert x.size >= 4
+        x = x[:: max(1, x.size // 16)]
+        n, V = x.size, 3001
+        z = logits(n, V).clamp(max=12.0)
+        z[torch.arange(n), torch.randint(0, V, (n,), generator=gen(1))] = torch.from_numpy(x)
+        s = dict(T=np.full(n, T))
+        if kind == "k":
+            s["k"] = 1 + np.arange(n) % 4 * 7 + 1
+        if kind == "p":
+            s["p"] = 0.2 + 0.75 * np.arange(n) / n
+        if kind == "m":
+            s["m"] = 0.001 * (1 + np.arange(n))
+        _check(z, **s)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.75])
+def test_logits_on_the_borders_of_the_cut(T):
+    """Such logits, and others of the bins on either side of theirs, around the cut: each of
+    them is kept or not by its place in the order alone."""
+    x = np.concatenate(_on_a_border(T, 5.0, 6.0))
+    assert x.size >= 8
+    x = x[:: max(1, x.size // 24)]
+    near = (x[:, None] + np.array([-0.03, -0.01, 0.0, 0.0, 0.01, 0.03], np.float32) * T).reshape(-1)
+    row = np.concatenate([[7.0], near, np.linspace(-2, 2, 50)]).astype(np.float32)
+    row = torch.from_numpy(row)[torch.randperm(row.size, generator=gen(2))]
+    n = near.size + 1
+    z = row.expand(n, -1).contiguous()
+    _check(z, T=np.full(n, T), k=1 + np.arange(n))
+    # Between two tokens of the row, a quarter of one past the one before.
+    w = np.sort(np.exp(row.numpy().astype(np.float64) / T))[::-1]
+    p = ((np.cumsum(w) - 0.75 * w) / w.sum())[:n].astype(np.float32)
+    _check(z, T=np.full(n, T), p=p)
