@@ -51,13 +51,13 @@ constexpr int kList = 2048;                // tokens of a bin that are sorted
 constexpr int kSliceBytes = 80 * 1024;     // preferred bytes of a slice: two CTAs on an SM
 constexpr int kSegment = 8 * (int)kBins / 2 / kWarps;  // kept tokens that a warp lists, in the bins' memory
 constexpr int64_t kBias = 1ll << 26;       // keeps 2^32 E positive
-constexpr int kUnitShift = 42;             // a weight of 1 in whole numbers is 2^42
+constexpr int kGroup = 4;                  // runs of 32 pieces whose kept weight a warp notes as one
 constexpr float kMagic = 393216.f;         // 1.5 2^18: floats there are 1/32 apart
 
 struct Params {
   SampleArgs a;
   int C, per, chunk;
-  int runs;            // runs of 32 pieces that a warp takes
+  int runs, groups;    // runs of 32 pieces that a warp takes, and groups of those
   uint64_t table[32];  // 2^(63 - j / 32)
 };
 
@@ -114,6 +114,45 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v) {  // inclusive
   }
   return v;
 }
+// A draw's weights are whole numbers of 2^-94 (of a token at its place on the grid that is as
+// probable as the first): all of a weight's 31 bits down to the last octave, and room for the
+// sum of 2^20.
+using Whole = unsigned __int128;
+__device__ __forceinline__ Whole warp_sum(Whole v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v += (Whole)__shfl_xor_sync(0xffffffffu, (uint64_t)(v >> 64), o) << 64 |
+         __shfl_xor_sync(0xffffffffu, (uint64_t)v, o);
+  return v;
+}
+__device__ __forceinline__ Whole warp_scan(Whole v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Whole t = (Whole)__shfl_up_sync(0xffffffffu, (uint64_t)(v >> 64), o) << 64 |
+                    __shfl_up_sync(0xffffffffu, (uint64_t)v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+__device__ __forceinline__ Whole from_lane(Whole v, int lane) {
+  return (Whole)__shfl_sync(0xffffffffu, (uint64_t)(v >> 64), lane) << 64 |
+         __shfl_sync(0xffffffffu, (uint64_t)v, lane);
+}
+struct Weight {
+  uint32_t w;  // in 2^-31 of the octave
+  uint32_t o;  // below 64
+  __device__ __forceinline__ Whole whole() const {
+    return (Whole)((uint64_t)(w >> 1) >> o) << 64 | (uint64_t)w << (63 - o);
+  }
+};
+// floor(u total) for 0 <= u < 1 and a total below 2^115: exceeded where u total is.
+__device__ __forceinline__ Whole share_of(Whole total, float u) {
+  const uint32_t bits = __float_as_uint(u), e = max(bits >> 23, 1u);
+  const uint32_t mant = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);  // u = mant 2^(e - 150)
+  const Whole t = (total >> 24) * mant + ((uint64_t)((uint32_t)total & 0xffffffu) * mant >> 24);
+  return t >> (126 - e);
+}
 // Ends with a __syncthreads().
 __device__ __forceinline__ uint64_t block_sum64(uint64_t v, uint64_t* s) {
   v = warp_sum64(v);
@@ -153,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __shared__ double s_log;               // T log(min_p)
   __shared__ uint64_t s_target;
   __shared__ int s_n;
-  __shared__ uint64_t s_total;
+  __shared__ __align__(16) uint64_t s_total[2];
+  __shared__ Whole s_part[kWarps];
   __shared__ uint64_t s_sum[2][2];  // of the halving steps: counts and sums, in turn
   struct Found {
     uint32_t bin;
@@ -177,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   uint32_t* const bin_lo = reinterpret_cast<uint32_t*>(smem + (size_t)P.per * 16);  // sums of 2^32 E
   uint32_t* const bin_n = bin_lo + kBins;  // counts, and in the upper half the sums' carries
   uint64_t* const list = reinterpret_cast<uint64_t*>(bin_n + kBins);
-  uint64_t* const run_sum = list + kList;  // [kWarps][P.runs]
+  Whole* const group_sum = reinterpret_cast<Whole*>(list + kList) + warp * P.groups;  // this warp's
   uint16_t* const kept = reinterpret_cast<uint16_t*>(bin_lo) + warp * kSegment;  // this warp's, places in the slice
 
   const float temp = A.temperature ? A.temperature[b] : 1.f;
@@ -507,14 +547,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // ---- the kept weights in whole numbers
-  auto weight = [&](float x) -> uint64_t {
+  auto weight = [&](float x) -> Weight {
     const auto a = grid.at(x);
-    if (a.bin >= kBins) return 0;
     const uint32_t t = (uint32_t)(s_tab[a.bin & 31] >> 32);
     const uint32_t w = t + (uint32_t)((int64_t)((uint64_t)t) * grid.e32(a) >> 32);
-    // w / 2^31 2^-octave, in units of 2^-42, rounded.
-    const uint64_t u = (uint64_t)w << (kUnitShift - 31 + 1) >> (a.bin >> 5);
-    return (u + 1) >> 1;
+    return a.bin < kBins ? Weight{w, a.bin >> 5} : Weight{0, 0};
   };
   // A warp takes its slice's pieces in order, as runs of 32, and lists what is kept of
   // them; where that is too much for its list, `dense`, it adds up run by run.
@@ -555,108 +592,105 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
   }
   __syncwarp();
-  uint64_t mine = 0;
-  if (!dense) {
-    for (int i = lane; i < n_kept; i += 32) mine += weight((float)zs[kept[i]]);
-    mine = warp_sum64(mine);
-  } else {
-    for (int q0 = q_begin; q0 < q_end; q0 += 32) {
-      const int q = q0 + lane, v = S.index(q);
-      uint64_t w = 0;
-      if (q < q_end) {
-        float x[G];
-        unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
+  // What is kept of the piece that this lane has of a run.
+  auto kept_of = [&](int q) -> Whole {
+    Whole w = 0;
+    if (q < q_end) {
+      float x[G];
+      unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
 #pragma unroll
-        for (int e = 0; e < G; ++e) {
-          const uint64_t t = weight(x[e]);  // (0 for -inf)
-          if (cut.keeps(x[e], v + e)) w += t;
-        }
+      for (int e = 0; e < G; ++e) {
+        const Whole t = weight(x[e]).whole();  // (0 for -inf)
+        if (cut.keeps(x[e], S.index(q) + e)) w += t;
       }
-      w = warp_sum64(w);
-      if (lane == 0) run_sum[warp * P.runs + (q0 - q_begin) / 32] = w;
+    }
+    return w;
+  };
+  Whole mine = 0;
+  if (!dense) {
+    for (int i = lane; i < n_kept; i += 32) mine += weight((float)zs[kept[i]]).whole();
+    mine = warp_sum(mine);
+  } else {
+    for (int g = 0; g < P.groups; ++g) {
+      Whole w = 0;
+      for (int r = 0; r < kGroup; ++r) w += kept_of(q_begin + (g * kGroup + r) * 32 + lane);
+      w = warp_sum(w);
+      if (lane == 0) group_sum[g] = w;
       mine += w;
     }
   }
-  if (lane == 0) s_red[warp] = mine;
+  if (lane == 0) s_part[warp] = mine;
   __syncthreads();
-  uint64_t slice = 0, slice_before = 0;  // the slice's, and what its warps before this one have
+  Whole slice = 0, slice_before = 0;  // the slice's, and what its warps before this one have
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) slice_before += s_red[w];
-    slice += s_red[w];
+    if (w < warp) slice_before += s_part[w];
+    slice += s_part[w];
   }
-  if (tid == 0) s_total = slice;
+  if (tid == 0) {
+    s_total[0] = (uint64_t)slice;
+    s_total[1] = (uint64_t)(slice >> 64);
+  }
   cluster_sync();
-  uint64_t total, before;
+  Whole total, before;
   {
-    const uint64_t o = lane < C ? ld_cluster(&s_total, lane) : 0;
-    const uint64_t run = warp_scan64(o);
-    total = __shfl_sync(0xffffffffu, run, 31);
-    before = __shfl_sync(0xffffffffu, run - o, rank) + slice_before;
+    Whole o = 0;
+    if (lane < C) o = (Whole)ld_cluster(&s_total[1], lane) << 64 | ld_cluster(&s_total[0], lane);
+    const Whole run = warp_scan(o);
+    total = from_lane(run, 31);
+    before = from_lane(run - o, rank) + slice_before;
   }
   cluster_arrive_release();  // done with the neighbours' shared memory; waited for at the end
+  const float total_f = (float)(uint64_t)(total >> 50);  // in 2^-44
 
   // ---- the token: its warp finds it
   if (A.u && before < total) {
-    uint64_t at = (uint64_t)fmax(0.0, (double)A.u[row] * (double)total);
-    at = min(at, total - 1);
-    auto drawn = [&](int v, uint64_t w) {
+    const float u = A.u[row];
+    Whole at = u >= 1.f ? total - 1 : u > 0.f ? share_of(total, u) : 0;
+    // (The logarithm of the weight's own bits, over the total's.)
+    auto drawn = [&](int v, const Weight& w) {
       if (A.tokens) A.tokens[row] = v;
-      if (A.logprobs) A.logprobs[row] = logf((float)w / (float)total);
+      if (A.logprobs) A.logprobs[row] = logf((float)w.w * __uint_as_float((127 + 13 - w.o) << 23) / total_f);
     };
     if (before <= at && at < before + mine) {
       at -= before;
       if (!dense) {
         for (int i0 = 0; i0 < n_kept; i0 += 32) {
           const int place = i0 + lane < n_kept ? kept[i0 + lane] : 0;
-          const uint64_t w = i0 + lane < n_kept ? weight((float)zs[place]) : 0;
-          const uint64_t run = warp_scan64(w);
-          if (run > at && run - w <= at) drawn(S.first + place, w);
-          const uint64_t all = __shfl_sync(0xffffffffu, run, 31);
+          const Weight of = i0 + lane < n_kept ? weight((float)zs[place]) : Weight{0, 0};
+          const Whole w = of.whole(), run = warp_scan(w);
+          if (run > at && run - w <= at) drawn(S.first + place, of);
+          const Whole all = from_lane(run, 31);
           if (all > at) break;
           at -= all;
         }
       } else {
-        // The run of pieces, then the lane's piece, then the element.
-        const int n = (q_end - q_begin + 31) / 32;
-        int q0 = q_begin;
-        for (int u0 = 0; u0 < n; u0 += 32) {
-          const uint64_t w = u0 + lane < n ? run_sum[warp * P.runs + u0 + lane] : 0;
-          const uint64_t run = warp_scan64(w);
-          const uint32_t over = __ballot_sync(0xffffffffu, run > at);
-          if (over) {
-            const int j = __ffs((int)over) - 1;
-            at -= __shfl_sync(0xffffffffu, run - w, j);
-            q0 = q_begin + (u0 + j) * 32;
-            break;
+        // The group of runs, then the run, the lane's piece, and the element.
+        int g = 0;
+        while (g + 1 < P.groups && group_sum[g] <= at) at -= group_sum[g++];
+        for (int q0 = q_begin + g * kGroup * 32; q0 < q_end; q0 += 32) {
+          const Whole w = kept_of(q0 + lane), run = warp_scan(w), all = from_lane(run, 31);
+          if (all <= at) {
+            at -= all;
+            continue;
           }
-          at -= __shfl_sync(0xffffffffu, run, 31);
-        }
-        const int q = q0 + lane, v = S.index(q);
-        float x[G];
-        uint64_t w[G], sum = 0;
+          if (run > at && run - w <= at) {
+            float x[G];
+            unpack_piece(*reinterpret_cast<const uint4*>(zs + (q0 + lane) * G), x);
+            const int v = S.index(q0 + lane);
+            Whole acc = run - w;
+            bool done = false;
 #pragma unroll
-        for (int e = 0; e < G; ++e) w[e] = 0;
-        if (q < q_end) {
-          unpack_piece(*reinterpret_cast<const uint4*>(zs + q * G), x);
-#pragma unroll
-          for (int e = 0; e < G; ++e) {
-            if (cut.keeps(x[e], v + e)) w[e] = weight(x[e]);
-            sum += w[e];
-          }
-        }
-        const uint64_t run = warp_scan64(sum);
-        if (run - sum <= at && at < run) {
-          uint64_t acc = run - sum;
-          bool done = false;
-#pragma unroll
-          for (int e = 0; e < G; ++e) {
-            acc += w[e];
-            if (!done && acc > at) {
-              done = true;
-              drawn(v + e, w[e]);
+            for (int e = 0; e < G; ++e) {
+              const Weight of = weight(x[e]);
+              if (cut.keeps(x[e], v + e)) acc += of.whole();
+              if (!done && acc > at) {
+                done = true;
+                drawn(v + e, of);
+              }
             }
           }
+          break;
         }
       }
     }
@@ -665,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the probabilities
   if (probs) {
     // 1 / total, for weights in units of the maximum's bin.
-    const float inv = 1.f / ((float)total * 0x1p-42f);
+    const float inv = 1.f / (total_f * 0x1p-44f);
     auto probability = [&](float x) {
       const auto a = grid.at(x);
       const float p = ex2((float)a.bin * (-1.f / 32.f)) * fmaf((float)grid.e32(a), 0x1p-32f, 1.f) * inv;
@@ -718,7 +752,8 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   const int round = 512;
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
   P.runs = ((P.per + 31) / 32 + kWarps - 1) / kWarps;
-  const int smem = P.per * 16 + kBins * 8 + kList * 8 + kWarps * P.runs * 8;
+  P.groups = (P.runs + kGroup - 1) / kGroup;
+  const int smem = P.per * 16 + kBins * 8 + kList * 8 + kWarps * P.groups * (int)sizeof(Whole);
   prof_before(s, STT_KERNEL_SAMPLE);
   static Raised raised[2];
   const cudaError_t e =

@@ -71,3 +71,32 @@ def test_logits_on_the_borders_of_the_cut(T):
     w = np.sort(np.exp(row.numpy().astype(np.float64) / T))[::-1]
     p = ((np.cumsum(w) - 0.75 * w) / w.sum())[:n].astype(np.float32)
     _check(z, T=np.full(n, T), p=p)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [700, 151936])
+@pytest.mark.parametrize("peak", ["first", "last"])
+@pytest.mark.parametrize("k", [0, 300])
+def test_tokens_far_less_likely_than_the_first(V, bf16, peak, k):
+    """One likely token and a flat rest, 8 to 43 nats below it (2^-62): draws that land in the
+    rest, with the smallest number there is, in its middle and at the upper end, take its tokens
+    by their shares and know their probabilities."""
+    t = torch.bfloat16 if bf16 else torch.float32
+    n = min(k or V, V) - 1                                  # tokens of the rest that are kept
+    for below in (8.0, 17.0, 22.0, 26.5, 30.0, 36.0, 43.0):
+        z = torch.full((1, V), -below)
+        z[0, 0 if peak == "first" else V - 1] = 0.0
+        z = z.to(t)
+        w = np.exp(float(z.min()))
+        total = 1 + n * w
+        if peak == "last":                                  # within a token, away from its ends
+            u = [0.0, 2.0 ** -149, 2.0 ** -126, 0.5 * w / total, (n // 3 + 0.5) * w / total,
+                 (n - 0.5) * w / total, 0.5]
+        else:
+            u = [0.0, 0.5 / total]
+            if w > 2.0 ** -32:                              # (the oracle's sum in 64 bits is off by n 2^-53)
+                u += [float(np.nextafter(np.float32(1), np.float32(0)))]
+            if n * w / total > 2.0 ** -10:
+                u += [(1 + (n // 3 + 0.5) * w) / total]
+        kk = {} if k == 0 else dict(k=[min(k, V)] * len(u))
+        _check(z.expand(len(u), V).contiguous(), T=np.ones(len(u)), u=torch.tensor(u, dtype=torch.float32), **kk)
