@@ -166,7 +166,9 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, uint64_t* s) {
 }
 
 // The weight of `count` tokens of a bin, `sum` being that of their 2^32 E + 2^26, in units
-// of 2^-42; `table` is that of 2^(63 - j / 32).
+// of 2^-42; `table` is that of 2^(63 - j / 32).  (Rounded once for a bin of a slice, so that the
+// scans over the bins stay in 64 bits: half a unit each, of either sign.  A sum of fp64 weights,
+// one token after another, rounds 2^-53 a token, which over a row of 2^17 is no less.)
 __device__ __forceinline__ uint64_t weight_of(uint32_t bin, int64_t count, int64_t sum,
                                               const uint64_t* table) {
   const uint64_t n = (uint64_t)((count << 32) + (sum - count * kBias));  // below 2^53
@@ -452,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         turn ^= 1;
         n = (int64_t)warp_sum64(on);
         s = (int64_t)warp_sum64(os);
-        return need >= 0 ? n >= need : n > 0 && f.mass + weight_of(f.bin, n, s, s_tab) >= target;
+        // (The whole bin always does: see the rounding in find_bin.)
+        return need >= 0 ? n >= need
+                         : n == f.in_bin || (n > 0 && f.mass + weight_of(f.bin, n, s, s_tab) >= target);
       };
       // The logit first, then the index.
       uint64_t lo = 0, hi = (uint64_t)order_of(m) + 1;  // `lo` reaches, `hi` does not

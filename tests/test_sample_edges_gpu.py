@@ -100,3 +100,40 @@ def test_tokens_far_less_likely_than_the_first(V, bf16, peak, k):
                 u += [(1 + (n // 3 + 0.5) * w) / total]
         kk = {} if k == 0 else dict(k=[min(k, V)] * len(u))
         _check(z.expand(len(u), V).contiguous(), T=np.ones(len(u)), u=torch.tensor(u, dtype=torch.float32), **kk)
+
+
+def test_a_crowded_bin_that_just_reaches():
+    """The sum that top-p asks for ends within the rounding of a bin's weight over the row's
+    slices (2^-42 of the first token's), and the bin holds too many tokens to be sorted: the
+    bin's tokens are kept, and of those below one at most."""
+    V, size, first, more = 70000, 4376, 14, 15              # elements of a slice; octaves
+    T = np.float32(np.log2(np.e))                           # a logit of -k is 2^-k to within 2^-25 k
+    e = [round(k * (np.log2(np.e) / float(T) - 1) * np.log(2) * 2.0 ** 32) for k in range(43)]
+    token = lambda k: 2 ** 32 - e[k]                        # in 2^-32 of its octave  # noqa: E731
+    weight = lambda k, n: (2 * n * token(k) * 2 ** 10 + 2 ** k) // 2 ** (k + 1)  # noqa: E731
+    n_slices, many = 16, 130                                # 2 mod 4: half a unit up in each
+    z = np.full(V, -np.inf, np.float32)
+    free = [list(range(r * size, min(V, (r + 1) * size))) for r in range(n_slices)]
+    z[free[0].pop()] = 0.0
+    for r in range(n_slices):
+        for _ in range(many):
+            z[free[r].pop()] = -first
+    below = 2 ** 42 + weight(first, n_slices * many)        # with one rounding
+    above = 2 ** 42 + n_slices * weight(first, many)        # with one in each slice
+    assert above - below >= 6 and n_slices * many > 2048
+    rest = below                                            # half of all lies between the two
+    each = rest * 2 ** more // (token(more) * 2 ** 10) // n_slices
+    for k in range(more, 43):
+        n = n_slices * each if k == more else max(0, rest) // weight(k, 1)
+        for r in range(n_slices):
+            here = n // n_slices + (r < n % n_slices)
+            for _ in range(here):
+                z[free[r].pop()] = -k
+            rest -= weight(k, here)
+    assert abs(rest) <= 2
+    zd = torch.from_numpy(z)[None].cuda()
+    T = torch.tensor([T], device="cuda")
+    _, _, probs = ops.stt_sample(zd, temperature=T, top_p=torch.tensor([0.5], device="cuda"))
+    kept = (probs[0] > 0).cpu().numpy()
+    assert (kept == (z >= -first))[z > -more].all()
+    assert kept[z <= -more].sum() <= 1
