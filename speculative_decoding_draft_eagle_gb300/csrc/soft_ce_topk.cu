@@ -22,6 +22,7 @@
 // by atomics 2220 us for the first, without them 1446; slices of three CTAs on an SM 1374.
 // A persistent form took 2778 and was left out.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/stt.h"
@@ -41,9 +42,9 @@ constexpr int kSliceBytes = 62 * 1024;
 
 struct Params {
   SoftCeTopkArgs a;
-  float inv_tau, c;   // 1 / tau, log2(e) / tau
-  int C, per, chunk;  // CTAs of a row, pieces of a CTA, pieces of a copy
-  bool withhold;      // test hook: the first CTA of a row sends no part
+  float inv_tau, inv_lo, c;  // 1 / tau, what its rounding left, log2(e) / tau
+  int C, per, chunk;         // CTAs of a row, pieces of a CTA, pieces of a copy
+  bool withhold;             // test hook: the first CTA of a row sends no part
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
     constexpr int kAhead = 4;  // groups of 32 entries whose loads are in flight
     const int32_t* const idx = A.indices + row * A.K;
     const float* const val = A.values + row * A.K;
-    // f(group's tokens or -1, their t / tau or -inf), kAhead groups at a time
+    // f(group's tokens or -1, their t or -inf), kAhead groups at a time
     auto each = [&](auto&& f) {
       for (int k0 = 0; k0 < A.K; k0 += 32 * kAhead) {
         int v[kAhead];
@@ -148,14 +149,36 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
           // any, its exponent would be -inf + inf.)
           const bool there = v[u] >= 0 && v[u] < A.V && t[u] != -INFINITY;
           v[u] = there ? v[u] : -1;
-          t[u] = there ? t[u] * P.inv_tau : -INFINITY;
+          t[u] = there ? t[u] : -INFINITY;
         }
         f(v, t);
       }
     };
-    float L;
+    float s = 0.f;
+    int n = 0;
+    auto list = [&](auto&& share) {
+      each([&](const int (&v)[kAhead], const float (&t)[kAhead]) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const float p = v[u] < 0 ? 0.f : share(t[u]);
+          s += p;
+          const int at = v[u] - S.first;
+          const bool here = v[u] >= 0 && at >= 0 && at < S.pieces * G;
+          const uint32_t mask = __ballot_sync(0xffffffffu, here);
+          if (here) {
+            const int i = n + __popc(mask & ((1u << lane) - 1u));
+            ent_v[i] = at;
+            ent_p[i] = p;
+          }
+          n += __popc(mask);
+        }
+      });
+    };
+    // p = e^(t / tau - L) in one rounding at the difference's size, or e^((t - max t) / tau) over
+    // their sum: t / tau by itself would cost its own size's bits, and may not be finite.
     if (A.lse) {
-      L = __ldg(A.lse + row);
+      const float L = __ldg(A.lse + row);
+      list([&](float t) { return ex2(fmaf(t, P.inv_lo, fmaf(t, P.inv_tau, -L)) * kLog2e); });
     } else {
       float top = -INFINITY, e = 0.f;
       each([&](const int (&)[kAhead], const float (&t)[kAhead]) {
@@ -163,32 +186,15 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
         for (int u = 0; u < kAhead; ++u) top = fmaxf(top, t[u]);
       });
       top = warp_max(top);
-      if (top == -INFINITY) top = 0.f;
+      const float first = top == -INFINITY ? 0.f : top;
       each([&](const int (&)[kAhead], const float (&t)[kAhead]) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) e += ex2((t[u] - top) * kLog2e);
+        for (int u = 0; u < kAhead; ++u) e += ex2((t[u] - first) * P.c);
       });
       e = warp_sum(e);
-      L = e == 0.f ? 0.f : top + logf(e);
+      const float inv_sum = e == 0.f ? 0.f : 1.f / e;
+      list([&](float t) { return ex2((t - first) * P.c) * inv_sum; });
     }
-    float s = 0.f;
-    int n = 0;
-    each([&](const int (&v)[kAhead], const float (&t)[kAhead]) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float p = v[u] < 0 ? 0.f : ex2((t[u] - L) * kLog2e);
-        s += p;
-        const int at = v[u] - S.first;
-        const bool here = v[u] >= 0 && at >= 0 && at < S.pieces * G;
-        const uint32_t mask = __ballot_sync(0xffffffffu, here);
-        if (here) {
-          const int i = n + __popc(mask & ((1u << lane) - 1u));
-          ent_v[i] = at;
-          ent_p[i] = p;
-        }
-        n += __popc(mask);
-      }
-    });
     s = warp_sum(s);
     __syncwarp();
     // A token twice: up to 32 entries by comparison, more with the bit map.
@@ -378,6 +384,7 @@ cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s) {
   Params P{};
   P.a = a;
   P.inv_tau = 1.f / a.temperature;
+  P.inv_lo = (float)(1.0 / (double)a.temperature - (double)P.inv_tau);
   P.c = (float)(1.4426950408889634 / (double)a.temperature);
   int C = (int)((a.V * (int64_t)size + kSliceBytes - 1) / kSliceBytes);
   C = std::max(1, std::min(C, kRowMaxCtas));
