@@ -7,10 +7,13 @@
 //   l = s log sum_v exp(z_v / tau) - sum_k p_k z_{i_k} / tau
 //   dz_v = g / tau (s pi_v - sum over k with i_k = v of p_k)
 //
+// The loss is taken as s log sum_v exp((z_v - m) / tau) + sum_k p_k (m - z_{i_k}) / tau, m = max z:
+// two sums without a minus, the same for logits that are all larger by a constant.
+//
 // Bound by HBM: a logit is read once and its gradient written once.  A cluster of C
 // CTAs takes a row, each its slice in shared memory (bulk copies); the maximum and sum
-// of every slice, and its part of sum p z, go to the others by st.async, which signals an
-// mbarrier there (a cluster barrier would wait for stores to drain), and the gradient is
+// of every slice, and its parts of sum p z and sum p, go to the others by st.async, which signals
+// an mbarrier there (a cluster barrier would wait for stores to drain), and the gradient is
 // written out of shared memory.  One warp looks through the teacher's entries meanwhile
 // and lists the slice's own; their elements are written again after the dense pass.
 // Entries of the same token are found by comparison, or among more than 32 with a bit map
@@ -75,7 +78,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(128) unsigned char smem[];  // the slice, its bit map, its entries
   __shared__ uint64_t bars[kMaxChunks], bar_part;
-  __shared__ float red[3][kWarps];
+  __shared__ __align__(16) float red[4][kWarps];
   __shared__ __align__(16) float4 s_part[kRowMaxCtas];
   __shared__ int s_entries, s_twice;
   __shared__ float s_sum;
@@ -269,39 +272,65 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
       red[1][warp] = l;
     }
     __syncthreads();  // and the entries are listed
-    // What the entries here contribute to sum p z; p = 0 counts for nothing whatever z is.
-    float d = 0.f;
+    // What the entries here contribute to sum p (z - max z) / tau, with the slice's maximum for the
+    // row's: differences, so that an offset of all logits costs the loss no bits.  p = 0 counts for
+    // nothing whatever z is.
+    float d = 0.f, ps = 0.f;
     const int n = s_entries;
-    for (int i = tid; i < n; i += kThreads)
-      if (ent_p[i] != 0.f) d = fmaf(ent_p[i], (float)zs[ent_v[i]] * P.inv_tau, d);
-    if (warp * 32 < n) d = warp_sum(d);
-    if (lane == 0) red[2][warp] = d;
+    if (warp * 32 < n) {
+      static_assert(kWarps == 8, "two loads");
+      const float4 a = *reinterpret_cast<const float4*>(&red[0][0]), b = *reinterpret_cast<const float4*>(&red[0][4]);
+      float at = fmaxf(fmax3(fmax3(a.x, a.y, a.z), a.w, b.x), fmax3(b.y, b.z, b.w));
+      at = at == -INFINITY ? 0.f : at;
+      for (int i = tid; i < n; i += kThreads) {
+        const float p = ent_p[i];
+        if (p != 0.f) {
+          d = fmaf(p, ((float)zs[ent_v[i]] - at) * P.inv_tau, d);
+          ps += p;
+        }
+      }
+      d = warp_sum(d);
+      ps = warp_sum(ps);
+    }
+    if (lane == 0) {
+      red[2][warp] = d;
+      red[3][warp] = ps;
+    }
     __syncthreads();
   }
-  float d;
+  float d, ps;
   {
-    auto rows = [&](float a, float b, float c) {  // lanes' parts to the sum of all
+    // The slice's, from its warps'.
+    auto slice = [&] {
+      const bool has = lane < kWarps;
+      const float a = has ? red[0][lane] : -INFINITY, b = has ? red[1][lane] : 0.f;
       m = warp_max(a);
       const float base = m == -INFINITY ? 0.f : m;
       l = warp_sum(b == 0.f ? 0.f : b * ex2((a - base) * P.c));
-      d = warp_sum(c);
+      d = warp_sum(has ? red[2][lane] : 0.f);
+      ps = warp_sum(has ? red[3][lane] : 0.f);
     };
-    const bool has = lane < kWarps;
     if (P.C == 1) {
-      rows(has ? red[0][lane] : -INFINITY, has ? red[1][lane] : 0.f, has ? red[2][lane] : 0.f);
+      slice();
     } else {
       cluster_wait_acquire();
       if (warp == 0) {
-        rows(has ? red[0][lane] : -INFINITY, has ? red[1][lane] : 0.f, has ? red[2][lane] : 0.f);
+        slice();
         if (lane < P.C && !(P.withhold && rank == 0))
-          st_async_f4(mapa_shared(smem_u32(&s_part[rank]), (uint32_t)lane), make_float4(m, l, d, 0.f),
+          st_async_f4(mapa_shared(smem_u32(&s_part[rank]), (uint32_t)lane), make_float4(m, l, d, ps),
                       mapa_shared(smem_u32(&bar_part), (uint32_t)lane));
         __syncwarp();
       }
       cluster_arrive_relaxed();  // this CTA has sent its part; waited for at the end
       mbar_wait_cluster(&bar_part, 0, STT_DEVERR_CE_WAIT);
       const float4 o = lane < P.C ? s_part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      rows(o.x, o.y, o.z);
+      m = warp_max(o.x);
+      const float base = m == -INFINITY ? 0.f : m;
+      l = warp_sum(o.y == 0.f ? 0.f : o.y * ex2((o.x - base) * P.c));
+      if (rank == 0 && warp == 0) {  // (A slice of -inf alone took its differences to 0.)
+        const float shift = ((o.x == -INFINITY ? 0.f : o.x) - base) * P.inv_tau;
+        d = warp_sum(o.w == 0.f ? o.z : fmaf(o.w, shift, o.z));
+      }
     }
   }
 
@@ -363,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
       if (mine) out[S.first + at] = (T)fmaf(ex2(((float)zs[at] - m) * P.c), a, -t * scale);
     }
     if (rank == 0 && tid == 0) {
-      const float loss = fmaf(s, m * P.inv_tau + logf(l), -d);
+      const float loss = fmaf(s, logf(l), -d);  // both at least 0
       if (A.row_loss) A.row_loss[row] = loss;
       A.wl[row] = g * loss;
     }

@@ -104,3 +104,69 @@ def test_a_log_sum_exp_beyond_the_floats():
     _, _, dz = ops.soft_ce_topk_fwd_bwd(logits(N, V).to(DEV), t(val), t(idx), t(np.full(N, tau, np.float32)),
                                         t(lse), tau)
     assert not dz.any()
+
+
+def _loss_bound(z, val, idx, tau, whole=None):
+    """Both of its terms are positive: s log sum e^((z - max) / tau), whose logarithm is off by
+    the sum's relative error and 2 steps, and sum p (max - z) / tau, of one difference and three
+    roundings a term and two for each that is added up."""
+    p, _, rel_p, _, rel_l = _bounds(z, val, idx, np.ones(len(z)), tau, whole)
+    gap = (z.max(1, keepdims=True) - np.take_along_axis(z, idx.astype(np.int64), 1)) / tau
+    log_l = ot.logsumexp((z - z.max(1, keepdims=True)) / tau)
+    s, n = p.sum(1), idx.shape[1] / 256 + 12
+    part = (p * gap * (rel_p + (5 + 2 * n) * FP32)).sum(1)
+    return part + s * rel_l + (s * (n + 6) * FP32 + (p * rel_p).sum(1)) * log_l
+
+
+@pytest.mark.parametrize("offset", [0.0, 1e4, -3e5])
+@pytest.mark.parametrize("tau", [1.0, 0.25, 3.0])
+@pytest.mark.parametrize("V", [600, 151936])
+def test_an_offset_of_all_logits_costs_the_loss_no_bits(offset, tau, V):
+    N, K = 5, 20
+    val, idx = _teacher(N, V, K)
+    z = logits(N, V) + offset                       # in fp32: the logits as they are then
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    g = np.ones(N, np.float32)
+    lse = (ot.logsumexp(val.astype(np.float64) / tau) + 0.2).astype(np.float32)
+    for whole in (None, lse):
+        _, row_loss, _ = ops.soft_ce_topk_fwd_bwd(z.to(DEV), t(val), t(idx), t(g),
+                                                  None if whole is None else t(whole), tau)
+        z0 = f64(z) - f64(z).max(1, keepdims=True)
+        _, want, _ = ot.soft_ce(z0, val.astype(np.float64), idx, g.astype(np.float64),
+                                None if whole is None else whole.astype(np.float64), tau)
+        within(row_loss, want, _loss_bound(z0, val, idx, tau, whole), "row_loss")
+
+
+@pytest.mark.parametrize("tau", [2.0 ** -126, 1e-37, 0.01])
+@pytest.mark.parametrize("V", [40, 151936])
+def test_the_loss_at_small_temperatures(tau, V):
+    """z / tau is no float, or one with a size that hides the loss, which is that of the
+    differences: 0 where the student's first token is the teacher's."""
+    N, K = 4, 6
+    tau = float(np.float32(tau))
+    val, idx = _teacher(N, V, K)
+    val = (50 + np.sort(val)[:, ::-1]).astype(np.float32)
+    z = logits(N, V) + 50
+    z[torch.arange(N), idx[:, 0].astype(np.int64)] = 90.0
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    _, row_loss, _ = ops.soft_ce_topk_fwd_bwd(z.to(DEV), t(val), t(idx), t(np.full(N, tau, np.float32)), None, tau)
+    z0, v0 = (x - x.max(1, keepdims=True) for x in (f64(z), val.astype(np.float64)))
+    _, want, _ = ot.soft_ce(z0, v0, idx, np.ones(N), None, tau)
+    within(row_loss, want, _loss_bound(z0, v0, idx, tau) + 1e-37, "row_loss")
+
+
+def test_a_masked_token_of_the_teacher_in_a_slice_of_masked_ones():
+    """The teacher's token is forbidden, and with it all logits of its CTA's slice, or all but
+    one: the loss is +inf where it has a share, and that of the others otherwise."""
+    N, V, K = 3, 151936, 3
+    z = logits(N, V)
+    val, idx = _teacher(N, V, K)
+    idx[:] = [10, 75000, 151000]
+    z[:, 60000:90000] = -np.inf
+    z[1, 75000] = -5.0
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    g = torch.ones(N, device=DEV)
+    _, row_loss, dz = ops.soft_ce_topk_fwd_bwd(z.to(DEV), t(val), t(idx), g)
+    assert f64(row_loss)[0] == np.inf and np.isfinite(f64(row_loss)[1]) and torch.isfinite(dz).all()
+    val[0, 1] = val[2, 1] = -np.inf
+    _check(z, val, idx, np.ones(N, np.float32))
