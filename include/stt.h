@@ -120,6 +120,8 @@ STT_API int stt_device_error(void* stream, uint32_t* word);
  *   STT_INJECT_CE_TOPK_WITHHOLD_PARTS  the first CTA of a row that several share
  *                              does not send the others its part of the soft-CE against
  *                              top logits.
+ *   STT_INJECT_SLICE_WITHHOLD_COPIES  the first CTA of a row does not fetch its logits, in the
+ *                              soft-CE against top logits and in sampling.
  * 0 switches injection off.  Unknown bits return STT_ERR_INVALID_ARG.  The
  * setting is process-wide; it is meant for tests, never for production runs.
  */
@@ -129,6 +131,7 @@ STT_API int stt_debug_inject(uint32_t what);
 #define STT_INJECT_LOGITS_WITHHOLD_PAIRS 0x2u
 #define STT_INJECT_PAGED_WITHHOLD_Q 0x4u
 #define STT_INJECT_CE_TOPK_WITHHOLD_PARTS 0x8u
+#define STT_INJECT_SLICE_WITHHOLD_COPIES 0x10u
 
 /* --------------------------------------------------------------------------
  * Sparse-tree attention, forward.

@@ -76,9 +76,11 @@ struct RowSlice {
 
 // Brings a slice into shared memory at `dst`: whole pieces by bulk copies, `chunk`
 // pieces on each of `bars` (initialised here), the others by the threads, before the
-// __syncthreads() in here.  Called by all threads, at least 64 of them.
+// __syncthreads() in here.  Called by all threads, at least 64 of them.  `withhold`, a test hook:
+// no copy is issued, and no wait for one can end.
 template <class T>
-__device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64_t* bars, int chunk) {
+__device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64_t* bars, int chunk,
+                                            bool withhold) {
   constexpr int G = RowSlice<T>::G;
   const int tid = threadIdx.x;
   const int n_chunks = (s.pieces + chunk - 1) / chunk;
@@ -87,7 +89,7 @@ __device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64
     fence_mbar_init();
     const int a = s.pieces > 0 && !s.whole(0) ? 1 : 0;
     const int b = s.pieces > 0 && !s.whole(s.pieces - 1) ? s.pieces - 1 : s.pieces;
-    for (int c = 0; c < n_chunks; ++c) {
+    for (int c = 0; c < n_chunks && !withhold; ++c) {
       const int lo = max(a, c * chunk), hi = min(b, (c + 1) * chunk);
       const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
       mbar_arrive_expect_tx(&bars[c], bytes);
@@ -103,12 +105,17 @@ __device__ __forceinline__ void fetch_slice(const RowSlice<T>& s, T* dst, uint64
   }
   __syncthreads();
 }
-// Waits for a slice's c-th copies; where that gives up, once more for all of them, so that a
-// CTA does not leave while they are on their way.  (Here and not at its end, where it took 2 %
-// of a gradient's time.)
-__device__ __forceinline__ void wait_slice(uint64_t* bars, int c, int n_chunks, uint32_t site) {
-  if (!mbar_wait(&bars[c], 0, site))
-    for (int i = 0; i < n_chunks; ++i) mbar_wait(&bars[i], 0, site);
+// Waits for a slice's c-th copies.  False: that gave up, and the caller waits for no more of them;
+// they have been waited for once more, within one budget for all together, so that a CTA does not
+// leave while they are on their way.  (Here and not at its end, where it took 2 % of a gradient's
+// time.)
+__device__ __forceinline__ bool wait_slice(uint64_t* bars, int c, int n_chunks, uint32_t site) {
+  if (mbar_wait(&bars[c], 0, site)) return true;
+  const uint64_t t0 = globaltimer_ns(), budget = *(volatile uint64_t*)&g_wait_budget_ns;
+  for (int i = 0; i < n_chunks; ++i)
+    while (!mbar_try_wait_suspend(&bars[i], 0, 20000u))
+      if (globaltimer_ns() - t0 > budget) return false;
+  return false;
 }
 
 // ------------------------------------------------------------------ order --

@@ -57,6 +57,7 @@ constexpr float kMagic = 393216.f;         // 1.5 2^18: floats there are 1/32 ap
 struct Params {
   SampleArgs a;
   int C, per, chunk;
+  bool no_copies;      // test hook: the first CTA of a row fetches nothing
   int runs, groups;    // runs of 32 pieces that a warp takes, and groups of those
   uint64_t table[32];  // 2^(63 - j / 32)
 };
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (want_k || want_p)
     for (int i = tid; i < 2 * (int)kBins; i += kThreads) bin_lo[i] = 0;
   if (tid == 0) s_index = INT_MAX;
-  fetch_slice(S, zs, bars, P.chunk);
+  fetch_slice(S, zs, bars, P.chunk, P.no_copies && rank == 0);
 
   auto each_piece = [&](auto&& f) {
     for (int q = tid; q < S.pieces; q += kThreads) {
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   {
     for (int c = 0; c < n_chunks; ++c) {
-      wait_slice(bars, c, n_chunks, STT_DEVERR_SAMPLE_WAIT);
+      if (!wait_slice(bars, c, n_chunks, STT_DEVERR_SAMPLE_WAIT)) break;
       const int end = min(S.pieces, (c + 1) * P.chunk);
       for (int q = c * P.chunk + tid; q < end; q += kThreads) {
         float x[G];
@@ -758,6 +759,7 @@ cudaError_t sample_launch(const SampleArgs& a, cudaStream_t s) {
   P.runs = ((P.per + 31) / 32 + kWarps - 1) / kWarps;
   P.groups = (P.runs + kGroup - 1) / kGroup;
   const int smem = P.per * 16 + kBins * 8 + kList * 8 + kWarps * P.groups * (int)sizeof(Whole);
+  P.no_copies = (debug_inject() & STT_INJECT_SLICE_WITHHOLD_COPIES) != 0;
   prof_before(s, STT_KERNEL_SAMPLE);
   static Raised raised[2];
   const cudaError_t e =

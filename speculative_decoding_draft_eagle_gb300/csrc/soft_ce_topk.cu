@@ -47,7 +47,7 @@ struct Params {
   SoftCeTopkArgs a;
   float inv_tau, inv_lo, c;  // 1 / tau, what its rounding left, log2(e) / tau
   int C, per, chunk;         // CTAs of a row, pieces of a CTA, pieces of a copy
-  bool withhold;             // test hook: the first CTA of a row sends no part
+  bool withhold, no_copies;  // test hooks: the first CTA of a row sends no part, fetches nothing
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
     fence_mbar_init();
     if (P.C > 1) mbar_arrive_expect_tx(&bar_part, (uint32_t)P.C * 16u);
   }
-  fetch_slice(S, zs, bars, P.chunk);
+  fetch_slice(S, zs, bars, P.chunk, P.no_copies && rank == 0);
   if (P.C > 1) cluster_arrive_relaxed();  // everyone runs before anyone writes to a neighbour
 
   // ---- the teacher's entries, by the last warp: p of all, and the list of the slice's own in
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) soft_ce_topk_kernel(const __grid_con
   float m = -INFINITY, l = 0.f;
   const int n_chunks = (S.pieces + P.chunk - 1) / P.chunk;
   for (int c = 0; c < n_chunks; ++c) {
-    wait_slice(bars, c, n_chunks, STT_DEVERR_CE_WAIT);
+    if (!wait_slice(bars, c, n_chunks, STT_DEVERR_CE_WAIT)) break;
     const int end = min(S.pieces, (c + 1) * P.chunk);
     for (int q = c * P.chunk + tid; q < end; q += U * kThreads) {
       float x[U][G];
@@ -424,6 +424,7 @@ cudaError_t soft_ce_topk_launch(const SoftCeTopkArgs& a, cudaStream_t s) {
   const int round = 1024;  // four pieces of fp32 to a thread, or eight of bf16
   P.chunk = ((P.per + kMaxChunks - 1) / kMaxChunks + round - 1) / round * round;
   const int smem = P.per * 16 + (P.per * (16 / size) + 31) / 32 * 4 + a.K * 8;
+  P.no_copies = (debug_inject() & STT_INJECT_SLICE_WITHHOLD_COPIES) != 0;
   P.withhold = (debug_inject() & STT_INJECT_CE_TOPK_WITHHOLD_PARTS) != 0;
   prof_before(s, STT_KERNEL_SOFT_CE_TOPK);
   static Raised raised[2];
