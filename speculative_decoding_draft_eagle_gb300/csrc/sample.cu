@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     total = from_lane(run, 31);
     before = from_lane(run - o, rank) + slice_before;
   }
+  __syncwarp();
   cluster_arrive_release();  // done with the neighbours' shared memory; waited for at the end
   const float total_f = (float)(uint64_t)(total >> 50);  // in 2^-44
 

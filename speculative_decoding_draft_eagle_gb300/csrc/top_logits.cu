@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
   const RowSlice<T> S(static_cast<const T*>(A.z) + row * A.ld_z, A.V, rank, P.per);
   const int K = A.K, cap = P.cap;
   if (tid == 0) s_n = s_pieces = 0;
+  __syncwarp();
   if (P.C > 1) cluster_arrive_relaxed();  // everyone runs before anyone writes to the first CTA
 
   // ---- a bound from the sample; -inf where the slice is kept whole
@@ -460,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       s_m = m;
       s_l = l;
     }
+    __syncwarp();
     cluster_wait_acquire();
     for (int i = tid; i < K; i += kThreads) st_cluster(all_keys + rank * K + i, 0, i < n ? keys[i] : 0ull);
     if (rank == 0)
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       l = warp_sum(ol == 0.f ? 0.f : ol * (om == m ? 1.f : ex2(om - m)));
     }
     __syncwarp();
-    cluster_arrive_relaxed();
+    cluster_arrive_release();  // the sums have been read
     if (rank == 0) {
       // Of every slice's first K / C the last, the least of which has K keys at or above it:
       // what is below is not among the row's (8 bf16 rows of 151936, K 128, 16 CTAs: 61 us
