@@ -448,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 4) top_logits_kernel(const __grid_co
       l += red[kWarps + w] == 0.f ? 0.f : red[kWarps + w] * (red[w] == m ? 1.f : ex2(red[w] - m));
   }
   auto give = [&](int place, uint64_t key) {
-    A.values[row * K + place] = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
+    float z = key ? logit_of((uint32_t)(key >> 32)) : -INFINITY;
+    if (z == 0.f) z = (float)S.row[key_index(key)];  // the order knows no sign of it
+    A.values[row * K + place] = z;
     A.indices[row * K + place] = key ? key_index(key) : -1;
   };
   if (P.C == 1) {
