@@ -48,7 +48,11 @@ constexpr int kMaxChunks = 8;
 constexpr int kOctaves = 64;
 constexpr uint32_t kBins = 32 * kOctaves;
 constexpr int kList = 2048;                // tokens of a bin that are sorted
-constexpr int kSliceBytes = 80 * 1024;     // preferred bytes of a slice: two CTAs on an SM
+// Preferred bytes of a slice: with the bins, the list, the groups' sums, 4 KB of static and reserved
+// shared memory, and a piece more where the row starts off a piece, two CTAs fit on an SM's 228 KB.
+// (Of 80 KB, where one fits: 320 fp32 rows of 100000 by top-p 307 us, of 77 KB 220; 320 bf16 rows of
+// 40960 106 and 88.)
+constexpr int kSliceBytes = 77 * 1024;
 constexpr int kSegment = 8 * (int)kBins / 2 / kWarps;  // kept tokens that a warp lists, in the bins' memory
 constexpr int64_t kBias = 1ll << 26;       // keeps 2^32 E positive
 constexpr int kGroup = 4;                  // runs of 32 pieces whose kept weight a warp notes as one
@@ -177,6 +181,10 @@ __device__ __forceinline__ uint64_t weight_of(uint32_t bin, int64_t count, int64
   const uint32_t o = bin >> 5;
   return o == 0 ? w : ((w >> (o - 1)) + 1) >> 1;
 }
+
+static_assert(2 * (kSliceBytes + 16 + 8 * (int)kBins + 8 * kList +
+                   kWarps * (kSliceBytes / 16 / 32 / kWarps / kGroup + 1) * (int)sizeof(Whole) + 4096) <= 228 * 1024,
+              "two CTAs on an SM");
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params P) {
