@@ -130,10 +130,11 @@ __device__ __forceinline__ Whole warp_sum(Whole v) {
          __shfl_xor_sync(0xffffffffu, (uint64_t)v, o);
   return v;
 }
-__device__ __forceinline__ Whole warp_scan(Whole v) {  // inclusive
+template <int n = 32>
+__device__ __forceinline__ Whole warp_scan(Whole v) {  // inclusive, of the first n lanes
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < n; o <<= 1) {
     const Whole t = (Whole)__shfl_up_sync(0xffffffffu, (uint64_t)(v >> 64), o) << 64 |
                     __shfl_up_sync(0xffffffffu, (uint64_t)v, o);
     if (lane >= o) v += t;
@@ -626,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   } else {
     for (int g = 0; g < P.groups; ++g) {
       Whole w = 0;
-      for (int r = 0; r < kGroup; ++r) w += kept_of(q_begin + (g * kGroup + r) * 32 + lane);
+      const int q0 = q_begin + g * kGroup * 32;
+      for (int q = q0; q < min(q0 + kGroup * 32, q_end); q += 32) w += kept_of(q + lane);
       w = warp_sum(w);
       if (lane == 0) group_sum[g] = w;
       mine += w;
@@ -634,23 +636,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   if (lane == 0) s_part[warp] = mine;
   __syncthreads();
-  Whole slice = 0, slice_before = 0;  // the slice's, and what its warps before this one have
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) slice_before += s_part[w];
-    slice += s_part[w];
-  }
-  if (tid == 0) {
-    s_total[0] = (uint64_t)slice;
-    s_total[1] = (uint64_t)(slice >> 64);
+  Whole slice_before;  // what the slice's warps before this one have
+  {
+    const Whole part = lane < kWarps ? s_part[lane] : 0, run = warp_scan<kWarps>(part);
+    slice_before = from_lane(run - part, warp);
+    if (tid == kWarps - 1) {
+      s_total[0] = (uint64_t)run;
+      s_total[1] = (uint64_t)(run >> 64);
+    }
   }
   cluster_sync();
   Whole total, before;
   {
     Whole o = 0;
     if (lane < C) o = (Whole)ld_cluster(&s_total[1], lane) << 64 | ld_cluster(&s_total[0], lane);
-    const Whole run = warp_scan(o);
-    total = from_lane(run, 31);
+    const Whole run = warp_scan<kRowMaxCtas>(o);
+    total = from_lane(run, kRowMaxCtas - 1);
     before = from_lane(run - o, rank) + slice_before;
   }
   __syncwarp();
