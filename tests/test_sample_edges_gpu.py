@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from _serving import gen
-from _top import logits
+from _serving import DEV, gen
+from _top import in_rows, logits
 from speculative_decoding_draft_eagle_gb300 import ops
 from test_sample_gpu import _check
 
@@ -137,3 +137,30 @@ def test_a_crowded_bin_that_just_reaches():
     kept = (probs[0] > 0).cpu().numpy()
     assert (kept == (z >= -first))[z > -more].all()
     assert kept[z <= -more].sum() <= 1
+
+
+@pytest.mark.parametrize("V", [33, 12345, 151936])
+@pytest.mark.parametrize("layout", ["dense", "odd"])
+def test_a_draw_whose_probabilities_go_over_the_logits(V, layout):
+    N = 4
+    z = logits(N, V)
+    u = torch.rand(N, generator=gen(V)).to(DEV)
+    k = torch.tensor([0, 7], dtype=torch.int32, device=DEV)
+    p = torch.tensor([0.9, 1.0], device=DEV)
+    want = ops.stt_sample(in_rows(z, layout), u, 2, top_k=k, top_p=p, want_probs=True)
+    over = in_rows(z, layout)
+    got = ops.stt_sample(over, u, 2, top_k=k, top_p=p, probs=over)
+    assert got[2].data_ptr() == over.data_ptr()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_settings_that_cut_nothing_or_all_but_one():
+    """The ends of each setting's range and what lies beyond; an infinite temperature makes all
+    allowed tokens equal."""
+    V = 5000
+    z = logits(9, V, ban=0.3)
+    inf = np.inf
+    _check(z, T=[1.0, inf, inf, inf, 1.0, 1.0, 2.0, inf, 1.0],
+           k=[V, 0, V + 7, 100, -3, V - 1, 0, 0, 2 ** 31 - 1],
+           p=[1.0, 1.0, 0.5, 0.5, 1.5, 0.999, 0.0, 1.0, inf],
+           m=[0.0, 0.0, 0.0, 0.0, -1.0, 0.0, 0.0, 1.0, 1e-30])
