@@ -267,6 +267,16 @@ __device__ __forceinline__ void st_cluster(const uint64_t* p, int rank, uint64_t
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 // max(a, b, c) that passes NaN on.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;

@@ -50,17 +50,6 @@ struct Params {
   bool withhold, no_copies;  // test hooks: the first CTA of a row sends no part, fetches nothing
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 template <class T>
 __device__ __forceinline__ void store_piece(T* dst, const float (&y)[16 / sizeof(T)]) {
   if constexpr (sizeof(T) == 4) {
