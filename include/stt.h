@@ -616,11 +616,13 @@ STT_API int stt_top_logits(const void* z, int64_t ld_z, int64_t N, int64_t V, in
  *           outside [0, V) is none (so is one of -inf); entries of one token add up.
  *  t_lse    fp32 [N]: the teacher's log sum_v exp(t_v / tau) over its whole row, as
  *           stt_top_logits gives it: p are then the teacher's probabilities and s
- *           their sum.  NULL: over the row's entries alone, s = 1.
+ *           their sum (0 under an lse of +inf).  NULL: over the row's entries alone,
+ *           s = 1.
  *  g        fp32 [N], as soft_ce_fwd_bwd_inplace: rows with g_r = 0 are not read,
  *           their gradient and row_loss are 0.
  *  N        rows, >= 0.   V  1..STT_ROW_MAX_V.   K  1..STT_TOP_MAX_K.
- *  temperature  finite and at least 2^-126.
+ *  temperature  finite and at least 2^-126; that g_r / temperature is finite is the
+ *           caller's to see to.
  *  dz       the gradient, of z's type, rows ld_dz apart, OVERWRITTEN, rounded once.
  *           It may be z (with ld_dz = ld_z); otherwise it may not overlap z.
  *  row_loss fp32 [N] or NULL;  loss  fp32 scalar (device), summed in a fixed order.
@@ -655,9 +657,11 @@ STT_API int soft_ce_topk_fwd_bwd(const void* z, int64_t ld_z, const float* t_val
  *  N        rows, >= 0, a multiple of `rows` >= 1.   V  1..STT_ROW_MAX_V.
  *  temperature, top_p, min_p  fp32 [N / rows], top_k  int32 [N / rows]; each may be
  *           NULL (1, 1, 0, off).  temperature = 0, like top_k = 1, keeps the first
- *           token alone; top_k <= 0 or >= V, top_p >= 1 and min_p <= 0 cut nothing.
+ *           token alone; top_k <= 0 or >= V, top_p >= 1 and min_p <= 0 cut nothing,
+ *           top_p <= 0 leaves one token, and min_p > 1 counts as 1.
  *           That none is NaN and temperature >= 0 is the caller's to see to.
  *  u        fp32 [N] in [0, 1), or NULL: nothing is drawn (tokens and logprobs NULL).
+ *           Running sums and u times their whole are exact in 128 bits, of weights to 31.
  *  tokens   int32 [N].   logprobs  fp32 [N] or NULL: log probs[token].
  *  probs    fp32, rows ld_probs elements apart, or NULL (with u); may be z where that
  *           is fp32 (with ld_probs = ld_z), otherwise it may not overlap z.

@@ -22,16 +22,20 @@
 // sums are exact and weights are good to about 2^-31: a weight is 2^(-bin / 32) (1 + E),
 // z log2(e) / T being a product of two floats in full; E, below 2^-6, comes from a
 // polynomial of degree 4 and is summed as a whole number of 2^-32.  A histogram's bin
-// holds the count and the sum of E in 64 bits, split over two words of shared memory.
-// A weight more than 2048 bins, about 2^-64, below the largest is taken as 0.
+// holds the count and the sum of E in 64 bits, split over two words of shared memory; its
+// weight is a whole number of 2^-42 of the first token's.  A draw's sums take 128 bits, in
+// which the least weight keeps its 31.  A weight more than 2048 bins, about 2^-64, below the
+// largest is taken as 0.
 //
-// 320 fp32 rows of 151936 by top-p, with probabilities: 286 us, against 58 at HBM's rate; 64
-// bf16 rows of 128256 with all cuts, tokens alone: 41 (2.4); 99 bf16 rows of 50257: 40 (4.4);
-// one fp32 row of 32000: 18 to 22, most of it the call's host path.  HBM is at 11 % of its
-// rate: bound by instructions (112 of a warp for 32 logits, half of the issue slots) and by
-// the row's CTAs waiting at barriers (a quarter of the stalls).  Left out after measuring: a
-// row to one CTA that reads its logits again from L2 (266 to 290 us for the first, but 50,
-// 60 and 23 on the others); threads' own lists of the kept (295).
+// 320 fp32 rows of 151936 by top-p, with probabilities: 291 us, against 58 at HBM's rate; 64
+// bf16 rows of 128256 with all cuts, tokens alone: 41 (2.5); 99 bf16 rows of 50257: 40 (4.5);
+// one fp32 row of 32000: 16 by top-p, 8.4 with nothing cut (19 of a call through the binding).
+// HBM is at 11 % of its rate: bound by instructions (113 of a warp for 32 logits, half of the
+// issue slots) and by the row's CTAs waiting at barriers (a quarter of the stalls); few rows by
+// the chain of a row's steps.  Off the usual path: 64 bf16 rows of 128256 at T = 30 by top-p,
+// whose cut is found by halving, 612; of equal logits 744; 320 fp32 rows of 151936 at T = 30 3890.
+// Left out after measuring: a row to one CTA that reads its logits again from L2 (266 to 290 us
+// for the first, but 50, 60 and 23 on the others); threads' own lists of the kept (295).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

@@ -19,11 +19,12 @@
 // Entries of the same token are found by comparison, or among more than 32 with a bit map
 // over the slice; only then are they added up, in their order.
 //
-// 8192 fp32 rows of 151936, a fifth masked, K 128: 1374 us, 6.5 TB/s (0.97); 4096 bf16 rows of
-// 128256, K 64: 372 us, 5.6 TB/s (0.84); 999 fp32 rows of 50257: 66 us (0.79).  On the way:
-// cluster barriers that order memory, which wait for stores on their way, and entries found
-// by atomics 2220 us for the first, without them 1446; slices of three CTAs on an SM 1374.
-// A persistent form took 2778 and was left out.
+// 8192 fp32 rows of 151936, a fifth masked, K 128: 1387 us, 6.5 TB/s (0.97); 4096 bf16 rows of
+// 128256, K 64: 376 us, 5.6 TB/s (0.84); 999 fp32 rows of 50257: 66 us (0.80); 64 bf16 rows of
+// 32000, K 8, with the loss's sum: 11 us.  On the way: cluster barriers that order memory, which
+// wait for stores on their way, and entries found by atomics 2220 us for the first, without them
+// 1446; slices of three CTAs on an SM 1374; the loss from differences and waits that give up once
+// 1387.  A persistent form took 2778 and was left out.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

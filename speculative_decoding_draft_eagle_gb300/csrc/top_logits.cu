@@ -17,7 +17,9 @@
 // instructions beside HBM: 10 of a warp for 32 logits, 65 % of the issue slots.  On the way:
 // elements kept in the loop 489 us, pieces listed and looked at afterwards 336, listed with
 // their bits, narrowed and sorted in the warps' runs 260, exponentials from one product and
-// sum 238.
+// sum 238.  Logits that crowd by index make the runs of 32 pieces a poor sample, and the digits
+// cost up to nine more passes: the first case with -a log(index + 100) added takes 232 us for a =
+// 0.5, 395 for 0.75, 970 for 1, 5240 for 1.5; with equal logits 8240.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
