@@ -661,7 +661,7 @@ STT_API int soft_ce_topk_fwd_bwd(const void* z, int64_t ld_z, const float* t_val
  *           top_p <= 0 leaves one token, and min_p > 1 counts as 1.
  *           That none is NaN and temperature >= 0 is the caller's to see to.
  *  u        fp32 [N] in [0, 1), or NULL: nothing is drawn (tokens and logprobs NULL).
- *           Running sums and u times their whole are exact in 128 bits, of weights to 31.
+ *           Weights have 31 bits; their running sums, and u times the whole, are exact.
  *  tokens   int32 [N].   logprobs  fp32 [N] or NULL: log probs[token].
  *  probs    fp32, rows ld_probs elements apart, or NULL (with u); may be z where that
  *           is fp32 (with ld_probs = ld_z), otherwise it may not overlap z.

@@ -26,7 +26,6 @@
 // 1446; slices of three CTAs on an SM 1374; the loss from differences and waits that give up once
 // 1387.  A persistent form took 2778 and was left out.
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 
 #include "../../include/stt.h"
